@@ -62,6 +62,7 @@ typedef enum pa_status {
 #define PA_DEVERR_TIMEOUT 0x8u  /* an internal pipeline wait gave up (should never happen) */
 #define PA_DEVERR_PREFIX  0x10u /* pa_decode_shared_prefix: a sequence could not use its group's
                                    shared prefix (see there) and was decoded in full instead */
+#define PA_DEVERR_POSITION 0x20u /* pa_rope_and_cache: a position was >= max_positions      */
 
 /* Element type of q, the caches and the output (and of k, v for
  * reshape_and_cache): IEEE binary16, or bfloat16 (the top 16 bits of an
@@ -410,6 +411,150 @@ int pa_decode_shared_prefix(void *out, const void *q, const void *k_cache, const
 int pa_decode_static(void *out, const void *q, const void *k_cache, const void *v_cache,
                      const int32_t *block_tables, const int32_t *context_lens, float scale,
                      int32_t max_blocks_per_seq, const pa_dims *dims, void *stream);
+
+/*
+ * pa_rope_and_cache -- rotate each new token's q and k by its position and
+ * append k and v to the paged cache, in one pass.
+ *
+ * The step in front of the attention of a model with rotary positions and
+ * shared K/V heads: pa_reshape_and_cache with the rotation applied on the way
+ * (K rows are stored rotated, V rows as they are), and the rotated q written
+ * for the attention call that follows.  The rotation turns pairs of elements
+ * of each head's first rotary_dim dims by the angle the table gives for the
+ * token's position p:
+ *   y_a = x_a cos[p][i] - x_b sin[p][i],   y_b = x_b cos[p][i] + x_a sin[p][i]
+ * with i in [0, rotary_dim / 2) and (a, b) = (i, i + rotary_dim / 2), or, with
+ * interleaved != 0, (2 i, 2 i + 1).  Dims from rotary_dim on are copied.  The
+ * arithmetic is fp32, rounded once (to nearest even) to the element type.
+ *
+ *   q_out        device, [num_tokens, num_q_heads, D], rows q_out_stride apart
+ *                (written).  It may be q itself, with the same stride;
+ *                otherwise the two must not overlap
+ *   q            device, [num_tokens, num_q_heads, D], rows q_stride apart
+ *   k, v         device, [num_tokens, H, D], rows k_stride / v_stride apart
+ *   q_stride, k_stride, v_stride, q_out_stride
+ *                elements between one token's row and the next: multiples of 8,
+ *                >= 0, and >= num_q_heads * D for q_out.  The heads of a row
+ *                are adjacent, so q, k and v may be slices of one projection's
+ *                output [num_tokens, (num_q_heads + 2 H) * D]
+ *   k_cache, v_cache, slot_mapping: as pa_reshape_and_cache (slot < 0: the
+ *                token's q is rotated, its k and v are not stored)
+ *   positions    device, int32 [num_tokens]: p of each token.  A negative
+ *                position marks a padding row: nothing is written for it.  A
+ *                position >= max_positions flags PA_DEVERR_POSITION and
+ *                nothing is written for the token
+ *   cos_sin      device, fp32 [max_positions, rotary_dim]: row p holds
+ *                cos(angle_i) for i < rotary_dim / 2, then sin(angle_i)
+ *   rotary_dim   a multiple of 16 in [16, D]
+ *   dims         host; num_heads (H) is the K/V heads; num_seqs is not used
+ *
+ * num_q_heads may be any number >= 1.  Two tokens with one slot race.
+ */
+int pa_rope_and_cache(void *q_out, const void *q, const void *k, const void *v, void *k_cache,
+                      void *v_cache, const int32_t *positions, const float *cos_sin,
+                      const int32_t *slot_mapping, int32_t num_tokens, int32_t num_q_heads,
+                      int64_t q_stride, int64_t k_stride, int64_t v_stride, int64_t q_out_stride,
+                      int32_t rotary_dim, int32_t max_positions, int32_t interleaved,
+                      const pa_dims *dims, void *stream);
+
+/*
+ * What the scores of the grouped attention calls go through.  A NULL
+ * pa_attn_opts, or one of all zeros, is plain causal attention.
+ *
+ * For a query at position p of a sequence of ctx tokens, head h, and key j:
+ *   s_j = scale * q . k_j
+ *   s_j = softcap * tanh(s_j / softcap)              if softcap > 0
+ *   s_j = s_j - alibi_slopes[h] * |p - j|            if alibi_slopes
+ *   key j is visible iff j < ctx and (j < prefix_lens[s], or
+ *                    j <= p and (window == 0 or j > p - window))
+ * and the output is the softmax over the visible keys' scores times their
+ * values.  So window limits a query to the last `window` keys up to its own,
+ * and the first prefix_lens[s] keys of sequence s stay visible to all its
+ * queries: to later ones past the window, and to earlier ones before them in
+ * the sequence (a prompt's part that is read in both directions).
+ */
+typedef struct pa_attn_opts {
+    float softcap;               /* 0: none; otherwise finite and > 0                     */
+    int32_t window;              /* 0: none; otherwise >= 1                               */
+    const float *alibi_slopes;   /* device, fp32 [num_q_heads], or NULL                   */
+    const int32_t *prefix_lens;  /* device, int32 [S], or NULL; clamped to [0, ctx]       */
+} pa_attn_opts;
+
+/*
+ * pa_decode_grouped -- pa_decode for query heads that share K/V heads, with
+ * the score options of pa_attn_opts.
+ *
+ *   out, q        device, [S, num_q_heads, D]; query head h reads K/V head
+ *                 h / (num_q_heads / H)
+ *   k_cache, v_cache, block_tables, context_lens, scale, max_blocks_per_seq,
+ *   dims, stream: as pa_decode_ws; dims->num_heads (H) is the K/V heads, and
+ *                 num_q_heads a multiple of it
+ *   opts          host, or NULL
+ *   workspace     device, pa_decode_grouped_workspace_bytes(...) bytes,
+ *                 16-byte aligned, no initialisation
+ *   counters      device, pa_decode_grouped_counters_bytes(...) bytes, 4-byte
+ *                 aligned, all zero before the first call and left zero by
+ *                 every call that completes without a device error.  Calls
+ *                 that share a workspace or counters must not overlap
+ *
+ * The query of sequence s is its last token, at p = ctx_s - 1.  ctx_s = 0
+ * gives a zero row; a ctx_s outside [0, max_blocks_per_seq * B] flags
+ * PA_DEVERR_CONTEXT and gives a zero row.  Only table entries of blocks that
+ * hold a visible key are read, and no row of K or V that is not visible
+ * reaches the output whatever it holds, so blocks that the window has left
+ * behind may be freed and their entries hold anything.  A used entry outside
+ * [0, N) flags PA_DEVERR_TABLE and its keys are left out.
+ * PA_ERR_SHAPE if num_q_heads is not a positive multiple of H, N * H * B or
+ * S * num_q_heads exceeds INT32_MAX, window < 0, or softcap is negative or
+ * not finite.
+ *
+ * Each K and V row is read once for all query heads that share it (in chunks
+ * of 16 heads; of 8 for D = 256).  Scores, softmax and sums are fp32; the
+ * weights enter the P V product as a pair of 16-bit values (about 22 bits).
+ */
+int pa_decode_grouped(void *out, const void *q, const void *k_cache, const void *v_cache,
+                      const int32_t *block_tables, const int32_t *context_lens, float scale,
+                      int32_t max_blocks_per_seq, const pa_dims *dims, int32_t num_q_heads,
+                      const pa_attn_opts *opts, void *workspace, size_t workspace_bytes,
+                      uint32_t *counters, size_t counters_bytes, void *stream);
+
+/* Bytes of pa_decode_grouped's workspace ((size_t)-1 on invalid sizes) and
+ * counters (0 on invalid sizes). */
+size_t pa_decode_grouped_workspace_bytes(const pa_dims *dims, int32_t num_q_heads);
+size_t pa_decode_grouped_counters_bytes(const pa_dims *dims, int32_t num_q_heads);
+
+/*
+ * pa_prefill_grouped -- pa_prefill for query heads that share K/V heads, with
+ * the score options of pa_attn_opts.
+ *
+ *   out, q        device, [total_query_tokens, num_q_heads, D]
+ *   query_start, total_query_tokens, max_query_len, and the rest: as
+ *                 pa_prefill_ws; dims->num_heads (H) is the K/V heads
+ *   workspace, counters: as pa_decode_grouped, sized by
+ *                 pa_prefill_grouped_workspace_bytes (0: none is needed, and
+ *                 NULL will do) and pa_prefill_grouped_counters_bytes
+ *
+ * Query i of sequence s sits at position p = ctx_s - q_len_s + i.  Rows of
+ * out that belong to no sequence are left as they are, and so are the rows of
+ * a sequence with q_len_s > ctx_s, q_len_s > max_query_len, ctx_s outside
+ * [0, max_blocks_per_seq * B] or rows outside [0, total_query_tokens), which
+ * flags PA_DEVERR_CONTEXT.  Table entries of blocks in which no query of the
+ * call sees a key may hold anything, and so may key rows from ctx_s on; V rows
+ * of the other keys must be finite (a weight of zero times a NaN is NaN).
+ *
+ * Built for head_dim 64 and 128, block_size 8, 16 and 32, fp16 and bf16, up
+ * to 128 query heads per K/V head (PA_ERR_UNSUPPORTED otherwise).
+ */
+int pa_prefill_grouped(void *out, const void *q, const void *k_cache, const void *v_cache,
+                       const int32_t *block_tables, const int32_t *context_lens,
+                       const int32_t *query_start, int32_t total_query_tokens,
+                       int32_t max_query_len, float scale, int32_t max_blocks_per_seq,
+                       const pa_dims *dims, int32_t num_q_heads, const pa_attn_opts *opts,
+                       void *workspace, size_t workspace_bytes, uint32_t *counters,
+                       size_t counters_bytes, void *stream);
+size_t pa_prefill_grouped_workspace_bytes(const pa_dims *dims, int32_t num_q_heads,
+                                          int32_t max_query_len);
+size_t pa_prefill_grouped_counters_bytes(const pa_dims *dims, int32_t num_q_heads);
 
 /*
  * KV block manager (host only; no CUDA call).

@@ -13,6 +13,9 @@ Functions (names follow the C ABI):
   decode(out, q, k_cache, v_cache, block_tables, context_lens, scale, ...)
   decode_shared_prefix(out, q, k_cache, v_cache, block_tables, context_lens, scale,
                        group_start, group_prefix_blocks, ...)
+  rope_and_cache(q_out, q, k, v, k_cache, v_cache, positions, cos_sin, slot_mapping, ...)
+  decode_grouped(out, q, k_cache, v_cache, block_tables, context_lens, scale, ...)
+  prefill_grouped(out, q, k_cache, v_cache, block_tables, context_lens, query_start, scale, ...)
   decode_workspace_bytes(...), decode_counters_bytes(...), device_errors(), version(),
   selftest_wait_timeout()
 """
@@ -22,19 +25,24 @@ import ctypes
 import threading
 
 from . import build as _build
+from . import grouped as _grouped
 
 __all__ = ["PaError", "Dims", "KVManager", "lib", "reshape_and_cache", "copy_blocks", "decode",
            "decode_shared_prefix", "selftest_wait_timeout",
            "prefill", "decode_workspace_bytes", "decode_shared_prefix_workspace_bytes",
            "decode_shared_prefix_counters_bytes",
            "decode_counters_bytes", "device_errors", "reset_workspaces", "version", "DEVERR_TABLE", "DEVERR_CONTEXT",
-           "DEVERR_SLOT", "DEVERR_TIMEOUT", "DEVERR_PREFIX"]
+           "DEVERR_SLOT", "DEVERR_TIMEOUT", "DEVERR_PREFIX", "DEVERR_POSITION",
+           "rope_and_cache", "rope_table", "decode_grouped", "prefill_grouped",
+           "decode_grouped_workspace_bytes", "decode_grouped_counters_bytes",
+           "prefill_grouped_workspace_bytes", "prefill_grouped_counters_bytes"]
 
 DEVERR_TABLE = 0x1
 DEVERR_CONTEXT = 0x2
 DEVERR_SLOT = 0x4
 DEVERR_TIMEOUT = 0x8
 DEVERR_PREFIX = 0x10
+DEVERR_POSITION = 0x20
 
 STATUS = {0: "PA_OK", -1: "PA_ERR_NULL", -2: "PA_ERR_SHAPE", -3: "PA_ERR_UNSUPPORTED",
           -4: "PA_ERR_ALIGN", -5: "PA_ERR_WORKSPACE", -6: "PA_ERR_CUDA",
@@ -50,7 +58,10 @@ EXPORTS = ("pa_reshape_and_cache", "pa_copy_blocks", "pa_decode", "pa_prefill", 
            "pa_kvm_context_len", "pa_kvm_slot", "pa_kvm_block_tables", "pa_selftest_wait_timeout",
            "pa_decode_shared_prefix", "pa_decode_shared_prefix_ws",
            "pa_decode_shared_prefix_workspace_bytes", "pa_decode_shared_prefix_counters_bytes",
-           "pa_kvm_prefix_groups")
+           "pa_kvm_prefix_groups",
+           "pa_rope_and_cache", "pa_decode_grouped", "pa_decode_grouped_workspace_bytes",
+           "pa_decode_grouped_counters_bytes", "pa_prefill_grouped",
+           "pa_prefill_grouped_workspace_bytes", "pa_prefill_grouped_counters_bytes")
 _SIZE_ERROR = (1 << 64) - 1
 
 
@@ -130,6 +141,7 @@ def _declare(l):
                  "pa_device_errors",
                  "pa_last_cuda_error", "pa_version"):
         getattr(l, name).restype = ctypes.c_int
+    _grouped.declare(l, dp)
     return l
 
 
@@ -416,6 +428,7 @@ def reset_workspaces():
             ctr.zero_()
         for ctr in _prefill_counters.values():
             ctr.zero_()
+    _grouped.reset_counters()
 
 
 def decode(out, q, k_cache, v_cache, block_tables, context_lens, scale,
@@ -663,3 +676,9 @@ def device_errors(stream=None, device=None) -> int:
         rc = lib().pa_device_errors(sh, ctypes.byref(flags))
     _check(rc, "pa_device_errors")
     return int(flags.value)
+
+
+from .grouped import (decode_grouped, decode_grouped_counters_bytes,  # noqa: E402
+                      decode_grouped_workspace_bytes, prefill_grouped,
+                      prefill_grouped_counters_bytes, prefill_grouped_workspace_bytes,
+                      rope_and_cache, rope_table)

@@ -21,7 +21,7 @@ namespace {
 
 constexpr int kMaxDevices = 64;
 constexpr int kDefaultPartitionTokens = 512;
-constexpr int kVersion = 10000;  // 1.0.0
+constexpr int kVersion = 10100;  // 1.1.0
 
 struct DeviceState {
     bool ready = false;

@@ -128,4 +128,59 @@ cudaError_t launch_reshape_and_cache(const uint16_t *k, const uint16_t *v, uint1
                                      int32_t block_size, int32_t num_blocks, unsigned int *err,
                                      cudaStream_t stream);
 
+// Arguments of the grouped-query attention calls (device pointers unless noted).
+struct GroupedArgs {
+    uint16_t *out;                 // [rows, Hq, D]
+    const uint16_t *q;             // [rows, Hq, D]
+    const uint16_t *k_cache;       // [N, Hkv, B, D]
+    const uint16_t *v_cache;       // [N, Hkv, B, D]
+    const int32_t *block_tables;   // [S, max_blocks_per_seq]
+    const int32_t *context_lens;   // [S]
+    const int32_t *query_start;    // [S + 1] (prefill)
+    const float *alibi_slopes;     // [Hq] or nullptr
+    const int32_t *prefix_lens;    // [S] or nullptr
+    float scale;
+    float softcap;                 // 0: none
+    int32_t window;                // 0: none
+    int32_t num_seqs;
+    int32_t num_q_heads;
+    int32_t num_kv_heads;
+    int32_t num_blocks;
+    int32_t block_size;
+    int32_t max_blocks_per_seq;
+    int32_t total_q;               // rows of q and out (prefill)
+    int32_t max_q;                 // bound of every q_len (prefill)
+    void *workspace;
+    uint32_t *counters;
+    unsigned int *err;
+};
+
+bool prefill_grouped_supported(int dtype, int head_dim, int block_size, int group);
+size_t decode_grouped_workspace_bytes(int head_dim, int group);
+size_t decode_grouped_counters_bytes(int num_seqs, int num_kv_heads, int group, int head_dim);
+size_t prefill_grouped_workspace_bytes(int num_seqs, int num_kv_heads, int group, int head_dim,
+                                       int max_query_len);
+size_t prefill_grouped_counters_bytes();
+cudaError_t launch_decode_grouped(const GroupedArgs &args, int dtype, int head_dim, int num_sms,
+                                  cudaStream_t stream);
+cudaError_t launch_prefill_grouped(const GroupedArgs &args, int dtype, int head_dim, int num_sms,
+                                   cudaStream_t stream);
+
+// Arguments of one rope_and_cache launch (device pointers unless noted).
+struct RopeArgs {
+    uint16_t *q_out;
+    const uint16_t *q, *k, *v;
+    uint16_t *k_cache, *v_cache;   // [N, Hkv, B, D]
+    const int32_t *positions;      // [T]
+    const float *cos_sin;          // [max_positions, rotary_dim]
+    const int32_t *slot_mapping;   // [T]
+    long long q_stride, k_stride, v_stride, q_out_stride;   // elements between tokens
+    int32_t num_tokens, num_q_heads, num_kv_heads, head_dim, block_size;
+    int32_t rotary_dim, max_positions;
+    long long pool_slots;          // N * B
+    unsigned int *err;
+};
+cudaError_t launch_rope_and_cache(const RopeArgs &args, int dtype, bool interleaved, int num_sms,
+                                  cudaStream_t stream);
+
 }  // namespace pa
