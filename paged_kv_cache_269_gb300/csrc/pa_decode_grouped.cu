@@ -1,0 +1,836 @@
+// pa_decode_grouped.cu -- attention of one new token per sequence over the
+// paged cache, with query heads that share K/V heads (sm_103a).
+//
+// Mathematics: for the G = Hq / Hkv query heads of one K/V head,
+//   s_gj = f(scale q_g . k_j),  o_g = sum_j 2^(x_gj - m_g) v_j / sum_j 2^(x_gj - m_g)
+// with x = s log2(e) (f: the optional tanh cap and distance bias), one pass
+// over the keys with a running reference m_g that every weight and the sum
+// share, so the result does not depend on it.
+//
+// What bounds it: each K and V element is used G times (2 G flops per
+// element read), so the call is bound by HBM as long as the products are
+// cheaper than the loads.  On the FMA pipe they are not from G = 4 on, so both
+// products run as mma.sync m16n8k16 with the 16 rows on the keys (then the
+// head dims) and the 8 columns on the query heads: a group of 8 heads fills
+// the shape, where tcgen05's 128-row tiles would be 1/16 used.
+//
+// How:
+//  * Work is cut evenly, not by sequence: all sequences' visible key tiles,
+//    laid end to end per (sequence, K/V head, chunk of query heads), form one
+//    line; CTA i takes the i-th equal piece of it.  A piece may end inside a
+//    context: it then leaves a partial (max, sum, unnormalised output) in one
+//    of its two slots, and the last piece of the context to finish (a ticket
+//    per context) joins all of them, in order, so the result does not depend
+//    on which came last.
+//  * No roles: each warp owns a ring of stages and is its own producer.  It
+//    takes every 4th tile of its CTA's piece, waits for the tile's TMA boxes,
+//    computes, and refills the stage it just read; the table entry of the
+//    refill was loaded one tile earlier.  Warps meet only where a context
+//    ends, to merge their (max, sum, output) through shared memory, while
+//    their rings keep filling.
+//  * S^T = K Q^T (rows: keys, columns: heads), so a lane holds the scores of
+//    two heads; the weights become the second product's B operand with one
+//    movmatrix, and O^T = V^T P^T accumulates in registers.
+//  * The weights enter P V as a 16-bit pair P_hi + P_lo (about 22 bits; 16 in
+//    bf16), so the output is as exact as fp32 weights make it.  With G <= 4
+//    the two halves share one product: columns 4-7 repeat the heads and carry
+//    P_lo.
+//  * The reference m is raised only when a score exceeds it by more than 8
+//    (weights stay below 2^(8 + 6), inside fp16), so most tiles need no
+//    maximum across lanes and no rescaling.
+//  * Keys that are not visible get weight 0 and their V values are cleared in
+//    registers, so nothing they hold reaches the output.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "pa_device.cuh"
+#include "pa_internal.h"
+#include "pa_tensor.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kW = 4;                  // warps per CTA
+constexpr int kThreads = kW * 32;
+constexpr int kChunks = 512;           // entries of the CTA's prefix over the sequences
+constexpr int kMaxCtas = 640;          // bounds the partial slots (2 per CTA)
+constexpr float kRaise = 8.f;
+constexpr float kBias = 6.f;           // weights are 2^(x - m + 6)
+
+struct DecodeGroupedArgs {
+    GroupedArgs g;
+    float scale_log2;                  // plain scores: x = scale_log2 (q . k)
+    float cap_log2, cap_in;            // capped: x = cap_log2 tanh(...), 2^(cap_in q.k) = e^(2 s / cap)
+    int group, chunks;                 // heads per K/V head; chunks of heads per K/V head
+    int chunk_shift;                   // sequences per prefix entry: 2^chunk_shift
+    float *partials;                   // [2 * kMaxCtas][heads * (D + 2)]
+};
+
+template <bool kBf16>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+    if constexpr (kBf16)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+            "{%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+            "{%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4_trans(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+__device__ __forceinline__ float fast_rcp(float x) {   // 1 ulp; 1 / inf = 0
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Two weights as packed 16-bit values, and the packed remainders.
+template <bool kBf16>
+__device__ __forceinline__ void split_pair(float a, float b, uint32_t &hi, uint32_t &lo) {
+    if constexpr (kBf16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        hi = *reinterpret_cast<const uint32_t *>(&h);
+        const __nv_bfloat162 l = __floats2bfloat162_rn(a - __uint_as_float(hi << 16),
+                                                       b - __uint_as_float(hi & 0xFFFF0000u));
+        lo = *reinterpret_cast<const uint32_t *>(&l);
+    } else {
+        const __half2 h = __floats2half2_rn(a, b);
+        const float2 f = __half22float2(h);
+        const __half2 l = __floats2half2_rn(a - f.x, b - f.y);
+        hi = *reinterpret_cast<const uint32_t *>(&h);
+        lo = *reinterpret_cast<const uint32_t *>(&l);
+    }
+}
+template <bool kBf16>
+__device__ __forceinline__ uint32_t pack_pair(float a, float b) {
+    if constexpr (kBf16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    } else {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+}
+
+// A sequence's visible keys as tiles of TK keys: tile i covers keys from
+// TK * (i < na ? i : i + skip); [lo, ctx) and [0, pre) are visible.
+struct Geo {
+    int ctx, lo, pre, na, skip, nt;
+};
+template <int TK>
+__device__ __forceinline__ Geo make_geo(const GroupedArgs &a, int ctx, int pre_raw) {
+    Geo g;
+    g.ctx = ctx;
+    g.lo = a.window > 0 ? max(0, ctx - a.window) : 0;
+    g.pre = max(0, min(pre_raw, ctx));
+    const int total = (ctx + TK - 1) / TK, first = g.lo / TK;
+    g.na = (g.pre + TK - 1) / TK;
+    if (first <= g.na && g.pre > 0) {
+        g.na = 0, g.skip = 0, g.nt = total;
+    } else {
+        g.skip = first - g.na;
+        g.nt = g.na + total - first;
+    }
+    return g;
+}
+
+// Context length of sequence s (0 for one outside its bounds) and prefix.
+__device__ __forceinline__ int load_ctx(const GroupedArgs &a, int s) {
+    if (s >= a.num_seqs) return 0;
+    const int c = __ldg(a.context_lens + s);
+    return (c < 0 || c > a.max_blocks_per_seq * a.block_size) ? 0 : c;
+}
+__device__ __forceinline__ int load_pre(const GroupedArgs &a, int s) {
+    return a.prefix_lens && s < a.num_seqs ? __ldg(a.prefix_lens + s) : 0;
+}
+
+// A position on the line: tile `idx` of unit `unit` of sequence s.  A unit is
+// one (K/V head, chunk of query heads); the lanes hold the lengths of 32
+// sequences.
+template <int TK>
+struct Cursor {
+    int s, unit, idx;
+    Geo g;
+    int base, ctx_l, pre_l;
+    __device__ __forceinline__ void load_group(const GroupedArgs &a, int lane) {
+        base = s & ~31;
+        ctx_l = load_ctx(a, base + lane);
+        pre_l = load_pre(a, base + lane);
+    }
+    __device__ __forceinline__ void set_geo(const GroupedArgs &a) {
+        g = make_geo<TK>(a, __shfl_sync(0xffffffffu, ctx_l, s & 31),
+                         __shfl_sync(0xffffffffu, pre_l, s & 31));
+    }
+    // The next sequence with tiles (or s = num_seqs, nt = 0).
+    __device__ __forceinline__ void next_seq(const GroupedArgs &a, int lane) {
+        ++s;
+        unit = 0;
+        for (;;) {
+            if (s >= a.num_seqs) {
+                s = a.num_seqs;
+                g.nt = 0;
+                return;
+            }
+            if ((s & ~31) != base) load_group(a, lane);
+            const unsigned rest = __ballot_sync(0xffffffffu, ctx_l > 0) >> (s & 31);
+            if (rest) {
+                s += __ffs(rest) - 1;
+                set_geo(a);
+                return;
+            }
+            s = base + 32;
+        }
+    }
+    __device__ __forceinline__ void advance(const GroupedArgs &a, int units, int by, int lane) {
+        idx += by;
+        while (idx >= g.nt && s < a.num_seqs) {
+            idx -= g.nt;
+            if (++unit == units) next_seq(a, lane);
+        }
+    }
+};
+
+template <int D, int NT>
+struct Cfg {
+    static constexpr int TK = D == 64 ? 32 : 16;       // keys per tile
+    static constexpr int MT = TK / 16;
+    static constexpr int kHeads = 8 * NT;
+    static constexpr int kMat = TK * D * 2;            // bytes of a K (or V) tile
+    static constexpr int kStage = 2 * kMat;
+    static constexpr int kStages = D == 64 ? 3 : 2;
+    static constexpr int kRow = D + 4;                 // floats of a merge row (no bank conflicts)
+    static constexpr int OFF_O = kW * kStages * kStage;
+    static constexpr int OFF_ML = OFF_O + kW * kHeads * kRow * 4;
+    static constexpr int OFF_PREFIX = OFF_ML + kW * kHeads * 8;
+    static constexpr int OFF_BAR = OFF_PREFIX + (kChunks + 1) * 8;
+    static constexpr int OFF_MASK = OFF_BAR + kW * kStages * 8;
+    static constexpr int OFF_FLAG = OFF_MASK + kW * kStages * 4;
+    static constexpr int kBytes = OFF_FLAG + 16 + 1024;  // + alignment slack
+    static constexpr int kCtasPerSm = 233472 / (kBytes + 1024) < 1 ? 1 : 233472 / (kBytes + 1024);
+};
+
+template <bool kBf16, int D, int NT, bool kDup>
+__global__ void __launch_bounds__(kThreads, 1)
+    decode_grouped_kernel(const __grid_constant__ CUtensorMap tm_k,
+                          const __grid_constant__ CUtensorMap tm_v,
+                          const __grid_constant__ DecodeGroupedArgs p) {
+    using C = Cfg<D, NT>;
+    constexpr int TK = C::TK, MT = C::MT, KS = D / 16, kHeads = C::kHeads;
+    const GroupedArgs &a = p.g;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    float *obuf = reinterpret_cast<float *>(smem + C::OFF_O);
+    float2 *ml = reinterpret_cast<float2 *>(smem + C::OFF_ML);
+    long long *prefix = reinterpret_cast<long long *>(smem + C::OFF_PREFIX);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_FLAG);
+    volatile int *last_flag = abort_flag + 1;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    uint64_t *bar = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR) + warp * C::kStages;
+    volatile uint32_t *stage_mask =
+        reinterpret_cast<volatile uint32_t *>(smem + C::OFF_MASK) + warp * C::kStages;
+    uint8_t *ring = smem + warp * C::kStages * C::kStage;
+
+    if (threadIdx.x == 0) {
+        *abort_flag = 0;
+        uint64_t *all = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
+        for (int i = 0; i < kW * C::kStages; ++i) mbar_init(&all[i], 1);
+        mbar_init_fence();
+    }
+    allow_dependents_to_launch();
+    grid_dependency_wait();
+
+    const int units = a.num_kv_heads * p.chunks;
+    // prefix[c]: tiles of the sequences before chunk c, all units
+    {
+        const int nchunks = (a.num_seqs + (1 << p.chunk_shift) - 1) >> p.chunk_shift;
+        for (int c = threadIdx.x; c < kChunks; c += kThreads) {
+            long long n = 0;
+            if (c < nchunks) {
+                const int s0 = c << p.chunk_shift;
+                const int s1 = min(a.num_seqs, (c + 1) << p.chunk_shift);
+                for (int s = s0; s < s1; ++s)
+                    n += make_geo<TK>(a, load_ctx(a, s), load_pre(a, s)).nt;
+            }
+            prefix[c + 1] = n * units;
+        }
+        __syncthreads();
+        if (warp == 0) {
+            constexpr int kPer = kChunks / 32;
+            long long v[kPer], sum = 0;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                sum += prefix[lane * kPer + i + 1];
+                v[i] = sum;
+            }
+            long long run = sum;
+#pragma unroll
+            for (int o = 1; o < 32; o *= 2) {
+                const long long t = __shfl_up_sync(0xffffffffu, run, o);
+                if (lane >= o) run += t;
+            }
+            run -= sum;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) prefix[lane * kPer + i + 1] = run + v[i];
+            if (lane == 0) prefix[0] = 0;
+        }
+        __syncthreads();
+    }
+    const long long total = prefix[kChunks];
+
+    // rows of sequences without keys are zero; bad lengths are reported
+    for (int s = blockIdx.x; s < a.num_seqs; s += gridDim.x) {
+        const int c = __ldg(a.context_lens + s);
+        if (c > 0 && c <= a.max_blocks_per_seq * a.block_size) continue;
+        if (c != 0 && threadIdx.x == 0) atomicOr(a.err, PA_DEVERR_CONTEXT);
+        uint4 *row = reinterpret_cast<uint4 *>(a.out + static_cast<size_t>(s) * a.num_q_heads * D);
+        for (int i = threadIdx.x; i < a.num_q_heads * (D / 8); i += kThreads)
+            row[i] = make_uint4(0, 0, 0, 0);
+    }
+
+    // Equal pieces.  Few tiles go to fewer CTAs: a context of n tiles is not
+    // cut finer than about sqrt(n / 2) tiles, where one CTA's streaming of a
+    // piece and its joining of the other pieces' partials take equally long.
+    long long ctas = gridDim.x;
+    {
+        const float mean = static_cast<float>(total) / (static_cast<float>(a.num_seqs) * units);
+        const int least = max(kW, static_cast<int>(sqrtf(mean * 0.5f)));
+        ctas = min(ctas, (total + least - 1) / least);
+    }
+    if (blockIdx.x >= ctas) return;
+    const long long f0 = blockIdx.x * total / ctas, f1 = (blockIdx.x + 1) * total / ctas;
+    const int mine = static_cast<int>(f1 - f0);       // tiles of this CTA
+
+    // the CTA's start: its prefix entry, then its sequence within the entry
+    Cursor<TK> cons;
+    {
+        int below = 0;
+        for (int c = lane; c < kChunks; c += 32) below += prefix[c + 1] <= f0;
+        const int c = __reduce_add_sync(0xffffffffu, below);
+        long long r = f0 - prefix[c];
+        cons.s = c << p.chunk_shift;
+        for (;;) {
+            cons.load_group(a, lane);
+            const int first = cons.s & 31;
+            long long n = lane >= first ? static_cast<long long>(make_geo<TK>(a, cons.ctx_l, cons.pre_l).nt) * units : 0;
+            long long run = n;
+#pragma unroll
+            for (int o = 1; o < 32; o *= 2) {
+                const long long t = __shfl_up_sync(0xffffffffu, run, o);
+                if (lane >= o) run += t;
+            }
+            const unsigned past = __ballot_sync(0xffffffffu, run > r);
+            if (past) {
+                const int l = __ffs(past) - 1;
+                r -= __shfl_sync(0xffffffffu, run - n, l);
+                cons.s = cons.base + l;
+                cons.set_geo(a);
+                cons.unit = static_cast<int>(r / cons.g.nt);
+                cons.idx = static_cast<int>(r % cons.g.nt);
+                break;
+            }
+            r -= __shfl_sync(0xffffffffu, run, 31);
+            cons.s = cons.base + 32;
+            if (cons.s >= a.num_seqs) return;   // cannot happen: f0 < total
+        }
+    }
+
+    // ---------------------------------------------------------- producer side
+    // A tile arrives as boxes of RB rows (8 for 8-token blocks, else 16): lane
+    // i < TK / RB owns box i, its table entry and its two copies.
+    const int B = a.block_size;
+    const int RB = B == 8 ? 8 : 16;
+    const int rb_shift = B == 8 ? 3 : 4;
+    const int boxes = TK / RB;
+    Cursor<TK> prod = cons;
+    prod.advance(a, units, warp, lane);
+    int issue_t = warp;                      // the CTA tile the next issue is for
+    // the lane's box of the tile at `prod`: physical block (-1: not needed,
+    // -2: needed but its entry is bad) and row within the block
+    int box_blk = -1, box_row = 0;
+    auto look_up = [&]() {
+        box_blk = -1;
+        if (lane < boxes && issue_t < mine) {
+            const int i = prod.idx;
+            const int k = TK * (i < prod.g.na ? i : i + prod.g.skip) + lane * RB;
+            if (k < prod.g.ctx && (k < prod.g.pre || k + RB > prod.g.lo)) {
+                const int e = __ldg(a.block_tables + static_cast<size_t>(prod.s) * a.max_blocks_per_seq + k / B);
+                box_blk = static_cast<unsigned>(e) < static_cast<unsigned>(a.num_blocks) ? e : -2;
+                box_row = k % B;
+            }
+        }
+    };
+    auto issue = [&](int stage) {
+        // every lane has read the stage's last tile (the caller's __syncwarp)
+        if (box_blk == -2) atomicOr(a.err, PA_DEVERR_TABLE);
+        const unsigned have = __ballot_sync(0xffffffffu, box_blk >= 0);
+        if (lane == 0) {
+            stage_mask[stage] = have;
+            mbar_arrive_expect_tx(&bar[stage], __popc(have) * 2u * RB * D * 2u);
+        }
+        __syncwarp();
+        if (box_blk >= 0) {
+            const int hk = prod.unit / p.chunks;
+            const int y = (box_blk * a.num_kv_heads + hk) * B + box_row;
+            uint8_t *dst = ring + stage * C::kStage + lane * (RB * D * 2);
+            tma_load_3d(dst, &tm_k, 0, y, 0, &bar[stage]);
+            tma_load_3d(dst + C::kMat, &tm_v, 0, y, 0, &bar[stage]);
+        }
+        issue_t += kW;
+        if (issue_t < mine) prod.advance(a, units, kW, lane);
+    };
+    int issued = 0;
+#pragma unroll
+    for (int st = 0; st < C::kStages; ++st)
+        if (issue_t < mine) {
+            look_up();
+            issue(st);
+            ++issued;
+        }
+    look_up();
+
+    // ---------------------------------------------------------- consumer side
+    // shared-memory layout of 16 keys: [D / 64 halves][16 rows][128 bytes],
+    // or per 8-token box, [halves][8 rows][128 bytes]; 128-byte swizzle
+    const uint32_t row_group = B == 8 ? 8 * D * 2 : 1024;   // rows 8-15 of 16
+    const uint32_t half_step = B == 8 ? 1024 : 2048;        // dims 64 apart
+    const uint32_t ring_addr = smem_addr(ring);
+    // ldmatrix rows: K (a0: keys 0-7, a1: keys 8-15, a2, a3: next 8 dims);
+    // V transposed (a0, a1: dims 0-7, 8-15 of keys 0-7; a2, a3: keys 8-15)
+    const int krow = (lane & 7), kgrp = (lane >> 3) & 1, kchunk = lane >> 4;
+    const int vgrp = lane >> 4, vchunk = (lane >> 3) & 1;
+    const uint32_t k_lane = kgrp * row_group + krow * 128;
+    const uint32_t v_lane = vgrp * row_group + krow * 128;
+    const int col = 2 * (lane & 3);          // the lane's two head columns
+    const int row = lane >> 2;               // its key row (and row + 8)
+
+    uint32_t qf[KS][NT][2];
+    float m[NT][2], l[NT][2], o[KS][NT][4], slope[NT][2];
+    bool ok = true;
+    int t = warp;                            // next tile of this warp
+    int n_done = 0;                          // tiles taken
+    int seg_start = 0;                       // CTA tile at which the segment starts
+
+    auto load_q = [&]() {
+        const int hk = cons.unit / p.chunks, h0 = (cons.unit % p.chunks) * kHeads;
+        const uint32_t *src = reinterpret_cast<const uint32_t *>(
+            a.q + (static_cast<size_t>(cons.s) * a.num_q_heads + hk * p.group) * D);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int hq = h0 + nt * 8 + (kDup ? (lane >> 2) % 4 : lane >> 2);
+            const bool live = hq < p.group;
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                qf[ks][nt][0] = live ? __ldg(src + (hq * D + ks * 16) / 2 + (lane & 3)) : 0u;
+                qf[ks][nt][1] = live ? __ldg(src + (hq * D + ks * 16 + 8) / 2 + (lane & 3)) : 0u;
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int h = h0 + nt * 8 + (kDup ? (col + e) % 4 : col + e);
+                slope[nt][e] = a.alibi_slopes && h < p.group
+                                   ? __ldg(a.alibi_slopes + hk * p.group + h) * 1.4426950408889634f
+                                   : 0.f;
+            }
+        }
+    };
+
+    load_q();
+    while (seg_start < mine) {
+        const Geo g = cons.g;
+        const int seg_len = min(g.nt - cons.idx, mine - seg_start);
+        const int idx0 = cons.idx;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            m[nt][0] = m[nt][1] = -INFINITY;
+            l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[ks][nt][e] = 0.f;
+        }
+        for (; t < seg_start + seg_len; t += kW) {
+            const int st = n_done % C::kStages;
+            const uint32_t ph = (n_done / C::kStages) & 1;
+            ++n_done;
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(&bar[st], ph, abort_flag, a.err));
+            if (!ok) continue;
+            const int ti = idx0 + (t - seg_start);
+            const int k0 = TK * (ti < g.na ? ti : ti + g.skip);
+            const uint32_t kb = ring_addr + st * C::kStage, vb = kb + C::kMat;
+            float sc[MT][NT][4];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sc[mt][nt][e] = 0.f;
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                const uint32_t c16 = ks * 2 + kchunk;   // 16-byte chunk of the row
+                const uint32_t off = (ks / 4) * half_step + (((c16 & 7) ^ krow) << 4);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    uint32_t kf[4];
+                    ldsm4(kf, kb + mt * (16 * D * 2) + k_lane + off);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma16816<kBf16>(sc[mt][nt], kf, qf[ks][nt][0], qf[ks][nt][1]);
+                }
+            }
+            // scores in the log2 domain
+            const unsigned have = stage_mask[st];
+            const bool partial = have != (1u << boxes) - 1 || k0 + TK > g.ctx ||
+                                 (k0 < g.lo && k0 + TK > g.pre);
+            bool raise = false;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float x = sc[mt][nt][e];
+                        if (a.softcap > 0.f)
+                            x = p.cap_log2 - 2.f * p.cap_log2 * fast_rcp(1.f + fast_exp2(x * p.cap_in));
+                        else
+                            x *= p.scale_log2;
+                        const int key = k0 + mt * 16 + row + (e >= 2 ? 8 : 0);
+                        if (a.alibi_slopes) x -= slope[nt][e & 1] * static_cast<float>(g.ctx - 1 - key);
+                        if (partial) {
+                            const bool vis = (key < g.pre || key >= g.lo) && key < g.ctx &&
+                                             ((have >> ((key - k0) >> rb_shift)) & 1);
+                            x = vis ? x : -INFINITY;
+                        }
+                        sc[mt][nt][e] = x;
+                        raise |= x > m[nt][e & 1] + kRaise;
+                    }
+            if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float x = -INFINITY;
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt)
+                            x = fmaxf(x, fmaxf(sc[mt][nt][e], sc[mt][nt][e + 2]));
+#pragma unroll
+                        for (int d = 4; d < 32; d *= 2)
+                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+                        if (x > m[nt][e] + kRaise) {
+                            const float r = m[nt][e] == -INFINITY ? 0.f : fast_exp2(m[nt][e] - x);
+                            m[nt][e] = x;
+                            l[nt][e] *= r;
+#pragma unroll
+                            for (int ks = 0; ks < KS; ++ks) {
+                                o[ks][nt][e] *= r;
+                                o[ks][nt][e + 2] *= r;
+                            }
+                        }
+                    }
+            }
+            uint32_t ph_[MT][NT][2], pl_[MT][NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const float b0 = m[nt][0] == -INFINITY ? 0.f : kBias - m[nt][0];
+                const float b1 = m[nt][1] == -INFINITY ? 0.f : kBias - m[nt][1];
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        const float w0 = fast_exp2(sc[mt][nt][2 * hf] + b0);
+                        const float w1 = fast_exp2(sc[mt][nt][2 * hf + 1] + b1);
+                        l[nt][0] += w0;
+                        l[nt][1] += w1;
+                        uint32_t hi, lo;
+                        split_pair<kBf16>(w0, w1, hi, lo);
+                        if constexpr (kDup) {
+                            // columns 4-7 (lanes with col >= 4) carry the remainders
+                            ph_[mt][nt][hf] = transpose8x8(col >= 4 ? lo : hi);
+                            pl_[mt][nt][hf] = 0;
+                        } else {
+                            ph_[mt][nt][hf] = transpose8x8(hi);
+                            pl_[mt][nt][hf] = transpose8x8(lo);
+                        }
+                    }
+            }
+            // O^T += V^T P^T
+            auto pv = [&](auto masked) {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    uint32_t keep0 = 0xFFFFFFFFu, keep1 = 0xFFFFFFFFu;
+                    if constexpr (decltype(masked)::value) {
+                        keep0 = keep1 = 0;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int key = k0 + mt * 16 + col + (e & 1) + (e >= 2 ? 8 : 0);
+                            const bool vis = (key < g.pre || key >= g.lo) && key < g.ctx &&
+                                             ((have >> ((key - k0) >> rb_shift)) & 1);
+                            const uint32_t bits = vis ? ((e & 1) ? 0xFFFF0000u : 0xFFFFu) : 0u;
+                            if (e < 2)
+                                keep0 |= bits;
+                            else
+                                keep1 |= bits;
+                        }
+                    }
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks) {
+                        const uint32_t c16 = ks * 2 + vchunk;
+                        const uint32_t off = (ks / 4) * half_step + (((c16 & 7) ^ krow) << 4);
+                        uint32_t vf[4];
+                        ldsm4_trans(vf, vb + mt * (16 * D * 2) + v_lane + off);
+                        if constexpr (decltype(masked)::value) {
+                            vf[0] &= keep0, vf[1] &= keep0, vf[2] &= keep1, vf[3] &= keep1;
+                        }
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma16816<kBf16>(o[ks][nt], vf, ph_[mt][nt][0], ph_[mt][nt][1]);
+                            if constexpr (!kDup)
+                                mma16816<kBf16>(o[ks][nt], vf, pl_[mt][nt][0], pl_[mt][nt][1]);
+                        }
+                    }
+                }
+            };
+            if (partial)
+                pv(std::true_type{});
+            else
+                pv(std::false_type{});
+            __syncwarp();
+            if (issue_t < mine) {
+                issue(st);
+                ++issued;
+                look_up();
+            }
+        }
+
+        // ------------------------------------------------ end of the segment
+        const int s = cons.s, unit = cons.unit;
+        const int hk = unit / p.chunks, h0 = (unit % p.chunks) * kHeads;
+        const int heads = min(kHeads, p.group - h0);
+        // the unit's place on the line, and whether this piece covers it whole
+        const bool from_start = idx0 == 0, to_end = idx0 + seg_len == g.nt;
+        const long long u0 = f0 + seg_start - idx0, u1 = u0 + g.nt;   // its tiles
+        // the next unit's q is loaded while this one is merged
+        seg_start += seg_len;
+        cons.idx += seg_len;
+        if (seg_start < mine) {
+            cons.advance(a, units, 0, lane);
+            load_q();
+        }
+        __syncthreads();   // everyone has read the previous merge
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float x = l[nt][e];
+#pragma unroll
+                for (int d = 4; d < 32; d *= 2) x += __shfl_xor_sync(0xffffffffu, x, d);
+                const int h = nt * 8 + col + e;
+                if (row == 0) ml[warp * kHeads + h] = make_float2(m[nt][e], x);
+                float *dst = obuf + (warp * kHeads + h) * C::kRow + row;
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) {
+                    dst[ks * 16] = o[ks][nt][e];
+                    dst[ks * 16 + 8] = o[ks][nt][e + 2];
+                }
+            }
+        __syncthreads();
+        constexpr int kVec = D / 4;            // float4s per head
+        const bool whole = from_start && to_end;
+        float *slot = p.partials + static_cast<size_t>(2 * blockIdx.x + (from_start ? 1 : 0)) *
+                                       (kHeads * (D + 2));
+        for (int i = threadIdx.x; i < heads * kVec; i += kThreads) {
+            const int h = i / kVec, d4 = i % kVec;
+            float mw[kW], top = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kW; ++w) {
+                mw[w] = ml[w * kHeads + h].x;
+                top = fmaxf(top, mw[w]);
+            }
+            float sum = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kW; ++w) {
+                const float f = mw[w] == -INFINITY ? 0.f : fast_exp2(mw[w] - top);
+                sum += f * ml[w * kHeads + h].y;
+                float4 v = *reinterpret_cast<const float4 *>(obuf + (w * kHeads + h) * C::kRow + d4 * 4);
+                if constexpr (kDup) {
+                    const float4 r = *reinterpret_cast<const float4 *>(
+                        obuf + (w * kHeads + h + 4) * C::kRow + d4 * 4);
+                    v.x += r.x, v.y += r.y, v.z += r.z, v.w += r.w;
+                }
+                acc.x += f * v.x, acc.y += f * v.y, acc.z += f * v.z, acc.w += f * v.w;
+            }
+            if (whole) {
+                const float inv = sum > 0.f ? 1.f / sum : 0.f;
+                uint2 r = make_uint2(pack_pair<kBf16>(acc.x * inv, acc.y * inv),
+                                     pack_pair<kBf16>(acc.z * inv, acc.w * inv));
+                *reinterpret_cast<uint2 *>(
+                    a.out + (static_cast<size_t>(s) * a.num_q_heads + hk * p.group + h0 + h) * D + d4 * 4) = r;
+            } else {
+                *reinterpret_cast<float4 *>(slot + h * D + d4 * 4) = acc;
+                if (d4 == 0)
+                    *reinterpret_cast<float2 *>(slot + kHeads * D + 2 * h) = make_float2(top, sum);
+            }
+        }
+        if (!whole) {
+            // pieces that hold part of the unit: the CTAs of its first and last tile
+            const int i0 = static_cast<int>(((u0 + 1) * ctas - 1) / total);
+            const int i1 = static_cast<int>((u1 * ctas - 1) / total);
+            __threadfence();
+            __syncthreads();
+            uint32_t *ticket = a.counters + static_cast<size_t>(s) * units + unit;
+            if (threadIdx.x == 0) {
+                const bool last = atomicAdd(ticket, 1u) == static_cast<uint32_t>(i1 - i0);
+                if (last) atomicExch(ticket, 0u);
+                *last_flag = last;
+            }
+            __syncthreads();
+            if (*last_flag) {
+                __threadfence();
+                // slot of piece i: 2 i + 1 for the one the unit starts in, else 2 i
+                auto part = [&](int i) {
+                    return p.partials + static_cast<size_t>(2 * i + (i == i0 ? 1 : 0)) * (kHeads * (D + 2));
+                };
+                for (int i = threadIdx.x; i < heads * kVec; i += kThreads) {
+                    const int h = i / kVec, d4 = i % kVec;
+                    float top = -INFINITY;
+#pragma unroll 8
+                    for (int c = i0; c <= i1; ++c)
+                        top = fmaxf(top, __ldcg(part(c) + kHeads * D + 2 * h));
+                    float sum = 0.f;
+                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+                    for (int c = i0; c <= i1; ++c) {
+                        const float *src = part(c);
+                        const float2 w = __ldcg(reinterpret_cast<const float2 *>(src + kHeads * D + 2 * h));
+                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(src + h * D + d4 * 4));
+                        const float f = w.x == -INFINITY ? 0.f : fast_exp2(w.x - top);
+                        sum += f * w.y;
+                        acc.x += f * v.x, acc.y += f * v.y, acc.z += f * v.z, acc.w += f * v.w;
+                    }
+                    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+                    uint2 r = make_uint2(pack_pair<kBf16>(acc.x * inv, acc.y * inv),
+                                         pack_pair<kBf16>(acc.z * inv, acc.w * inv));
+                    *reinterpret_cast<uint2 *>(
+                        a.out + (static_cast<size_t>(s) * a.num_q_heads + hk * p.group + h0 + h) * D + d4 * 4) = r;
+                }
+            }
+        }
+    }
+    if (!ok) {   // let every copy already issued land before the CTA leaves
+        for (int i = max(0, issued - C::kStages); i < issued; ++i)
+            mbar_wait_drain(&bar[i % C::kStages], (i / C::kStages) & 1);
+    }
+}
+
+int heads_per_chunk(int head_dim, int group) { return group > 8 && head_dim != 256 ? 16 : 8; }
+
+using Kernel = void (*)(CUtensorMap, CUtensorMap, DecodeGroupedArgs);
+struct Variant {
+    Kernel kernel;
+    int smem, ctas_per_sm;
+};
+template <bool kBf16, int D>
+Variant variant_of(int group) {
+    if (D != 256 && group > 8)
+        return {decode_grouped_kernel<kBf16, D, D == 256 ? 1 : 2, false>, Cfg<D, D == 256 ? 1 : 2>::kBytes,
+                Cfg<D, D == 256 ? 1 : 2>::kCtasPerSm};
+    if (group > 4)
+        return {decode_grouped_kernel<kBf16, D, 1, false>, Cfg<D, 1>::kBytes, Cfg<D, 1>::kCtasPerSm};
+    return {decode_grouped_kernel<kBf16, D, 1, true>, Cfg<D, 1>::kBytes, Cfg<D, 1>::kCtasPerSm};
+}
+
+}  // namespace
+
+size_t decode_grouped_workspace_bytes(int head_dim, int group) {
+    return static_cast<size_t>(2 * kMaxCtas) * heads_per_chunk(head_dim, group) * (head_dim + 2) * 4;
+}
+size_t decode_grouped_counters_bytes(int num_seqs, int num_kv_heads, int group, int head_dim) {
+    const int per = heads_per_chunk(head_dim, group);
+    const size_t tickets = static_cast<size_t>(num_seqs) * num_kv_heads * ((group + per - 1) / per);
+    return (tickets * 4 + 4 + 255) / 256 * 256;
+}
+
+cudaError_t launch_decode_grouped(const GroupedArgs &args, int dtype, int head_dim, int num_sms,
+                                  cudaStream_t stream) {
+    const bool bf16 = dtype == PA_DTYPE_BF16;
+    const int B = args.block_size, Hk = args.num_kv_heads;
+    DecodeGroupedArgs p;
+    p.g = args;
+    const double log2e = 1.4426950408889634;
+    p.scale_log2 = static_cast<float>(args.scale * log2e);
+    p.cap_log2 = static_cast<float>(args.softcap * log2e);
+    p.cap_in = args.softcap > 0.f ? static_cast<float>(2.0 * args.scale / args.softcap * log2e) : 0.f;
+    p.group = args.num_q_heads / Hk;
+    const int per = heads_per_chunk(head_dim, p.group);
+    p.chunks = (p.group + per - 1) / per;
+    p.chunk_shift = 0;
+    while (((static_cast<long long>(args.num_seqs) - 1) >> p.chunk_shift) >= kChunks) ++p.chunk_shift;
+    p.partials = static_cast<float *>(args.workspace);
+
+    // [D / 64 halves] x [all cache rows] x 64 dims: one box is a block's rows
+    // (or 16 of them) of one head, each half in the 128-byte swizzle
+    CUtensorMap tm_k, tm_v;
+    const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(args.num_blocks) * Hk * B,
+                                static_cast<cuuint64_t>(head_dim / 64)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_dim) * 2, 128};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(B == 8 ? 8 : 16),
+                               static_cast<cuuint32_t>(head_dim / 64)};
+    if (!encode(&tm_k, bf16, args.k_cache, 3, dims, strides, box) ||
+        !encode(&tm_v, bf16, args.v_cache, 3, dims, strides, box))
+        return cudaErrorInvalidValue;
+
+    Variant v;
+    if (bf16)
+        v = head_dim == 64 ? variant_of<true, 64>(p.group)
+                           : (head_dim == 128 ? variant_of<true, 128>(p.group) : variant_of<true, 256>(p.group));
+    else
+        v = head_dim == 64 ? variant_of<false, 64>(p.group)
+                           : (head_dim == 128 ? variant_of<false, 128>(p.group) : variant_of<false, 256>(p.group));
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(reinterpret_cast<const void *>(v.kernel),
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem);
+    if (e != cudaSuccess) return e;
+    const int ctas = v.ctas_per_sm * num_sms;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas < kMaxCtas ? ctas : kMaxCtas));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = v.smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    void *params[] = {&tm_k, &tm_v, &p};
+    return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void *>(v.kernel), params);
+}
+
+}  // namespace pa

@@ -116,15 +116,9 @@ cudaError_t launch_rows(const GroupedArgs &a, int dtype, int head_dim, int rows,
 bool prefill_grouped_supported(int dtype, int head_dim, int block_size, int group) {
     return decode_variant_supported(dtype, head_dim, block_size) && head_dim != 256 && group <= 128;
 }
-size_t decode_grouped_workspace_bytes(int, int) { return 256; }
-size_t decode_grouped_counters_bytes(int, int, int, int) { return 256; }
 size_t prefill_grouped_workspace_bytes(int, int, int, int, int) { return 0; }
 size_t prefill_grouped_counters_bytes() { return 256; }
 
-cudaError_t launch_decode_grouped(const GroupedArgs &args, int dtype, int head_dim, int,
-                                  cudaStream_t stream) {
-    return launch_rows(args, dtype, head_dim, 1, stream);
-}
 cudaError_t launch_prefill_grouped(const GroupedArgs &args, int dtype, int head_dim, int,
                                    cudaStream_t stream) {
     return launch_rows(args, dtype, head_dim, args.max_q, stream);
