@@ -71,6 +71,7 @@ GroupedArgs make_args(void *out, const void *q, const void *k_cache, const void 
 
 int finish(cudaError_t e) {
     if (e == cudaErrorInvalidValue) return PA_ERR_UNSUPPORTED;  // tensor maps could not be made
+    if (e == cudaErrorInvalidConfiguration) return PA_ERR_SHAPE;  // too many work items
     return e == cudaSuccess ? PA_OK : record_cuda_error(e);
 }
 

@@ -1,0 +1,837 @@
+// pa_prefill_grouped.cu -- many queries of each sequence over the paged cache,
+// with query heads that share K/V heads, on the tcgen05 tensor cores (sm_103a).
+//
+// Mathematics: for query row (token at position p, head g of K/V head h) and
+// key j, x_j = log2(e) f(scale q . k_j) with f the optional tanh cap and
+// distance bias, and o = sum_j 2^(x_j - m) v_j / sum_j 2^(x_j - m) over the
+// visible keys, in one pass over 128-key tiles with a reference m that is only
+// raised when a tile's maximum exceeds it by more than 8 (a common factor of
+// weights and sum cancels, so m need not be the maximum).
+//
+// What bounds it: 4 D flops per (row, key) pair on the tensor cores, and one
+// ex2 per pair (three with the cap) on the special-function unit.
+//
+// How (persistent, one CTA per SM, 384 threads):
+//  * A tile is 128 rows of (token, head) pairs: 128 / G tokens x the G heads of
+//    one K/V head, gathered by one tensor-map box of Q, so K and V are loaded
+//    and multiplied once for all heads that share them.  A work item is two
+//    such tiles, one K/V head, one sequence, and a range of key tiles.
+//  * Warp 8 (TMA) takes items from a queue, heaviest first, describes each to
+//    the other roles through a two-slot ring, and streams K and V tiles of 128
+//    keys (the blocks named by the table, as 64-dim x block boxes) through one
+//    ring of slots K0 V0 K1 V1 ...
+//  * Warps 9 and 10 issue the products of tile 0 and 1, one thread each:
+//    S = Q K^T into tensor memory; once the softmax has put P over S,
+//    O += P V (P read from tensor memory); once that is complete, the next S.
+//    While one tile's softmax works, the other tile's products run.
+//  * Warps 0-3 / 4-7 (softmax of tile 0 / 1): thread = row = tensor-memory
+//    lane.  Loads its 128 scores, takes the maximum, exponentiates, and stores
+//    the weights as 16-bit values over the scores.
+//  * The weights are rounded to 16 bits (the element type) before P V, the sum
+//    is taken before the rounding, in fp32.  A weight is then off by half a
+//    step of the type, independently of its neighbours, so the output's error
+//    grows to about 1.4 times that of its own final rounding; carrying a
+//    second 16-bit term would cost half as much tensor work again.
+//  * V rows that no query may see (past the context, or of blocks that are not
+//    loaded) are cleared, since a zero weight times a NaN is NaN.
+//  * Few rows over long contexts: an item's key tiles are split over several
+//    CTAs, which leave partial (max, sum, output) and take a ticket; the last
+//    one joins them in order.
+//  * Tensor memory: S/P of tile t at columns 128 t, O of tile t at 256 + D t.
+//  * Every wait is bounded; tensor memory is released on every path.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "pa_device.cuh"
+#include "pa_internal.h"
+#include "pa_tensor.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kBM = 128;               // rows per tile (MMA M)
+constexpr int kBN = 128;               // keys per tile
+constexpr int kThreads = 384;          // 2 x 4 softmax warps, TMA warp, 2 MMA warps, 1 idle
+constexpr int kTmaWarp = 8;
+constexpr int kMmaWarp0 = 9;
+// Register split: launched at 168 per thread; the four producer warps give
+// registers up to the eight softmax warps: 2 x 216 + 72 = 3 x 168.
+constexpr int kRegsSoftmax = 216, kRegsOther = 72;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kTmemO = 256;
+constexpr float kRaise = 8.f;
+constexpr float kBias = 6.f;           // weights are 2^(x - m + 6): at most 2^14
+constexpr int kMaskRing = 16;
+// Work is split over keys while there are fewer items than SMs (152).
+constexpr int kSplitTarget = 152;
+constexpr int kCounters = 2 + 8 * kSplitTarget;   // queue head, CTAs done, a ticket per (item, warp)
+
+struct PrefillGroupedArgs {
+    GroupedArgs g;
+    float scale_log2, cap_log2, cap_in;
+    int group, tpt;                    // heads per K/V head; tokens per tile
+    int num_pairs, splits;
+    int num_items;                     // num_pairs * splits * S * Hkv
+    float *partials;                   // [item without split][split][tile][D + 2][128]
+};
+
+// Everything the roles need to know of an item (the TMA warp writes it).
+struct Item {
+    int done;                          // 1: the queue is empty
+    int hk, q_first, tok0, q_len, ctx, pre;
+    int first_pos;                     // position of the pair's first token
+    int na, skip;                      // key tile of list entry i: i < na ? i : i + skip
+    int j0, nkt;                       // list entries of this split
+    int nk0, nk1;                      // of which tile 0 / 1 needs the first nk
+    int split, splits;                 // this split, of how many
+    int slot;                          // item without its split (partials, tickets)
+    int s;
+};
+
+template <int D>
+struct Cfg {
+    static constexpr int kHalves = D / 64;
+    static constexpr int kHalfQ = kBM * 128;
+    static constexpr int kTileQ = kHalves * kHalfQ;
+    static constexpr int kHalfKV = kBN * 128;
+    static constexpr int kTileKV = kHalves * kHalfKV;
+    static constexpr int kSlots = D == 64 ? 10 : 5;
+    static constexpr int OFF_Q = 0;
+    static constexpr int OFF_KV = 2 * kTileQ;
+    static constexpr int OFF_BAR = OFF_KV + kSlots * kTileKV;
+    static constexpr int Q_FULL = 0, Q_EMPTY = 1, V_LAND = 2;
+    static constexpr int S_FULL = 3, P_FULL = 5, PV_DONE = 7, MMA_DONE = 9;
+    static constexpr int ITEM_FULL = 11, ITEM_EMPTY = 13;
+    static constexpr int KV_FULL = 15, KV_EMPTY = KV_FULL + kSlots;
+    static constexpr int kNumBars = KV_EMPTY + kSlots;
+    static constexpr int OFF_TMEM = OFF_BAR + kNumBars * 8;
+    static constexpr int OFF_FLAG = OFF_TMEM + 4;
+    static constexpr int OFF_MASK = OFF_FLAG + 4;                   // uint32[kMaskRing]
+    static constexpr int OFF_ITEM = OFF_MASK + kMaskRing * 4;       // Item[2]
+    static constexpr int kSmemBytes = OFF_ITEM + 2 * static_cast<int>(sizeof(Item)) + 1024;
+    static_assert(kSmemBytes <= 232448, "shared memory");
+};
+
+// kind::f16 instruction descriptor: fp32 accumulate, A and B fp16 or bf16, A
+// K-major, B K-major or MN-major, M = 128.
+__host__ __device__ constexpr uint32_t instr_desc(bool bf16, bool b_mn, int n) {
+    return (1u << 4) | (static_cast<uint32_t>(bf16) << 7) | (static_cast<uint32_t>(bf16) << 10) |
+           (static_cast<uint32_t>(b_mn) << 16) | (static_cast<uint32_t>(n >> 3) << 17) |
+           (static_cast<uint32_t>(kBM >> 4) << 24);
+}
+
+template <bool kBf16>
+__device__ __forceinline__ uint32_t pack_pair(float a, float b) {
+    if constexpr (kBf16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    } else {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+}
+__device__ __forceinline__ float fast_rcp(float x) {   // 1 ulp; 1 / inf = 0
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// The low n bits set (none for n <= 0, all from n = 32 on).
+__device__ __forceinline__ uint32_t bits_below(int n) {
+    return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u);
+}
+// Keys 32 q .. 32 q + 31 of a tile that lie in blocks with their bit in `have`.
+__device__ __forceinline__ uint32_t present(unsigned have, int q, int block_size) {
+    if (block_size == 32) return (have >> q) & 1 ? 0xffffffffu : 0u;
+    if (block_size == 16)
+        return ((have >> (2 * q)) & 1 ? 0xffffu : 0u) | ((have >> (2 * q + 1)) & 1 ? 0xffff0000u : 0u);
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m |= (have >> (4 * q + i)) & 1 ? 0xffu << (8 * i) : 0u;
+    return m;
+}
+__device__ __forceinline__ bool warp_all(bool v) { return __all_sync(0xffffffffu, v); }
+
+// Work item w: (pair level, split, sequence, K/V head), latest pairs first.
+// False for an empty item, or for a sequence whose lengths are inconsistent
+// (reported once).
+__device__ __forceinline__ bool item_geometry(const PrefillGroupedArgs &p, int w, bool report,
+                                              Item &it) {
+    const GroupedArgs &a = p.g;
+    const int sh = a.num_seqs * a.num_kv_heads;
+    const int level = w / (sh * p.splits);
+    int rem = w - level * (sh * p.splits);
+    const int split = rem / sh;
+    rem -= split * sh;
+    const int s = rem / a.num_kv_heads, hk = rem - s * a.num_kv_heads;
+    const int pair = p.num_pairs - 1 - level;
+    const int q_first = __ldg(a.query_start + s), q_end = __ldg(a.query_start + s + 1);
+    const int ctx = __ldg(a.context_lens + s);
+    const int pre_raw = a.prefix_lens ? __ldg(a.prefix_lens + s) : 0;
+    const bool rows_bad = q_first < 0 || q_end < q_first || q_end > a.total_q;
+    const int q_len = rows_bad ? 0 : q_end - q_first;
+    const int tok0 = pair * 2 * p.tpt;
+    if (rows_bad || (q_len > 0 && (q_len > ctx || ctx > a.max_blocks_per_seq * a.block_size ||
+                                   q_len > a.max_q))) {
+        if (report && hk == 0 && pair == 0 && split == 0) atomicOr(a.err, PA_DEVERR_CONTEXT);
+        return false;
+    }
+    if (tok0 >= q_len) return false;
+    it.done = 0;
+    it.s = s;
+    it.hk = hk;
+    it.q_first = q_first;
+    it.tok0 = tok0;
+    it.q_len = q_len;
+    it.ctx = ctx;
+    it.pre = max(0, min(pre_raw, ctx));
+    it.first_pos = ctx - q_len + tok0;
+    // keys: [0, pre) and [lo, up), as a list of 128-key tiles
+    const int last_tok = min(tok0 + 2 * p.tpt, q_len) - 1;
+    const int up = max(ctx - q_len + last_tok + 1, it.pre);
+    const int lo = a.window > 0 ? max(0, it.first_pos - a.window + 1) : 0;
+    const int total = (up + kBN - 1) / kBN, first = lo / kBN;
+    int count;
+    it.na = (it.pre + kBN - 1) / kBN;
+    if (first <= it.na && it.pre > 0) {
+        it.na = 0, it.skip = 0, count = total;
+    } else {
+        it.skip = first - it.na;
+        count = it.na + max(total - first, 0);
+    }
+    // tile 0 ends earlier: its last token's key, or the prefix
+    const int up0 = max(min(it.first_pos + p.tpt, ctx), it.pre);
+    const int end0 = (up0 + kBN - 1) / kBN;
+    const int need0 = min(count, end0 <= it.na ? end0 : max(it.na, end0 - it.skip));
+    // one split per about sqrt(count / 2) key tiles: there, streaming a part
+    // and joining the others' partials take about equally long
+    int parts = 1;
+    if (p.splits > 1) {
+        const int per = max(2, static_cast<int>(ceilf(sqrtf(0.5f * count))));
+        parts = min(p.splits, (count + per - 1) / per);
+    }
+    if (split >= parts) return false;
+    const int j1 = static_cast<int>(static_cast<long long>(count) * (split + 1) / parts);
+    it.j0 = static_cast<int>(static_cast<long long>(count) * split / parts);
+    it.nkt = j1 - it.j0;
+    it.nk0 = max(0, min(need0, j1) - it.j0);
+    it.nk1 = tok0 + p.tpt < q_len ? it.nkt : -1;   // -1: tile 1 has no rows
+    it.split = split;
+    it.splits = parts;
+    it.slot = pair * sh + rem;
+    return true;
+}
+
+template <bool kBf16, int D, bool kCap, bool kAlibi>
+__global__ void __launch_bounds__(kThreads, 1)
+    prefill_grouped_kernel(const __grid_constant__ CUtensorMap tm_q,
+                           const __grid_constant__ CUtensorMap tm_k,
+                           const __grid_constant__ CUtensorMap tm_v,
+                           const __grid_constant__ PrefillGroupedArgs p) {
+    using C = Cfg<D>;
+    const GroupedArgs &a = p.g;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint64_t *bar = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
+    volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(smem + C::OFF_TMEM);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_FLAG);
+    volatile uint32_t *mask_ring = reinterpret_cast<volatile uint32_t *>(smem + C::OFF_MASK);
+    Item *items = reinterpret_cast<Item *>(smem + C::OFF_ITEM);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int B = a.block_size;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kNumBars; ++i) {
+            uint32_t count = 1;
+            if (i == C::P_FULL || i == C::P_FULL + 1) count = 4;              // softmax warps
+            if (i == C::ITEM_EMPTY || i == C::ITEM_EMPTY + 1) count = 10;     // 2 MMA threads, 8 warps
+            if (i == C::Q_EMPTY || i >= C::KV_EMPTY) count = 2;               // both MMA threads
+            mbar_init(&bar[i], count);
+        }
+        *abort_flag = 0;
+        mbar_init_fence();
+    }
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_addr(const_cast<uint32_t *>(tmem_slot))),
+                     "r"(kTmemCols));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    grid_dependency_wait();
+    allow_dependents_to_launch();
+
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+        if (warp == kTmaWarp) {
+            // -------------------------------------------------------- TMA
+            const int boxes = kBN / B;             // per K or V tile
+            uint32_t g = 0;                        // K and V tiles issued, over all items
+            uint32_t lands = 0, tiles = 0;
+            int k = 0;                             // items published
+            int q_loads = 0;
+            bool ok = true;
+            for (;;) {
+                int w = 0;
+                Item it;
+                for (;;) {
+                    if (lane == 0) w = static_cast<int>(atomicAdd(a.counters, 1u));
+                    w = __shfl_sync(0xffffffffu, w, 0);
+                    if (static_cast<unsigned>(w) >= static_cast<unsigned>(p.num_items)) break;
+                    if (item_geometry(p, w, lane == 0, it)) break;
+                }
+                const bool done = static_cast<unsigned>(w) >= static_cast<unsigned>(p.num_items);
+                const int slot = k % 2;
+                ok = warp_all(mbar_wait(&bar[C::ITEM_EMPTY + slot], ((k / 2) & 1) ^ 1, abort_flag, a.err));
+                if (!ok) break;
+                if (lane == 0) {
+                    if (done)
+                        items[slot].done = 1;
+                    else
+                        items[slot] = it;
+                    mbar_arrive(&bar[C::ITEM_FULL + slot]);
+                }
+                if (done) break;
+                // blocks some query of the sequence sees (only those are read)
+                const int lo_seq = a.window > 0 ? max(0, it.ctx - it.q_len - a.window + 1) : 0;
+                const int32_t *table = a.block_tables + static_cast<size_t>(it.s) * a.max_blocks_per_seq;
+                // this lane's block of list entry j: its physical block, -1 if
+                // it is not needed, -2 if its entry is bad
+                auto look_up = [&](int j) {
+                    if (lane >= boxes || j >= it.nkt) return -1;
+                    const int i = it.j0 + j;
+                    const int key = kBN * (i < it.na ? i : i + it.skip) + lane * B;
+                    if (key >= it.ctx || (key >= it.pre && key + B <= lo_seq)) return -1;
+                    const int e = __ldg(table + key / B);
+                    return static_cast<unsigned>(e) < static_cast<unsigned>(a.num_blocks) ? e : -2;
+                };
+                int blk = look_up(0);
+                for (int j = 0; j < it.nkt && ok; ++j) {
+                    const int next = look_up(j + 1);
+                    if (blk == -2) atomicOr(a.err, PA_DEVERR_TABLE);
+                    const unsigned have = __ballot_sync(0xffffffffu, blk >= 0);
+                    const uint32_t bytes = __popc(have) * static_cast<uint32_t>(B * D * 2);
+                    const int i = it.j0 + j;
+                    const int k0 = kBN * (i < it.na ? i : i + it.skip);
+                    const int y = (blk * a.num_kv_heads + it.hk) * B;
+                    // ---- K
+                    int st = g % C::kSlots;
+                    ok = warp_all(mbar_wait(&bar[C::KV_EMPTY + st], ((g / C::kSlots) & 1) ^ 1, abort_flag, a.err));
+                    if (!ok) break;
+                    if (lane == 0) {
+                        mask_ring[tiles % kMaskRing] = have;
+                        mbar_arrive_expect_tx(&bar[C::KV_FULL + st], bytes);
+                    }
+                    __syncwarp();
+                    if (blk >= 0) {
+                        uint8_t *dst = smem + C::OFF_KV + st * C::kTileKV + lane * (B * 128);
+#pragma unroll
+                        for (int hf = 0; hf < C::kHalves; ++hf)
+                            tma_load_2d(dst + hf * C::kHalfKV, &tm_k, hf * 64, y, &bar[C::KV_FULL + st]);
+                    }
+                    ++g;
+                    ++tiles;
+                    // ---- Q, once the previous item's S products are complete
+                    if (j == 0) {
+                        if (k > 0) {
+                            ok = warp_all(mbar_wait(&bar[C::Q_EMPTY], (k - 1) & 1, abort_flag, a.err));
+                            if (!ok) break;
+                        }
+                        if (lane == 0) {
+                            const int nt = it.nk1 >= 0 ? 2 : 1;
+                            mbar_arrive_expect_tx(&bar[C::Q_FULL],
+                                                  static_cast<uint32_t>(nt * p.tpt * p.group * D * 2));
+                            for (int t = 0; t < nt; ++t)
+                                for (int hf = 0; hf < C::kHalves; ++hf)
+                                    tma_load_3d(smem + C::OFF_Q + t * C::kTileQ + hf * C::kHalfQ, &tm_q,
+                                                hf * 64, it.hk * p.group,
+                                                it.q_first + it.tok0 + t * p.tpt, &bar[C::Q_FULL]);
+                        }
+                        ++q_loads;
+                        __syncwarp();
+                    }
+                    // ---- V
+                    st = g % C::kSlots;
+                    ok = warp_all(mbar_wait(&bar[C::KV_EMPTY + st], ((g / C::kSlots) & 1) ^ 1, abort_flag, a.err));
+                    if (!ok) break;
+                    uint8_t *vt = smem + C::OFF_KV + st * C::kTileKV;
+                    auto clear_row = [&](int r) {
+                        for (int c = lane; c < C::kHalves * 8; c += 32)
+                            *reinterpret_cast<uint4 *>(vt + (c / 8) * C::kHalfKV + r * 128 + (c % 8) * 16) =
+                                make_uint4(0, 0, 0, 0);
+                    };
+                    const unsigned full = boxes == 32 ? 0xffffffffu : (1u << boxes) - 1;
+                    if (have != full) {   // blocks that are not loaded: cleared up front
+                        for (int r = 0; r < kBN; ++r)
+                            if (!((have >> (r / B)) & 1)) clear_row(r);
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                    }
+                    // rows of the context's last block past its end are cleared
+                    // once the copies have landed
+                    const int tail = it.ctx - k0;          // valid rows, if < kBN
+                    const bool land = tail < kBN && tail % B != 0 && ((have >> (tail / B)) & 1);
+                    uint64_t *vbar = land ? &bar[C::V_LAND] : &bar[C::KV_FULL + st];
+                    if (lane == 0) mbar_arrive_expect_tx(vbar, bytes);
+                    __syncwarp();
+                    if (blk >= 0) {
+#pragma unroll
+                        for (int hf = 0; hf < C::kHalves; ++hf)
+                            tma_load_2d(vt + hf * C::kHalfKV + lane * (B * 128), &tm_v, hf * 64, y, vbar);
+                    }
+                    ++g;
+                    if (land) {
+                        ok = warp_all(mbar_wait(&bar[C::V_LAND], lands & 1, abort_flag, a.err));
+                        if (!ok) {
+                            mbar_wait_drain(&bar[C::V_LAND], lands & 1);
+                            --g;   // nothing signals this slot's FULL barrier
+                            break;
+                        }
+                        ++lands;
+                        for (int r = tail; r < (tail / B + 1) * B; ++r) clear_row(r);
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bar[C::KV_FULL + st]);
+                    }
+                    blk = next;
+                }
+                if (!ok) break;
+                ++k;
+            }
+            if (lane == 0) {
+                if (!ok) {   // let every copy already issued land
+                    if (q_loads > 0) mbar_wait_drain(&bar[C::Q_FULL], (q_loads - 1) & 1);
+                    for (uint32_t i = g > C::kSlots ? g - C::kSlots : 0; i < g; ++i)
+                        mbar_wait_drain(&bar[C::KV_FULL + i % C::kSlots], (i / C::kSlots) & 1);
+                }
+                __threadfence();
+                if (atomicAdd(a.counters + 1, 1u) == gridDim.x - 1) {
+                    atomicExch(a.counters, 0u);
+                    atomicExch(a.counters + 1, 0u);
+                }
+            }
+            __syncwarp();
+        } else if (warp == kMmaWarp0 || warp == kMmaWarp0 + 1) {
+            // -------------------------------------------------------- products
+            if (lane == 0) {
+                const int t = warp - kMmaWarp0;
+                constexpr uint32_t idesc_s = instr_desc(kBf16, false, kBN);
+                constexpr uint32_t idesc_pv = instr_desc(kBf16, true, D);
+                const uint32_t q_addr = smem_addr(smem + C::OFF_Q) + t * C::kTileQ;
+                const uint32_t kv_addr = smem_addr(smem + C::OFF_KV);
+                const uint32_t tm_s = tmem + t * kBN, tm_o = tmem + kTmemO + t * D;
+                uint32_t g = 0;        // first slot of the item
+                uint32_t n = 0;        // key tiles of this query tile, over all items
+                bool ok = true;
+                auto wait_slot = [&](uint32_t i) {
+                    return mbar_wait(&bar[C::KV_FULL + i % C::kSlots], (i / C::kSlots) & 1, abort_flag, a.err);
+                };
+                for (int k = 0; ok; ++k) {
+                    const int slot = k % 2;
+                    ok = mbar_wait(&bar[C::ITEM_FULL + slot], (k / 2) & 1, abort_flag, a.err);
+                    if (!ok) break;
+                    const volatile Item *it = items + slot;
+                    const bool done = it->done;
+                    const int nkt = it->nkt, nk = max(0, t == 0 ? it->nk0 : it->nk1);
+                    mbar_arrive(&bar[C::ITEM_EMPTY + slot]);
+                    if (done) break;
+                    ok = mbar_wait(&bar[C::Q_FULL], k & 1, abort_flag, a.err);
+                    if (!ok) break;
+                    if (nk == 0) mbar_arrive(&bar[C::Q_EMPTY]);
+                    for (int j = 0; j < nkt; ++j, g += 2) {
+                        if (j >= nk) {   // not this tile's: hand both slots back
+                            ok = wait_slot(g);
+                            if (!ok) break;
+                            mbar_arrive(&bar[C::KV_EMPTY + g % C::kSlots]);
+                            ok = wait_slot(g + 1);
+                            if (!ok) break;
+                            mbar_arrive(&bar[C::KV_EMPTY + (g + 1) % C::kSlots]);
+                            continue;
+                        }
+                        // S of key tile j, once P V of the tile before is complete
+                        if (n > 0) ok = mbar_wait(&bar[C::PV_DONE + t], (n - 1) & 1, abort_flag, a.err);
+                        ok = ok && wait_slot(g);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t ka = kv_addr + (g % C::kSlots) * C::kTileKV;
+#pragma unroll
+                        for (int ks = 0; ks < D / 16; ++ks) {
+                            const int half = ks / 4, kk = ks % 4;
+                            mma_ss(tm_s, smem_desc(q_addr + half * C::kHalfQ + kk * 32, 16, 1024),
+                                   smem_desc(ka + half * C::kHalfKV + kk * 32, 16, 1024), idesc_s, ks > 0);
+                        }
+                        mma_commit(&bar[C::S_FULL + t]);
+                        mma_commit(&bar[C::KV_EMPTY + g % C::kSlots]);
+                        if (j == nk - 1) mma_commit(&bar[C::Q_EMPTY]);
+                        // O += P V
+                        ok = wait_slot(g + 1) && mbar_wait(&bar[C::P_FULL + t], n & 1, abort_flag, a.err);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t va = kv_addr + ((g + 1) % C::kSlots) * C::kTileKV;
+#pragma unroll
+                        for (int ks = 0; ks < kBN / 16; ++ks)
+                            mma_ts(tm_o, tm_s + ks * 8, smem_desc(va + ks * 2048, C::kHalfKV, 1024),
+                                   idesc_pv, j > 0 || ks > 0);
+                        mma_commit(&bar[C::PV_DONE + t]);
+                        mma_commit(&bar[C::KV_EMPTY + (g + 1) % C::kSlots]);
+                        ++n;
+                    }
+                }
+                mma_commit(&bar[C::MMA_DONE + t]);
+                mbar_wait_drain(&bar[C::MMA_DONE + t], 0);
+            }
+            __syncwarp();
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+        // ------------------------------------------------------------ softmax
+        const int t = warp / 4;
+        const int r = (warp % 4) * 32 + lane;
+        const int tok = r / p.group, head = r - tok * p.group;   // within the tile
+        const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp % 4) * 32) << 16);
+        const uint32_t s_col = lane_base + t * kBN;
+        const uint32_t o_col = lane_base + kTmemO + t * D;
+        const float c = p.scale_log2;
+        const bool plain = !kCap && !kAlibi && c > 0.f;   // the scale goes into the exponent's FMA
+        const float cm = plain ? c : 1.f;
+        const unsigned full = B == 8 ? 0xffffu : (B == 16 ? 0xffu : 0xfu);
+        uint32_t n = 0;            // S tiles consumed
+        uint32_t tiles = 0;        // key tiles of all items (mask ring)
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+            const int slot = k % 2;
+            ok = warp_all(mbar_wait(&bar[C::ITEM_FULL + slot], (k / 2) & 1, abort_flag, a.err));
+            if (!ok) break;
+            // the slot stays held until the item's rows are written, so that its
+            // fields can be read when they are needed
+            const volatile Item *it = items + slot;
+            const bool done = it->done;
+            const int nk = t == 0 ? it->nk0 : it->nk1;
+            if (done) break;
+            const uint32_t tile_base = tiles;
+            tiles += it->nkt;
+            if (nk < 0) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar[C::ITEM_EMPTY + slot]);
+                continue;
+            }
+            // the row's position, -1 for a row without a query
+            const int pos = tok < min(p.tpt, it->q_len - it->tok0 - t * p.tpt)
+                                ? it->first_pos + t * p.tpt + tok
+                                : -1;
+            const int pre_all = it->pre, na = it->na, skip = it->skip, j0 = it->j0;
+            // positions of the warp's rows, for tiles that need no mask
+            const int wmin = __reduce_min_sync(0xffffffffu, pos);
+            const int wmax = __reduce_max_sync(0xffffffffu, pos);
+            float slope = 0.f;
+            if constexpr (kAlibi)
+                slope = pos >= 0 ? __ldg(a.alibi_slopes + it->hk * p.group + head) * 1.4426950408889634f : 0.f;
+            float m = -INFINITY, l = 0.f;
+            for (int j = 0; j < nk; ++j, ++n) {
+                ok = warp_all(mbar_wait(&bar[C::S_FULL + t], n & 1, abort_flag, a.err));
+                if (!ok) break;
+                tc_fence_after();
+                const int k0 = kBN * (j0 + j < na ? j0 + j : j0 + j + skip);
+                float x[kBN];
+                {
+                    uint32_t u[kBN];
+#pragma unroll
+                    for (int q = 0; q < kBN / 32; ++q)
+                        tmem_ld32_nowait(s_col + q * 32, *reinterpret_cast<uint32_t(*)[32]>(&u[q * 32]));
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < kBN; ++e) x[e] = __uint_as_float(u[e]);
+                }
+                if constexpr (kCap) {
+#pragma unroll
+                    for (int e = 0; e < kBN; ++e)
+                        x[e] = p.cap_log2 - 2.f * p.cap_log2 * fast_rcp(1.f + fast_exp2(x[e] * p.cap_in));
+                } else if (!plain) {
+#pragma unroll
+                    for (int e = 0; e < kBN; ++e) x[e] *= c;
+                }
+                if constexpr (kAlibi) {
+                    const float d0 = static_cast<float>(pos - k0);
+#pragma unroll
+                    for (int e = 0; e < kBN; ++e) x[e] -= slope * fabsf(d0 - static_cast<float>(e));
+                }
+                const unsigned have = mask_ring[(tile_base + j) % kMaskRing];
+                const bool all_visible = have == full &&
+                                         (k0 + kBN <= pre_all ? wmin >= 0
+                                                             : k0 + kBN - 1 <= wmin &&
+                                                                   (a.window == 0 || k0 > wmax - a.window));
+                if (!all_visible) {
+                    // one bit per key: keys before pr, and from lw up to h (none
+                    // for a row without a query), in blocks that are there
+                    const int h = pos + 1 - k0, pr = pos < 0 ? 0 : pre_all - k0;
+                    const int lw = a.window > 0 ? h - a.window : 0;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t vis = bits_below(pr - 32 * q) |
+                                       (bits_below(h - 32 * q) & ~bits_below(lw - 32 * q));
+                        if (have != full) vis &= present(have, q, B);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            x[32 * q + e] = (vis >> e) & 1 ? x[32 * q + e] : -INFINITY;
+                    }
+                }
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int e = 0; e < kBN; e += 8)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) mx[q] = max3(mx[q], x[e + 2 * q], x[e + 2 * q + 1]);
+                const float top = max3(mx[0], mx[1], fmaxf(mx[2], mx[3])) * cm;
+                const bool raise = top > m + kRaise;
+                if (__any_sync(0xffffffffu, raise)) {
+                    const float m_new = raise ? top : m;
+                    const float alpha = m == m_new ? 1.f : fast_exp2(m - m_new);
+                    m = m_new;
+                    l *= alpha;
+                    if (j > 0) {   // O holds complete products: S waited for them
+#pragma unroll 1
+                        for (int q = 0; q < D / 16; ++q) {
+                            uint32_t ov[16];
+                            tmem_ld16_nowait(o_col + q * 16, ov);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+                            tmem_st16(o_col + q * 16, ov);
+                        }
+                    }
+                }
+                const float bias = m == -INFINITY ? 0.f : kBias - m;
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int q = 0; q < kBN / 32; ++q) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        float *y = x + q * 32 + e;
+                        fma2(y[0], y[1], y[0], y[1], cm, cm, bias, bias);
+                        fma2(y[2], y[3], y[2], y[3], cm, cm, bias, bias);
+                        y[0] = fast_exp2(y[0]);
+                        y[1] = fast_exp2(y[1]);
+                        y[2] = fast_exp2(y[2]);
+                        y[3] = fast_exp2(y[3]);
+                        add2(sum[0], sum[1], sum[0], sum[1], y[0], y[1]);
+                        add2(sum[2], sum[3], sum[2], sum[3], y[2], y[3]);
+                        w[e / 2] = pack_pair<kBf16>(y[0], y[1]);
+                        w[e / 2 + 1] = pack_pair<kBf16>(y[2], y[3]);
+                    }
+                    tmem_st16(s_col + q * 16, w);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar[C::P_FULL + t]);
+            }
+            if (!ok) break;
+            if (nk > 0) {
+                ok = warp_all(mbar_wait(&bar[C::PV_DONE + t], (n - 1) & 1, abort_flag, a.err));
+                if (!ok) break;
+                tc_fence_after();
+            }
+            const bool live = pos >= 0;
+            uint16_t *dst = a.out + (static_cast<size_t>(it->q_first + it->tok0 + t * p.tpt + tok) * a.num_q_heads +
+                                     it->hk * p.group + head) * D;
+            const int splits = it->splits;
+            if (splits == 1) {
+                const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+                for (int q = 0; q < D / 32; ++q) {
+                    uint32_t ov[32];
+                    tmem_ld32_nowait(o_col + q * 32, ov);
+                    tmem_ld_wait();
+                    if (live) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
+                            uint4 v;
+                            uint32_t *u = reinterpret_cast<uint32_t *>(&v);
+#pragma unroll
+                            for (int z = 0; z < 4; ++z)
+                                u[z] = pack_pair<kBf16>(__uint_as_float(ov[e + 2 * z]) * inv,
+                                                        __uint_as_float(ov[e + 2 * z + 1]) * inv);
+                            *reinterpret_cast<uint4 *>(dst + q * 32 + e) = v;
+                        }
+                    }
+                }
+                tc_fence_before();
+            } else {
+                // a partial: [split][tile][D + 2][128 rows]
+                constexpr size_t kPart = static_cast<size_t>(D + 2) * kBM;
+                float *base = p.partials + (static_cast<size_t>(it->slot) * p.splits * 2 + t) * kPart + r;
+                float *mine = base + static_cast<size_t>(it->split) * 2 * kPart;
+#pragma unroll
+                for (int q = 0; q < D / 32; ++q) {
+                    uint32_t ov[32];
+                    tmem_ld32_nowait(o_col + q * 32, ov);
+                    tmem_ld_wait();
+                    if (live) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            mine[(q * 32 + e) * kBM] = nk > 0 ? __uint_as_float(ov[e]) : 0.f;
+                    }
+                }
+                tc_fence_before();
+                if (live) {
+                    mine[D * kBM] = m;
+                    mine[(D + 1) * kBM] = l;
+                }
+                // the warp's 32 rows are joined by the warp of the last split
+                __threadfence();
+                __syncwarp();
+                uint32_t last = 0;
+                if (lane == 0) {
+                    uint32_t *ticket = a.counters + 2 + it->slot * 8 + warp;
+                    last = atomicAdd(ticket, 1u) == static_cast<uint32_t>(splits - 1);
+                    if (last) atomicExch(ticket, 0u);
+                }
+                last = __shfl_sync(0xffffffffu, last, 0);
+                if (last && live) {
+                    __threadfence();
+                    float top = -INFINITY;
+                    for (int z = 0; z < splits; ++z)
+                        top = fmaxf(top, __ldcg(base + static_cast<size_t>(z) * 2 * kPart + D * kBM));
+                    float total = 0.f;
+                    for (int z = 0; z < splits; ++z) {
+                        const float *src = base + static_cast<size_t>(z) * 2 * kPart;
+                        const float mz = __ldcg(src + D * kBM);
+                        total += (mz == -INFINITY ? 0.f : fast_exp2(mz - top)) * __ldcg(src + (D + 1) * kBM);
+                    }
+                    const float inv = total > 0.f ? 1.f / total : 0.f;
+                    for (int q = 0; q < D / 16; ++q) {
+                        float acc[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) acc[e] = 0.f;
+                        for (int z = 0; z < splits; ++z) {
+                            const float *src = base + static_cast<size_t>(z) * 2 * kPart;
+                            const float mz = __ldcg(src + D * kBM);
+                            const float f = mz == -INFINITY ? 0.f : fast_exp2(mz - top);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) acc[e] += f * __ldcg(src + (q * 16 + e) * kBM);
+                        }
+#pragma unroll
+                        for (int e = 0; e < 16; e += 8) {
+                            uint4 v;
+                            uint32_t *u = reinterpret_cast<uint32_t *>(&v);
+#pragma unroll
+                            for (int z = 0; z < 4; ++z)
+                                u[z] = pack_pair<kBf16>(acc[e + 2 * z] * inv, acc[e + 2 * z + 1] * inv);
+                            *reinterpret_cast<uint4 *>(dst + q * 16 + e) = v;
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[C::ITEM_EMPTY + slot]);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                     "r"(kTmemCols));
+}
+
+// Query tiles (pairs) and key splits of a call.
+struct Plan {
+    long long pairs, base;    // base: items without splits
+    int splits;
+};
+Plan make_plan(int num_seqs, int num_kv_heads, int group, int max_q) {
+    Plan pl;
+    const int tpt = kBM / group;
+    pl.pairs = (static_cast<long long>(max_q) + 2 * tpt - 1) / (2 * tpt);
+    pl.base = pl.pairs * num_seqs * num_kv_heads;
+    pl.splits = pl.base > 0 && pl.base < kSplitTarget ? static_cast<int>(kSplitTarget / pl.base) : 1;
+    return pl;
+}
+
+using Kernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, PrefillGroupedArgs);
+template <bool kBf16, int D>
+Kernel pick(bool cap, bool alibi) {
+    return cap ? (alibi ? prefill_grouped_kernel<kBf16, D, true, true> : prefill_grouped_kernel<kBf16, D, true, false>)
+               : (alibi ? prefill_grouped_kernel<kBf16, D, false, true> : prefill_grouped_kernel<kBf16, D, false, false>);
+}
+
+}  // namespace
+
+bool prefill_grouped_supported(int dtype, int head_dim, int block_size, int group) {
+    return decode_variant_supported(dtype, head_dim, block_size) && head_dim != 256 && group <= kBM;
+}
+
+size_t prefill_grouped_workspace_bytes(int num_seqs, int num_kv_heads, int group, int head_dim,
+                                       int max_query_len) {
+    const Plan pl = make_plan(num_seqs, num_kv_heads, group, max_query_len);
+    if (pl.splits <= 1) return 0;
+    return static_cast<size_t>(pl.base) * pl.splits * 2 * (head_dim + 2) * kBM * sizeof(float);
+}
+
+size_t prefill_grouped_counters_bytes() { return (kCounters * 4 + 255) / 256 * 256; }
+
+cudaError_t launch_prefill_grouped(const GroupedArgs &args, int dtype, int head_dim, int num_sms,
+                                   cudaStream_t stream) {
+    const bool bf16 = dtype == PA_DTYPE_BF16;
+    const int Hk = args.num_kv_heads, Hq = args.num_q_heads, B = args.block_size, D = head_dim;
+    PrefillGroupedArgs p;
+    p.g = args;
+    const double log2e = 1.4426950408889634;
+    p.scale_log2 = static_cast<float>(args.scale * log2e);
+    p.cap_log2 = static_cast<float>(args.softcap * log2e);
+    p.cap_in = args.softcap > 0.f ? static_cast<float>(2.0 * args.scale / args.softcap * log2e) : 0.f;
+    p.group = Hq / Hk;
+    p.tpt = kBM / p.group;
+    const Plan pl = make_plan(args.num_seqs, Hk, p.group, args.max_q);
+    const long long items = pl.base * pl.splits;
+    // the queue head runs past the end by at most one per CTA
+    if (items > 0x7fffffffLL - 4096) return cudaErrorInvalidConfiguration;
+    p.num_pairs = static_cast<int>(pl.pairs);
+    p.splits = pl.splits;
+    p.num_items = static_cast<int>(items);
+    p.partials = static_cast<float *>(args.workspace);
+
+    CUtensorMap tm_q, tm_k, tm_v;
+    const cuuint64_t q_dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(Hq),
+                                  static_cast<cuuint64_t>(args.total_q)};
+    const cuuint64_t q_strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(Hq) * D * 2};
+    const cuuint32_t q_box[3] = {64, static_cast<cuuint32_t>(p.group), static_cast<cuuint32_t>(p.tpt)};
+    const cuuint64_t kv_dims[2] = {static_cast<cuuint64_t>(D),
+                                   static_cast<cuuint64_t>(args.num_blocks) * Hk * B};
+    const cuuint64_t kv_strides[1] = {static_cast<cuuint64_t>(D) * 2};
+    const cuuint32_t kv_box[2] = {64, static_cast<cuuint32_t>(B)};
+    if (!encode(&tm_q, bf16, args.q, 3, q_dims, q_strides, q_box) ||
+        !encode(&tm_k, bf16, args.k_cache, 2, kv_dims, kv_strides, kv_box) ||
+        !encode(&tm_v, bf16, args.v_cache, 2, kv_dims, kv_strides, kv_box))
+        return cudaErrorInvalidValue;
+    const bool cap = args.softcap > 0.f, alibi = args.alibi_slopes != nullptr;
+    const Kernel kernel = bf16 ? (D == 64 ? pick<true, 64>(cap, alibi) : pick<true, 128>(cap, alibi))
+                               : (D == 64 ? pick<false, 64>(cap, alibi) : pick<false, 128>(cap, alibi));
+    const int smem = D == 64 ? Cfg<64>::kSmemBytes : Cfg<128>::kSmemBytes;
+    cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel),
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(items < num_sms ? items : num_sms));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    void *params[] = {&tm_q, &tm_k, &tm_v, &p};
+    return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void *>(kernel), params);
+}
+
+}  // namespace pa
