@@ -23,7 +23,7 @@
 //    per context) joins all of them, in order, so the result does not depend
 //    on which came last.
 //  * No roles: each warp owns a ring of stages and is its own producer.  It
-//    takes every 4th tile of its CTA's piece, waits for the tile's TMA boxes,
+//    takes the next tile of its CTA's piece, waits for the tile's TMA boxes,
 //    computes, and refills the stage it just read; the table entry of the
 //    refill was loaded one tile earlier.  Warps meet only where a context
 //    ends, to merge their (max, sum, output) through shared memory, while
@@ -58,6 +58,10 @@ constexpr int kW = 4;                  // warps per CTA
 constexpr int kThreads = kW * 32;
 constexpr int kChunks = 512;           // entries of the CTA's prefix over the sequences
 constexpr int kMaxCtas = 640;          // bounds the partial slots (2 per CTA)
+#ifndef PA_DG_COST
+#define PA_DG_COST 4
+#endif
+constexpr int kUnitCost = PA_DG_COST;
 constexpr float kRaise = 8.f;
 constexpr float kBias = 6.f;           // weights are 2^(x - m + 6)
 
@@ -140,8 +144,10 @@ __device__ __forceinline__ uint32_t pack_pair(float a, float b) {
 
 // A sequence's visible keys as tiles of TK keys: tile i covers keys from
 // TK * (i < na ? i : i + skip); [lo, ctx) and [0, pre) are visible.
+// `len` is what a unit takes of the line: its tiles, and what its end costs a
+// CTA (merging the warps, a partial's ticket; 1.5 us), in tiles' time.
 struct Geo {
-    int ctx, lo, pre, na, skip, nt;
+    int ctx, lo, pre, na, skip, nt, len;
 };
 template <int TK>
 __device__ __forceinline__ Geo make_geo(const GroupedArgs &a, int ctx, int pre_raw) {
@@ -157,6 +163,7 @@ __device__ __forceinline__ Geo make_geo(const GroupedArgs &a, int ctx, int pre_r
         g.skip = first - g.na;
         g.nt = g.na + total - first;
     }
+    g.len = g.nt > 0 ? g.nt + kUnitCost : 0;
     return g;
 }
 
@@ -194,7 +201,7 @@ struct Cursor {
         for (;;) {
             if (s >= a.num_seqs) {
                 s = a.num_seqs;
-                g.nt = 0;
+                g.nt = g.len = 0;
                 return;
             }
             if ((s & ~31) != base) load_group(a, lane);
@@ -209,8 +216,8 @@ struct Cursor {
     }
     __device__ __forceinline__ void advance(const GroupedArgs &a, int units, int by, int lane) {
         idx += by;
-        while (idx >= g.nt && s < a.num_seqs) {
-            idx -= g.nt;
+        while (idx >= g.len && s < a.num_seqs) {
+            idx -= g.len;
             if (++unit == units) next_seq(a, lane);
         }
     }
@@ -223,17 +230,85 @@ struct Cfg {
     static constexpr int kHeads = 8 * NT;
     static constexpr int kMat = TK * D * 2;            // bytes of a K (or V) tile
     static constexpr int kStage = 2 * kMat;
+    
+#ifdef PA_STG
+    static constexpr int kStages = PA_STG;
+#else
     static constexpr int kStages = D == 64 ? 3 : 2;
+#endif
     static constexpr int kRow = D + 4;                 // floats of a merge row (no bank conflicts)
     static constexpr int OFF_O = kW * kStages * kStage;
     static constexpr int OFF_ML = OFF_O + kW * kHeads * kRow * 4;
     static constexpr int OFF_PREFIX = OFF_ML + kW * kHeads * 8;
-    static constexpr int OFF_BAR = OFF_PREFIX + (kChunks + 1) * 8;
-    static constexpr int OFF_MASK = OFF_BAR + kW * kStages * 8;
+    static constexpr int OFF_BAR = OFF_PREFIX + (kChunks + 1 + kW) * 8;
+    static constexpr int OFF_MASK = OFF_BAR + (kW * kStages + 1) * 8;   // rings, partial written
     static constexpr int OFF_FLAG = OFF_MASK + kW * kStages * 4;
     static constexpr int kBytes = OFF_FLAG + 16 + 1024;  // + alignment slack
     static constexpr int kCtasPerSm = 233472 / (kBytes + 1024) < 1 ? 1 : 233472 / (kBytes + 1024);
 };
+
+// Takes the ticket of a partial that the CTA left (one warp; the partial's
+// writes happen before the call at CTA scope): whether it was the unit's last.
+__device__ __forceinline__ bool take_ticket(const DecodeGroupedArgs &p, int s, int units, int unit,
+                                            int others, int lane) {
+    uint32_t last = 0;
+    if (lane == 0) {
+        uint32_t *ticket = p.g.counters + 2 + static_cast<size_t>(s) * units + unit;
+        __threadfence();   // the CTA's partial, ordered before its ticket
+        last = atomicAdd(ticket, 1u) == static_cast<uint32_t>(others);
+        if (last) atomicExch(ticket, 0u);
+    }
+    return __shfl_sync(0xffffffffu, last, 0) != 0;
+}
+
+// Joins the partials of a unit, which pieces i0 .. i1 left, and writes its
+// output rows.  tid of n threads.
+template <bool kBf16, int D, int kHeads>
+__device__ __forceinline__ void join_unit(const DecodeGroupedArgs &p, int s, int unit, int i0, int i1,
+                                          int tid, int n) {
+    constexpr int kVec = D / 4;
+    const GroupedArgs &a = p.g;
+    const int hk = unit / p.chunks, h0 = (unit % p.chunks) * kHeads;
+    const int heads = min(kHeads, p.group - h0);
+    // slot of piece i: 2 i + 1 for the one the unit starts in, else 2 i
+    auto part = [&](int i) {
+        return p.partials + static_cast<size_t>(2 * i + (i == i0 ? 1 : 0)) * (kHeads * (D + 2));
+    };
+    for (int i = tid; i < heads * kVec; i += n) {
+        const int h = i / kVec, d4 = i % kVec;
+        // batches of partials, each one round trip to L2
+        constexpr int kBatch = 8;
+        float top = -INFINITY, sum = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c0 = i0; c0 <= i1; c0 += kBatch) {
+            float2 w[kBatch];
+            float4 v[kBatch];
+#pragma unroll
+            for (int c = 0; c < kBatch; ++c) {
+                const float *src = part(min(c0 + c, i1));
+                w[c] = __ldcg(reinterpret_cast<const float2 *>(src + kHeads * D + 2 * h));
+                v[c] = __ldcg(reinterpret_cast<const float4 *>(src + h * D + d4 * 4));
+            }
+            float t2 = top;
+#pragma unroll
+            for (int c = 0; c < kBatch; ++c) t2 = fmaxf(t2, w[c].x);
+            const float f0_ = top == -INFINITY ? 0.f : fast_exp2(top - t2);
+            sum *= f0_, acc.x *= f0_, acc.y *= f0_, acc.z *= f0_, acc.w *= f0_;
+            top = t2;
+#pragma unroll
+            for (int c = 0; c < kBatch; ++c) {
+                const float f = w[c].x == -INFINITY || c0 + c > i1 ? 0.f : fast_exp2(w[c].x - top);
+                sum += f * w[c].y;
+                acc.x += f * v[c].x, acc.y += f * v[c].y, acc.z += f * v[c].z, acc.w += f * v[c].w;
+            }
+        }
+        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        uint2 r = make_uint2(pack_pair<kBf16>(acc.x * inv, acc.y * inv),
+                             pack_pair<kBf16>(acc.z * inv, acc.w * inv));
+        *reinterpret_cast<uint2 *>(
+            a.out + (static_cast<size_t>(s) * a.num_q_heads + hk * p.group + h0 + h) * D + d4 * 4) = r;
+    }
+}
 
 template <bool kBf16, int D, int NT, bool kDup>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -249,10 +324,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     float *obuf = reinterpret_cast<float *>(smem + C::OFF_O);
     float2 *ml = reinterpret_cast<float2 *>(smem + C::OFF_ML);
     long long *prefix = reinterpret_cast<long long *>(smem + C::OFF_PREFIX);
+    long long *warp_sum = prefix + kChunks + 1;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_FLAG);
     volatile int *last_flag = abort_flag + 1;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     uint64_t *bar = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR) + warp * C::kStages;
+    uint64_t *part_bar = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR) + kW * C::kStages;
     volatile uint32_t *stage_mask =
         reinterpret_cast<volatile uint32_t *>(smem + C::OFF_MASK) + warp * C::kStages;
     uint8_t *ring = smem + warp * C::kStages * C::kStage;
@@ -261,84 +338,106 @@ __global__ void __launch_bounds__(kThreads, 1)
         *abort_flag = 0;
         uint64_t *all = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
         for (int i = 0; i < kW * C::kStages; ++i) mbar_init(&all[i], 1);
+        mbar_init(&all[kW * C::kStages], kW);
         mbar_init_fence();
     }
     allow_dependents_to_launch();
     grid_dependency_wait();
 
     const int units = a.num_kv_heads * p.chunks;
-    // prefix[c]: tiles of the sequences before chunk c, all units
-    {
+    // rows of sequences without keys are zero; bad lengths are reported
+    auto zero_rows = [&]() {
+        for (int s = blockIdx.x; s < a.num_seqs; s += gridDim.x) {
+            const int c = __ldg(a.context_lens + s);
+            if (c > 0 && c <= a.max_blocks_per_seq * a.block_size) continue;
+            if (c != 0 && threadIdx.x == 0) atomicOr(a.err, PA_DEVERR_CONTEXT);
+            uint4 *dst = reinterpret_cast<uint4 *>(a.out + static_cast<size_t>(s) * a.num_q_heads * D);
+            for (int i = threadIdx.x; i < a.num_q_heads * (D / 8); i += kThreads)
+                dst[i] = make_uint4(0, 0, 0, 0);
+        }
+    };
+
+    // The line's length, and prefix[c], the tiles of the sequences before chunk
+    // c.  Up to 32 sequences need no prefix: a warp's lanes hold them.
+    Cursor<TK> cons;
+    cons.base = -1;
+    const bool small = a.num_seqs <= 32;
+    long long total;
+    if (small) {
+        cons.s = 0;
+        cons.load_group(a, lane);
+        total = static_cast<long long>(make_geo<TK>(a, cons.ctx_l, cons.pre_l).len) * units;
+#pragma unroll
+        for (int o = 16; o > 0; o /= 2) total += __shfl_xor_sync(0xffffffffu, total, o);
+        __syncthreads();                              // the barriers are set up
+    } else {
+        constexpr int kPer = kChunks / kThreads;      // neighbouring entries per thread
         const int nchunks = (a.num_seqs + (1 << p.chunk_shift) - 1) >> p.chunk_shift;
-        for (int c = threadIdx.x; c < kChunks; c += kThreads) {
+        long long v[kPer], sum = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int c = threadIdx.x * kPer + i;
             long long n = 0;
             if (c < nchunks) {
                 const int s0 = c << p.chunk_shift;
                 const int s1 = min(a.num_seqs, (c + 1) << p.chunk_shift);
                 for (int s = s0; s < s1; ++s)
-                    n += make_geo<TK>(a, load_ctx(a, s), load_pre(a, s)).nt;
+                    n += make_geo<TK>(a, load_ctx(a, s), load_pre(a, s)).len;
             }
-            prefix[c + 1] = n * units;
+            v[i] = n * units;
         }
-        __syncthreads();
-        if (warp == 0) {
-            constexpr int kPer = kChunks / 32;
-            long long v[kPer], sum = 0;
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                sum += prefix[lane * kPer + i + 1];
-                v[i] = sum;
-            }
-            long long run = sum;
-#pragma unroll
-            for (int o = 1; o < 32; o *= 2) {
-                const long long t = __shfl_up_sync(0xffffffffu, run, o);
-                if (lane >= o) run += t;
-            }
-            run -= sum;
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) prefix[lane * kPer + i + 1] = run + v[i];
-            if (lane == 0) prefix[0] = 0;
+        for (int i = 0; i < kPer; ++i) {
+            sum += v[i];
+            v[i] = sum;
         }
+        long long run = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+            const long long t = __shfl_up_sync(0xffffffffu, run, o);
+            if (lane >= o) run += t;
+        }
+        if (lane == 31) warp_sum[warp] = run;
         __syncthreads();
-    }
-    const long long total = prefix[kChunks];
-
-    // rows of sequences without keys are zero; bad lengths are reported
-    for (int s = blockIdx.x; s < a.num_seqs; s += gridDim.x) {
-        const int c = __ldg(a.context_lens + s);
-        if (c > 0 && c <= a.max_blocks_per_seq * a.block_size) continue;
-        if (c != 0 && threadIdx.x == 0) atomicOr(a.err, PA_DEVERR_CONTEXT);
-        uint4 *row = reinterpret_cast<uint4 *>(a.out + static_cast<size_t>(s) * a.num_q_heads * D);
-        for (int i = threadIdx.x; i < a.num_q_heads * (D / 8); i += kThreads)
-            row[i] = make_uint4(0, 0, 0, 0);
+        run -= sum;
+        for (int w = 0; w < warp; ++w) run += warp_sum[w];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) prefix[threadIdx.x * kPer + i + 1] = run + v[i];
+        if (threadIdx.x == 0) prefix[0] = 0;
+        __syncthreads();
+        total = prefix[kChunks];
     }
 
     // Equal pieces.  Few tiles go to fewer CTAs: a context of n tiles is not
     // cut finer than about sqrt(n / 2) tiles, where one CTA's streaming of a
     // piece and its joining of the other pieces' partials take equally long.
-    long long ctas = gridDim.x;
-    {
-        const float mean = static_cast<float>(total) / (static_cast<float>(a.num_seqs) * units);
-        const int least = max(kW, static_cast<int>(sqrtf(mean * 0.5f)));
-        ctas = min(ctas, (total + least - 1) / least);
+    const float mean = static_cast<float>(total) / (static_cast<float>(a.num_seqs) * units);
+    const int least = max(kW, static_cast<int>(sqrtf(mean * 0.5f)));
+    const long long ctas = min(static_cast<long long>(gridDim.x), (total + least - 1) / least);
+    if (blockIdx.x >= ctas) {
+        zero_rows();
+        return;
     }
-    if (blockIdx.x >= ctas) return;
     const long long f0 = blockIdx.x * total / ctas, f1 = (blockIdx.x + 1) * total / ctas;
     const int mine = static_cast<int>(f1 - f0);       // tiles of this CTA
 
-    // the CTA's start: its prefix entry, then its sequence within the entry
-    Cursor<TK> cons;
+    // the piece's start: its prefix entry, then its sequence within the entry
     {
-        int below = 0;
-        for (int c = lane; c < kChunks; c += 32) below += prefix[c + 1] <= f0;
-        const int c = __reduce_add_sync(0xffffffffu, below);
-        long long r = f0 - prefix[c];
-        cons.s = c << p.chunk_shift;
+        long long r = f0;
+        int s = 0;
+        if (!small) {
+            int below = 0;
+            for (int c = lane; c < kChunks; c += 32) below += prefix[c + 1] <= f0;
+            const int c = __reduce_add_sync(0xffffffffu, below);
+            r -= prefix[c];
+            s = c << p.chunk_shift;
+        }
         for (;;) {
-            cons.load_group(a, lane);
-            const int first = cons.s & 31;
-            long long n = lane >= first ? static_cast<long long>(make_geo<TK>(a, cons.ctx_l, cons.pre_l).nt) * units : 0;
+            cons.s = s;
+            if ((s & ~31) != cons.base) cons.load_group(a, lane);
+            const long long n = lane >= (s & 31)
+                                    ? static_cast<long long>(make_geo<TK>(a, cons.ctx_l, cons.pre_l).len) * units
+                                    : 0;
             long long run = n;
 #pragma unroll
             for (int o = 1; o < 32; o *= 2) {
@@ -351,13 +450,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 r -= __shfl_sync(0xffffffffu, run - n, l);
                 cons.s = cons.base + l;
                 cons.set_geo(a);
-                cons.unit = static_cast<int>(r / cons.g.nt);
-                cons.idx = static_cast<int>(r % cons.g.nt);
+                cons.unit = static_cast<int>(r / cons.g.len);
+                cons.idx = static_cast<int>(r - static_cast<long long>(cons.unit) * cons.g.len);
                 break;
             }
             r -= __shfl_sync(0xffffffffu, run, 31);
-            cons.s = cons.base + 32;
-            if (cons.s >= a.num_seqs) return;   // cannot happen: f0 < total
+            s = cons.base + 32;
+            if (s >= a.num_seqs) return;   // cannot happen: f0 < total
         }
     }
 
@@ -369,14 +468,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int rb_shift = B == 8 ? 3 : 4;
     const int boxes = TK / RB;
     Cursor<TK> prod = cons;
-    prod.advance(a, units, warp, lane);
-    int issue_t = warp;                      // the CTA tile the next issue is for
-    // the lane's box of the tile at `prod`: physical block (-1: not needed,
-    // -2: needed but its entry is bad) and row within the block
+    int at = 0;                              // tile of the piece `prod` is at
+    // the lane's box of tile `at`: physical block (-1: not needed, -2: needed
+    // but its entry is bad) and row within the block
     int box_blk = -1, box_row = 0;
-    auto look_up = [&]() {
+    auto look_up = [&](int tile) {           // moves to the warp's first tile from `tile` on
+        while (tile < mine) {
+            prod.advance(a, units, tile - at, lane);
+            at = tile;
+            if (prod.idx < prod.g.nt) break;
+            tile += kW;
+        }
+        at = tile;
         box_blk = -1;
-        if (lane < boxes && issue_t < mine) {
+        if (lane < boxes && tile < mine) {
             const int i = prod.idx;
             const int k = TK * (i < prod.g.na ? i : i + prod.g.skip) + lane * RB;
             if (k < prod.g.ctx && (k < prod.g.pre || k + RB > prod.g.lo)) {
@@ -386,34 +491,40 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     };
-    auto issue = [&](int stage) {
+    auto issue = [&](int stage, int blk, int box_y, int unit) {
         // every lane has read the stage's last tile (the caller's __syncwarp)
-        if (box_blk == -2) atomicOr(a.err, PA_DEVERR_TABLE);
-        const unsigned have = __ballot_sync(0xffffffffu, box_blk >= 0);
+        if (blk == -2) atomicOr(a.err, PA_DEVERR_TABLE);
+        const unsigned have = __ballot_sync(0xffffffffu, blk >= 0);
         if (lane == 0) {
             stage_mask[stage] = have;
             mbar_arrive_expect_tx(&bar[stage], __popc(have) * 2u * RB * D * 2u);
         }
         __syncwarp();
-        if (box_blk >= 0) {
-            const int hk = prod.unit / p.chunks;
-            const int y = (box_blk * a.num_kv_heads + hk) * B + box_row;
+        if (blk >= 0) {
+            const int y = (blk * a.num_kv_heads + unit / p.chunks) * B + box_y;
             uint8_t *dst = ring + stage * C::kStage + lane * (RB * D * 2);
             tma_load_3d(dst, &tm_k, 0, y, 0, &bar[stage]);
             tma_load_3d(dst + C::kMat, &tm_v, 0, y, 0, &bar[stage]);
         }
-        issue_t += kW;
-        if (issue_t < mine) prod.advance(a, units, kW, lane);
     };
+    int queue[C::kStages];                   // tiles issued and not yet taken
     int issued = 0;
+    {
+        int blk[C::kStages], y[C::kStages], un[C::kStages];
 #pragma unroll
-    for (int st = 0; st < C::kStages; ++st)
-        if (issue_t < mine) {
-            look_up();
-            issue(st);
-            ++issued;
+        for (int st = 0; st < C::kStages; ++st) {   // all entries before the first wait
+            look_up(st == 0 ? warp : at + kW);
+            queue[st] = at;
+            blk[st] = box_blk, y[st] = box_row, un[st] = prod.unit;
         }
-    look_up();
+#pragma unroll
+        for (int st = 0; st < C::kStages; ++st)
+            if (queue[st] < mine) {
+                issue(st, blk[st], y[st], un[st]);
+                ++issued;
+            }
+    }
+    look_up(at + kW);
 
     // ---------------------------------------------------------- consumer side
     // shared-memory layout of 16 keys: [D / 64 halves][16 rows][128 bytes],
@@ -433,7 +544,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t qf[KS][NT][2];
     float m[NT][2], l[NT][2], o[KS][NT][4], slope[NT][2];
     bool ok = true;
-    int t = warp;                            // next tile of this warp
     int n_done = 0;                          // tiles taken
     int seg_start = 0;                       // CTA tile at which the segment starts
 
@@ -463,8 +573,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     load_q();
     while (seg_start < mine) {
         const Geo g = cons.g;
-        const int seg_len = min(g.nt - cons.idx, mine - seg_start);
+        const int seg_len = min(g.len - cons.idx, mine - seg_start);
         const int idx0 = cons.idx;
+        if (idx0 >= g.nt) {   // the piece starts past the unit's tiles
+            seg_start += seg_len;
+            cons.idx += seg_len;
+            if (seg_start < mine) {
+                cons.advance(a, units, 0, lane);
+                load_q();
+            }
+            continue;
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             m[nt][0] = m[nt][1] = -INFINITY;
@@ -474,7 +593,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[ks][nt][e] = 0.f;
         }
-        for (; t < seg_start + seg_len; t += kW) {
+        while (queue[0] < seg_start + seg_len) {
+            const int t = queue[0];
+#pragma unroll
+            for (int i = 0; i + 1 < C::kStages; ++i) queue[i] = queue[i + 1];
+            queue[C::kStages - 1] = 0x7fffffff;
             const int st = n_done % C::kStages;
             const uint32_t ph = (n_done / C::kStages) & 1;
             ++n_done;
@@ -620,10 +743,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             else
                 pv(std::false_type{});
             __syncwarp();
-            if (issue_t < mine) {
-                issue(st);
+            if (at < mine) {
+                issue(st, box_blk, box_row, prod.unit);
                 ++issued;
-                look_up();
+                queue[C::kStages - 1] = at;
+                look_up(at + kW);
             }
         }
 
@@ -632,7 +756,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int hk = unit / p.chunks, h0 = (unit % p.chunks) * kHeads;
         const int heads = min(kHeads, p.group - h0);
         // the unit's place on the line, and whether this piece covers it whole
-        const bool from_start = idx0 == 0, to_end = idx0 + seg_len == g.nt;
+        const bool from_start = idx0 == 0, to_end = idx0 + seg_len >= g.nt;
         const long long u0 = f0 + seg_start - idx0, u1 = u0 + g.nt;   // its tiles
         // the next unit's q is loaded while this one is merged
         seg_start += seg_len;
@@ -701,47 +825,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             // pieces that hold part of the unit: the CTAs of its first and last tile
             const int i0 = static_cast<int>(((u0 + 1) * ctas - 1) / total);
             const int i1 = static_cast<int>((u1 * ctas - 1) / total);
-            __threadfence();
-            __syncthreads();
-            uint32_t *ticket = a.counters + static_cast<size_t>(s) * units + unit;
-            if (threadIdx.x == 0) {
-                const bool last = atomicAdd(ticket, 1u) == static_cast<uint32_t>(i1 - i0);
-                if (last) atomicExch(ticket, 0u);
-                *last_flag = last;
-            }
-            __syncthreads();
-            if (*last_flag) {
-                __threadfence();
-                // slot of piece i: 2 i + 1 for the one the unit starts in, else 2 i
-                auto part = [&](int i) {
-                    return p.partials + static_cast<size_t>(2 * i + (i == i0 ? 1 : 0)) * (kHeads * (D + 2));
-                };
-                for (int i = threadIdx.x; i < heads * kVec; i += kThreads) {
-                    const int h = i / kVec, d4 = i % kVec;
-                    float top = -INFINITY;
-#pragma unroll 8
-                    for (int c = i0; c <= i1; ++c)
-                        top = fmaxf(top, __ldcg(part(c) + kHeads * D + 2 * h));
-                    float sum = 0.f;
-                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-                    for (int c = i0; c <= i1; ++c) {
-                        const float *src = part(c);
-                        const float2 w = __ldcg(reinterpret_cast<const float2 *>(src + kHeads * D + 2 * h));
-                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(src + h * D + d4 * 4));
-                        const float f = w.x == -INFINITY ? 0.f : fast_exp2(w.x - top);
-                        sum += f * w.y;
-                        acc.x += f * v.x, acc.y += f * v.y, acc.z += f * v.z, acc.w += f * v.w;
+            if (seg_start < mine) {
+                // the warps go on; one of them sees to the ticket (a piece has at
+                // most one such segment, its first)
+                __syncwarp();
+                if (lane == 0) mbar_arrive(part_bar);
+                if (warp == kW - 1) {
+                    ok = ok && __all_sync(0xffffffffu, mbar_wait(part_bar, 0, abort_flag, a.err));
+                    if (ok && take_ticket(p, s, units, unit, i1 - i0, lane)) {
+                        __threadfence();
+                        join_unit<kBf16, D, kHeads>(p, s, unit, i0, i1, lane, 32);
                     }
-                    const float inv = sum > 0.f ? 1.f / sum : 0.f;
-                    uint2 r = make_uint2(pack_pair<kBf16>(acc.x * inv, acc.y * inv),
-                                         pack_pair<kBf16>(acc.z * inv, acc.w * inv));
-                    *reinterpret_cast<uint2 *>(
-                        a.out + (static_cast<size_t>(s) * a.num_q_heads + hk * p.group + h0 + h) * D + d4 * 4) = r;
                 }
+            } else {
+                __syncthreads();
+                if (warp == 0) {
+                    const bool last = take_ticket(p, s, units, unit, i1 - i0, lane);
+                    __threadfence();
+                    if (lane == 0) *last_flag = last;
+                }
+                __syncthreads();
+                if (*last_flag) join_unit<kBf16, D, kHeads>(p, s, unit, i0, i1, threadIdx.x, kThreads);
             }
         }
     }
+    zero_rows();
     if (!ok) {   // let every copy already issued land before the CTA leaves
         for (int i = max(0, issued - C::kStages); i < issued; ++i)
             mbar_wait_drain(&bar[i % C::kStages], (i / C::kStages) & 1);
