@@ -45,6 +45,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <mutex>
 #include <type_traits>
 
 #include "pa_device.cuh"
@@ -920,12 +921,23 @@ cudaError_t launch_decode_grouped(const GroupedArgs &args, int dtype, int head_d
     else
         v = head_dim == 64 ? variant_of<false, 64>(p.group)
                            : (head_dim == 128 ? variant_of<false, 128>(p.group) : variant_of<false, 256>(p.group));
+    // the kernel's shared-memory limit, once per device and variant
     int device = 0;
     cudaError_t e = cudaGetDevice(&device);
     if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(reinterpret_cast<const void *>(v.kernel),
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem);
-    if (e != cudaSuccess) return e;
+    if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
+    {
+        static std::mutex mu;
+        static bool ready[64][18] = {};
+        const int which = (bf16 ? 9 : 0) + (head_dim == 64 ? 0 : head_dim == 128 ? 3 : 6) + (p.group <= 4 ? 0 : p.group <= 8 ? 1 : 2);
+        std::lock_guard<std::mutex> lock(mu);
+        if (!ready[device][which]) {
+            e = cudaFuncSetAttribute(reinterpret_cast<const void *>(v.kernel),
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem);
+            if (e != cudaSuccess) return e;
+            ready[device][which] = true;
+        }
+    }
     const int ctas = v.ctas_per_sm * num_sms;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

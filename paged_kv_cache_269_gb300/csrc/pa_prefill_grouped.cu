@@ -46,6 +46,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <mutex>
+
 #include "pa_device.cuh"
 #include "pa_internal.h"
 #include "pa_tensor.cuh"
@@ -817,9 +819,23 @@ cudaError_t launch_prefill_grouped(const GroupedArgs &args, int dtype, int head_
     const Kernel kernel = bf16 ? (D == 64 ? pick<true, 64>(cap, alibi) : pick<true, 128>(cap, alibi))
                                : (D == 64 ? pick<false, 64>(cap, alibi) : pick<false, 128>(cap, alibi));
     const int smem = D == 64 ? Cfg<64>::kSmemBytes : Cfg<128>::kSmemBytes;
-    cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel),
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // the kernel's shared-memory limit, once per device and variant
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
     if (e != cudaSuccess) return e;
+    if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
+    {
+        static std::mutex mu;
+        static bool ready[64][16] = {};
+        const int which = (bf16 ? 8 : 0) + (D == 64 ? 0 : 4) + (cap ? 2 : 0) + (alibi ? 1 : 0);
+        std::lock_guard<std::mutex> lock(mu);
+        if (!ready[device][which]) {
+            e = cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel),
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (e != cudaSuccess) return e;
+            ready[device][which] = true;
+        }
+    }
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;

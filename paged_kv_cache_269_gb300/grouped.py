@@ -15,6 +15,20 @@ be used by two calls at once.
 from __future__ import annotations
 
 import ctypes
+import functools
+
+torch = Tensor = _I32 = _F32 = _U8 = _raw_stream = _package = None
+
+
+def _init():
+    """Imports what the calls need, at the first one (the package itself, with
+    its block manager, works without torch)."""
+    global torch, Tensor, _I32, _F32, _U8, _raw_stream, _package
+    import torch as torch_
+    import paged_kv_cache_269_gb300 as package
+    torch, Tensor, _package = torch_, torch_.Tensor, package
+    _I32, _F32, _U8 = torch.int32, torch.float32, torch.uint8
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 class AttnOpts(ctypes.Structure):
@@ -43,8 +57,52 @@ def declare(l, dims_p):
 
 
 def _pa():
-    import paged_kv_cache_269_gb300 as pa
-    return pa
+    if _package is None:
+        _init()
+    return _package
+
+
+# The checks below are made on every call, so they touch each tensor as little
+# as they can; one that fails is left to _need, which says what is wrong.
+def _plain(t, name, dtype, ndim, index, device):
+    """Checks a contiguous tensor on the given device; returns its pointer."""
+    if not (isinstance(t, Tensor) and t.dtype is dtype and t.dim() == ndim and t.get_device() == index
+            and t.is_contiguous()):
+        _pa()._need(t, name, dtype, ndim, device)
+    return t.data_ptr()
+
+
+def _caches(k_cache, v_cache):
+    """Checks the caches; returns (device index, device, dtype code, dtype, shape)."""
+    pa = _pa()
+    if not isinstance(k_cache, Tensor):
+        raise TypeError("k_cache must be a torch.Tensor")
+    code, et = pa._element_dtype(k_cache), k_cache.dtype
+    index = k_cache.get_device()
+    if index < 0 or k_cache.dim() != 4 or not k_cache.is_contiguous():
+        pa._need(k_cache, "k_cache", et, 4)
+    device = k_cache.device
+    _plain(v_cache, "v_cache", et, 4, index, device)
+    shape = k_cache.shape
+    if v_cache.shape != shape:
+        raise ValueError("k_cache and v_cache must have one shape")
+    return index, device, code, et, shape
+
+
+# What the library needs for given sizes (pure functions of them).
+@functools.lru_cache(maxsize=4096)
+def _decode_needs(S, Hq, H, D, B, code):
+    pa, l = _pa(), _pa().lib()
+    d = ctypes.byref(pa.Dims(S, H, D, B, 1, code))
+    return l.pa_decode_grouped_workspace_bytes(d, Hq), l.pa_decode_grouped_counters_bytes(d, Hq)
+
+
+@functools.lru_cache(maxsize=4096)
+def _prefill_needs(S, Hq, H, D, B, code, max_query_len):
+    pa, l = _pa(), _pa().lib()
+    d = ctypes.byref(pa.Dims(S, H, D, B, 1, code))
+    return (l.pa_prefill_grouped_workspace_bytes(d, Hq, max_query_len),
+            l.pa_prefill_grouped_counters_bytes(d, Hq))
 
 
 def rope_table(max_positions, rotary_dim, base=10000.0, inv_freq=None, device=None):
@@ -53,7 +111,7 @@ def rope_table(max_positions, rotary_dim, base=10000.0, inv_freq=None, device=No
     f_i = base^(-2 i / rotary_dim) or the given inv_freq [rotary_dim / 2].
     Angles are taken in 64 bits, so far positions keep their phase.  Made once,
     when a model is loaded."""
-    import torch
+    _pa()
     if rotary_dim <= 0 or rotary_dim % 2:
         raise ValueError("rotary_dim must be even and positive")
     half = rotary_dim // 2
@@ -67,25 +125,27 @@ def rope_table(max_positions, rotary_dim, base=10000.0, inv_freq=None, device=No
     return torch.cat([angle.cos(), angle.sin()], 1).to(torch.float32).contiguous()
 
 
-def _rows(t, name, dtype, device, heads, dim):
+def _rows(t, name, dtype, index, device, heads, dim):
     """Checks a [T, heads, dim] tensor whose rows may be apart (a slice of a
-    packed projection); returns the elements between one row and the next."""
-    import torch
-    if not isinstance(t, torch.Tensor):
+    packed projection); returns its pointer, its shape and the elements between
+    one row and the next."""
+    if not isinstance(t, Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[2] != dim or (heads is not None and t.shape[1] != heads):
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != dim or (heads is not None and shape[1] != heads):
         raise ValueError(f"{name} must have shape [T, {'H' if heads is None else heads}, {dim}], "
-                         f"got {tuple(t.shape)}")
-    if not t.is_cuda or t.device != device:
+                         f"got {tuple(shape)}")
+    if t.get_device() != index:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != dim):
+    stride = t.stride()
+    if stride[2] != 1 or (shape[1] > 1 and stride[1] != dim):
         raise ValueError(f"{name}: the heads of a row must be adjacent and contiguous")
-    stride = t.stride(0) if t.shape[0] > 1 else t.shape[1] * dim
-    if stride % 8:
+    step = stride[0] if shape[0] > 1 else shape[1] * dim
+    if step % 8:
         raise ValueError(f"{name}: rows must start on 16-byte boundaries")
-    return stride
+    return t.data_ptr(), shape, step
 
 
 def rope_and_cache(q_out, q, k, v, k_cache, v_cache, positions, cos_sin, slot_mapping,
@@ -100,57 +160,49 @@ def rope_and_cache(q_out, q, k, v, k_cache, v_cache, positions, cos_sin, slot_ma
     of 16 up to D.  interleaved pairs dims (2 i, 2 i + 1) instead of
     (i, i + rotary_dim / 2).  slot < 0 skips the token's k and v, a negative
     position the whole token."""
-    import torch
     pa = _pa()
-    pa._element_dtype(k_cache)
-    et = k_cache.dtype
-    pa._need(k_cache, "k_cache", et, 4)
-    dev = k_cache.device
-    pa._need(v_cache, "v_cache", et, 4, dev)
-    N, H, B, D = k_cache.shape
-    if v_cache.shape != k_cache.shape:
-        raise ValueError("rope_and_cache: inconsistent cache shapes")
-    qs = _rows(q, "q", et, dev, None, D)
-    Hq, T = q.shape[1], q.shape[0]
-    os_ = _rows(q_out, "q_out", et, dev, Hq, D)
-    ks, vs = _rows(k, "k", et, dev, H, D), _rows(v, "v", et, dev, H, D)
-    pa._need(positions, "positions", torch.int32, 1, dev)
-    pa._need(slot_mapping, "slot_mapping", torch.int32, 1, dev)
-    pa._need(cos_sin, "cos_sin", torch.float32, 2, dev)
-    if any(t.shape[0] != T for t in (q_out, k, v, positions, slot_mapping)):
+    index, dev, code, et, (N, H, B, D) = _caches(k_cache, v_cache)
+    if torch.cuda.current_device() != index:
+        with torch.cuda.device(index):
+            return rope_and_cache(q_out, q, k, v, k_cache, v_cache, positions, cos_sin, slot_mapping,
+                                  interleaved, stream)
+    q_p, (T, Hq, _), qs = _rows(q, "q", et, index, dev, None, D)
+    o_p, o_shape, os_ = _rows(q_out, "q_out", et, index, dev, Hq, D)
+    k_p, k_shape, ks = _rows(k, "k", et, index, dev, H, D)
+    v_p, v_shape, vs = _rows(v, "v", et, index, dev, H, D)
+    pos_p = _plain(positions, "positions", _I32, 1, index, dev)
+    slot_p = _plain(slot_mapping, "slot_mapping", _I32, 1, index, dev)
+    cs_p = _plain(cos_sin, "cos_sin", _F32, 2, index, dev)
+    if not (o_shape[0] == k_shape[0] == v_shape[0] == positions.shape[0] == slot_mapping.shape[0] == T):
         raise ValueError("rope_and_cache: inconsistent numbers of tokens")
     if T > 1 and os_ < Hq * D:
         raise ValueError("q_out: rows overlap")
     if T:
-        _refuse_overlap(q_out, os_, q, qs, "q", T, D, same_ok=True)
-        _refuse_overlap(q_out, os_, k, ks, "k", T, D)
-        _refuse_overlap(q_out, os_, v, vs, "v", T, D)
-    dims = pa._cache_dims(k_cache)
-    sh, _ = pa._stream_handle(dev, stream)
-    with torch.cuda.device(dev):
-        rc = pa.lib().pa_rope_and_cache(
-            pa._ptr(q_out), pa._ptr(q), pa._ptr(k), pa._ptr(v), pa._ptr(k_cache), pa._ptr(v_cache),
-            pa._ptr(positions), pa._ptr(cos_sin), pa._ptr(slot_mapping), T, Hq, qs, ks, vs, os_,
-            cos_sin.shape[1], cos_sin.shape[0], 1 if interleaved else 0, ctypes.byref(dims), sh)
-    pa._check(rc, "pa_rope_and_cache")
+        row, kv_row = Hq * D, H * D
+        if o_p != q_p or (os_ != qs and T > 1):
+            _refuse_overlap(o_p, os_, row, q_p, qs, row, T, "q")
+        _refuse_overlap(o_p, os_, row, k_p, ks, kv_row, T, "k")
+        _refuse_overlap(o_p, os_, row, v_p, vs, kv_row, T, "v")
+    max_positions, rotary_dim = cos_sin.shape
+    rc = pa.lib().pa_rope_and_cache(
+        o_p, q_p, k_p, v_p, k_cache.data_ptr(), v_cache.data_ptr(), pos_p, cs_p, slot_p, T, Hq, qs, ks,
+        vs, os_, rotary_dim, max_positions, 1 if interleaved else 0, ctypes.byref(pa.Dims(0, H, D, B, N, code)),
+        _raw_stream(index) if stream is None else stream.cuda_stream)
+    if rc:
+        pa._check(rc, "pa_rope_and_cache")
     return q_out
 
 
-def _refuse_overlap(out, out_stride, x, x_stride, name, T, D, same_ok=False):
-    """Refuses an input that shares elements with q_out (q itself excepted).
-    Slices of one packed tensor that interleave without sharing are fine."""
-    size = 2
-    a0, a_row = out.data_ptr(), out.shape[1] * D * size
-    b0, b_row = x.data_ptr(), x.shape[1] * D * size
-    if same_ok and a0 == b0 and (out_stride == x_stride or T == 1):
+def _refuse_overlap(a0, a_step, a_row, b0, b_step, b_row, T, name):
+    """Refuses an input of T rows at b0 that shares elements with q_out at a0
+    (pointers in bytes; steps and rows in elements of 2 bytes).  Slices of one
+    packed tensor that interleave without sharing are fine."""
+    if a0 + 2 * ((T - 1) * a_step + a_row) <= b0 or b0 + 2 * ((T - 1) * b_step + b_row) <= a0:
         return
-    a1, b1 = a0 + (T - 1) * out_stride * size + a_row, b0 + (T - 1) * x_stride * size + b_row
-    if a1 <= b0 or b1 <= a0:
-        return
-    if out_stride == x_stride and T > 1:
-        # rows of one stride: apart iff the offset leaves room on both sides
-        off = (b0 - a0) % (out_stride * size)
-        if off >= a_row and off + b_row <= out_stride * size:
+    if a_step == b_step and T > 1:
+        # rows of one step: apart iff the offset leaves room on both sides
+        off = (b0 - a0) % (2 * a_step)
+        if off >= 2 * a_row and off + 2 * b_row <= 2 * a_step:
             return
     raise ValueError(f"q_out overlaps {name}")
 
@@ -160,77 +212,85 @@ def _refuse_overlap(out, out_stride, x, x_stride, name, T, D, same_ok=False):
 _buffers: dict = {}
 
 
-def _buffers_for(device, stream, counters_bytes, workspace_bytes):
-    import torch
+def _buffers_for(index, stream, counters_bytes, workspace_bytes):
     pa = _pa()
-    with torch.cuda.stream(stream):
-        if torch.cuda.is_current_stream_capturing():
-            return (torch.zeros(counters_bytes // 4, dtype=torch.int32, device=device),
-                    torch.empty(max(workspace_bytes, 16), dtype=torch.uint8, device=device))
-        key = (device.index, stream.cuda_stream)
+    if stream is None:
+        capturing = torch.cuda.is_current_stream_capturing()
+        key = (index, _raw_stream(index))
+    else:
+        with torch.cuda.stream(stream):
+            capturing = torch.cuda.is_current_stream_capturing()
+        key = (index, stream.cuda_stream)
+    if not capturing:
+        got = _buffers.get(key)
+        if got is not None and got[2] >= counters_bytes and got[3] >= workspace_bytes:
+            return got[:2]
+    with torch.cuda.stream(stream):          # no change where stream is None
+        if capturing:
+            return (torch.zeros(counters_bytes // 4, dtype=_I32, device=index),
+                    torch.empty(max(workspace_bytes, 16), dtype=_U8, device=index))
         with pa._buf_lock:
-            ctr, ws = _buffers.get(key, (None, None))
-            if ctr is None or ctr.numel() * 4 < counters_bytes:
-                ctr = torch.zeros(max(counters_bytes, 1 << 14) // 4, dtype=torch.int32, device=device)
-            if ws is None or ws.numel() < workspace_bytes:
-                ws = torch.empty(max(workspace_bytes, 16), dtype=torch.uint8, device=device)
-            _buffers[key] = (ctr, ws)
+            ctr, ws, nc, nw = _buffers.get(key, (None, None, 0, 0))
+            if nc < counters_bytes:
+                nc = max(counters_bytes, 1 << 14)
+                ctr = torch.zeros(nc // 4, dtype=_I32, device=index)
+            if ws is None or nw < workspace_bytes:
+                nw = max(workspace_bytes, 16)
+                ws = torch.empty(nw, dtype=_U8, device=index)
+            _buffers[key] = (ctr, ws, nc, nw)
             return ctr, ws
 
 
 def reset_counters():
     """Zero every cached counter buffer (needed after a device error)."""
     with _pa()._buf_lock:
-        for ctr, _ in _buffers.values():
-            ctr.zero_()
+        for got in _buffers.values():
+            got[0].zero_()
 
 
 def _attention_args(what, out, q, k_cache, v_cache, block_tables, context_lens, softcap,
                     alibi_slopes, window, prefix_lens):
-    import torch
-    pa = _pa()
-    pa._element_dtype(k_cache)
-    et = k_cache.dtype
-    pa._need(k_cache, "k_cache", et, 4)
-    dev = k_cache.device
-    pa._need(v_cache, "v_cache", et, 4, dev)
-    pa._need(q, "q", et, 3, dev)
-    pa._need(out, "out", et, 3, dev)
-    pa._need(block_tables, "block_tables", torch.int32, 2, dev)
-    pa._need(context_lens, "context_lens", torch.int32, 1, dev)
-    S, Hq = context_lens.shape[0], q.shape[1]
-    H, D = k_cache.shape[1], k_cache.shape[3]
-    if v_cache.shape != k_cache.shape or out.shape != q.shape or q.shape[2] != D \
-            or block_tables.shape[0] != S:
+    index, dev, code, et, (N, H, B, D) = _caches(k_cache, v_cache)
+    q_p = _plain(q, "q", et, 3, index, dev)
+    o_p = _plain(out, "out", et, 3, index, dev)
+    t_p = _plain(block_tables, "block_tables", _I32, 2, index, dev)
+    l_p = _plain(context_lens, "context_lens", _I32, 1, index, dev)
+    shape = q.shape
+    Hq, (S, MB) = shape[1], block_tables.shape
+    if out.shape != shape or shape[2] != D or context_lens.shape[0] != S:
         raise ValueError(f"{what}: inconsistent shapes")
     if H == 0 or Hq == 0 or Hq % H:
         raise ValueError(f"{what}: query heads must be a multiple of the cache's heads")
-    if alibi_slopes is not None:
-        pa._need(alibi_slopes, "alibi_slopes", torch.float32, 1, dev)
-        if alibi_slopes.shape[0] != Hq:
-            raise ValueError(f"{what}: alibi_slopes must have one entry per query head")
-    if prefix_lens is not None:
-        pa._need(prefix_lens, "prefix_lens", torch.int32, 1, dev)
-        if prefix_lens.shape[0] != S:
-            raise ValueError(f"{what}: prefix_lens must have one entry per sequence")
-    opts = AttnOpts(float(softcap or 0.0), int(window or 0),
-                    None if alibi_slopes is None else alibi_slopes.data_ptr(),
-                    None if prefix_lens is None else prefix_lens.data_ptr())
-    return dev, S, Hq, pa._cache_dims(k_cache, S), opts
+    opts = None
+    if softcap or window or alibi_slopes is not None or prefix_lens is not None:
+        a_p = x_p = None
+        if alibi_slopes is not None:
+            a_p = _plain(alibi_slopes, "alibi_slopes", _F32, 1, index, dev)
+            if alibi_slopes.shape[0] != Hq:
+                raise ValueError(f"{what}: alibi_slopes must have one entry per query head")
+        if prefix_lens is not None:
+            x_p = _plain(prefix_lens, "prefix_lens", _I32, 1, index, dev)
+            if prefix_lens.shape[0] != S:
+                raise ValueError(f"{what}: prefix_lens must have one entry per sequence")
+        opts = ctypes.byref(AttnOpts(float(softcap or 0.0), int(window or 0), a_p, x_p))
+    head = (o_p, q_p, k_cache.data_ptr(), v_cache.data_ptr(), t_p, l_p)
+    return index, dev, S, Hq, (H, D, B, code), MB, shape[0], head, _pa().Dims(S, H, D, B, N, code), opts
 
 
-def _pick_buffers(dev, st, need_ctr, need_ws, counters, workspace):
-    import torch
-    pa = _pa()
+def _pick_buffers(index, dev, stream, need_ctr, need_ws, counters, workspace):
+    """(workspace pointer, bytes, counters pointer, bytes): the caller's, or
+    the cached ones."""
     if counters is None or (workspace is None and need_ws):
-        c2, w2 = _buffers_for(dev, st, need_ctr, need_ws)
-        counters = c2 if counters is None else counters
-        workspace = w2 if workspace is None else workspace
-    pa._need(counters, "counters", torch.int32, 1, dev)
-    if workspace is not None:
-        pa._need(workspace, "workspace", torch.uint8, 1, dev)
-    ws_ptr = pa._ptr(workspace) if workspace is not None else ctypes.c_void_p(0)
-    return counters, workspace, ws_ptr, workspace.numel() if workspace is not None else 0
+        c2, w2 = _buffers_for(index, stream, need_ctr, need_ws)
+        if counters is None:
+            counters = c2
+        if workspace is None:
+            workspace = w2
+    c_p = _plain(counters, "counters", _I32, 1, index, dev)
+    if workspace is None:
+        return None, 0, c_p, counters.numel() * 4
+    w_p = _plain(workspace, "workspace", _U8, 1, index, dev)
+    return w_p, workspace.numel(), c_p, counters.numel() * 4
 
 
 def decode_grouped_workspace_bytes(num_q_heads, num_kv_heads, head_dim, block_size) -> int:
@@ -287,27 +347,25 @@ def decode_grouped(out, q, k_cache, v_cache, block_tables, context_lens, scale, 
     own among them, and the first prefix_lens[s] (int32 [S]).  workspace
     (uint8) and counters (zeroed int32): see the _bytes functions; by default
     cached per stream, or taken from the graph's pool inside a capture."""
-    import torch
     pa = _pa()
-    dev, S, Hq, dims, opts = _attention_args("decode_grouped", out, q, k_cache, v_cache,
-                                             block_tables, context_lens, softcap, alibi_slopes,
-                                             window, prefix_lens)
-    if q.shape[0] != S:
+    index, dev, S, Hq, sizes, MB, rows, head, dims, opts = _attention_args(
+        "decode_grouped", out, q, k_cache, v_cache, block_tables, context_lens, softcap, alibi_slopes,
+        window, prefix_lens)
+    if rows != S:
         raise ValueError("decode_grouped: inconsistent shapes")
-    sh, st = pa._stream_handle(dev, stream)
-    l = pa.lib()
-    with torch.cuda.device(dev):
-        need_ws = l.pa_decode_grouped_workspace_bytes(ctypes.byref(dims), Hq)
-        need_ctr = l.pa_decode_grouped_counters_bytes(ctypes.byref(dims), Hq)
-        if need_ws == pa._SIZE_ERROR or need_ctr == 0:
-            raise pa.PaError(-3, "decode_grouped: unsupported head_dim or block_size")
-        counters, workspace, ws_ptr, ws_n = _pick_buffers(dev, st, need_ctr, need_ws, counters,
-                                                          workspace)
-        rc = l.pa_decode_grouped(pa._ptr(out), pa._ptr(q), pa._ptr(k_cache), pa._ptr(v_cache),
-                                 pa._ptr(block_tables), pa._ptr(context_lens), float(scale),
-                                 block_tables.shape[1], ctypes.byref(dims), Hq, ctypes.byref(opts),
-                                 ws_ptr, ws_n, pa._ptr(counters), counters.numel() * 4, sh)
-    pa._check(rc, "pa_decode_grouped")
+    if torch.cuda.current_device() != index:
+        with torch.cuda.device(index):
+            return decode_grouped(out, q, k_cache, v_cache, block_tables, context_lens, scale, softcap,
+                                  alibi_slopes, window, prefix_lens, workspace, counters, stream)
+    need_ws, need_ctr = _decode_needs(S, Hq, *sizes)
+    if need_ws == pa._SIZE_ERROR or need_ctr == 0:
+        raise pa.PaError(-3, "decode_grouped: unsupported head_dim or block_size")
+    w_p, w_n, c_p, c_n = _pick_buffers(index, dev, stream, need_ctr, need_ws, counters, workspace)
+    rc = pa.lib().pa_decode_grouped(
+        *head, float(scale), MB, ctypes.byref(dims), Hq, opts, w_p, w_n, c_p, c_n,
+        _raw_stream(index) if stream is None else stream.cuda_stream)
+    if rc:
+        pa._check(rc, "pa_decode_grouped")
     return out
 
 
@@ -321,31 +379,29 @@ def prefill_grouped(out, q, k_cache, v_cache, block_tables, context_lens, query_
     every q_len_s (computed from query_start, with a device sync, when None).
     The rest as decode_grouped; a query at position p sees keys up to p, and
     the first prefix_lens[s] keys wherever it stands."""
-    import torch
     pa = _pa()
-    dev, S, Hq, dims, opts = _attention_args("prefill_grouped", out, q, k_cache, v_cache,
-                                             block_tables, context_lens, softcap, alibi_slopes,
-                                             window, prefix_lens)
-    pa._need(query_start, "query_start", torch.int32, 1, dev)
+    index, dev, S, Hq, sizes, MB, rows, head, dims, opts = _attention_args(
+        "prefill_grouped", out, q, k_cache, v_cache, block_tables, context_lens, softcap, alibi_slopes,
+        window, prefix_lens)
+    qs_p = _plain(query_start, "query_start", _I32, 1, index, dev)
     if query_start.shape[0] != S + 1:
         raise ValueError("prefill_grouped: inconsistent shapes")
+    if torch.cuda.current_device() != index:
+        with torch.cuda.device(index):
+            return prefill_grouped(out, q, k_cache, v_cache, block_tables, context_lens, query_start,
+                                   scale, max_query_len, softcap, alibi_slopes, window, prefix_lens,
+                                   workspace, counters, stream)
     if max_query_len is None:
         max_query_len = int((query_start[1:] - query_start[:-1]).max()) if S else 0
-    sh, st = pa._stream_handle(dev, stream)
-    l = pa.lib()
-    with torch.cuda.device(dev):
-        need_ws = l.pa_prefill_grouped_workspace_bytes(ctypes.byref(dims), Hq, int(max_query_len))
-        need_ctr = l.pa_prefill_grouped_counters_bytes(ctypes.byref(dims), Hq)
-        if need_ws == pa._SIZE_ERROR or need_ctr == 0:
-            raise pa.PaError(-3, "prefill_grouped: unsupported head_dim, block_size or heads, or "
-                                 "a negative max_query_len")
-        counters, workspace, ws_ptr, ws_n = _pick_buffers(dev, st, need_ctr, need_ws, counters,
-                                                          workspace)
-        rc = l.pa_prefill_grouped(pa._ptr(out), pa._ptr(q), pa._ptr(k_cache), pa._ptr(v_cache),
-                                  pa._ptr(block_tables), pa._ptr(context_lens),
-                                  pa._ptr(query_start), q.shape[0], int(max_query_len),
-                                  float(scale), block_tables.shape[1], ctypes.byref(dims), Hq,
-                                  ctypes.byref(opts), ws_ptr, ws_n, pa._ptr(counters),
-                                  counters.numel() * 4, sh)
-    pa._check(rc, "pa_prefill_grouped")
+    max_query_len = int(max_query_len)
+    need_ws, need_ctr = _prefill_needs(S, Hq, *sizes, max_query_len)
+    if need_ws == pa._SIZE_ERROR or need_ctr == 0:
+        raise pa.PaError(-3, "prefill_grouped: unsupported head_dim, block_size or heads, or "
+                             "a negative max_query_len")
+    w_p, w_n, c_p, c_n = _pick_buffers(index, dev, stream, need_ctr, need_ws, counters, workspace)
+    rc = pa.lib().pa_prefill_grouped(
+        *head, qs_p, rows, max_query_len, float(scale), MB, ctypes.byref(dims), Hq, opts, w_p, w_n, c_p,
+        c_n, _raw_stream(index) if stream is None else stream.cuda_stream)
+    if rc:
+        pa._check(rc, "pa_prefill_grouped")
     return out
