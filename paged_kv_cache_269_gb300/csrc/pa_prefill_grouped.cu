@@ -17,16 +17,26 @@
 //    and multiplied once for all heads that share them.  A work item is two
 //    such tiles, one K/V head, one sequence, and a range of key tiles.
 //  * Warp 8 (TMA) takes items from a queue, heaviest first, describes each to
-//    the other roles through a two-slot ring, and streams K and V tiles of 128
-//    keys (the blocks named by the table, as 64-dim x block boxes) through one
-//    ring of slots K0 V0 K1 V1 ...
-//  * Warps 9 and 10 issue the products of tile 0 and 1, one thread each:
-//    S = Q K^T into tensor memory; once the softmax has put P over S,
-//    O += P V (P read from tensor memory); once that is complete, the next S.
-//    While one tile's softmax works, the other tile's products run.
+//    the other roles through a two-slot ring, and streams K and V tiles (the
+//    blocks named by the table, as 64-dim x block boxes) through one ring of
+//    slots K0 V0 K1 V1 ...
+//  * Warps 9 and 10 issue the products of query tile 0 and 1, one thread each:
+//    S = Q K^T into tensor memory, one key tile ahead (as soon as the softmax
+//    has loaded the scores before it), and O += P V (P read from tensor
+//    memory) once the softmax has stored P.  S, P and O have columns of their
+//    own, so no product waits for another one's operands: with P over S (128
+//    keys a tile), S had to wait for P V, and a step of both tiles took 5000
+//    cycles, of which the tensor core worked 2600.
 //  * Warps 0-3 / 4-7 (softmax of tile 0 / 1): thread = row = tensor-memory
-//    lane.  Loads its 128 scores, takes the maximum, exponentiates, and stores
-//    the weights as 16-bit values over the scores.
+//    lane.  Loads its scores, takes the maximum, exponentiates, and stores the
+//    weights as 16-bit values.
+//  * Tensor memory is what sets the key tile: S, P and O of two query tiles in
+//    512 columns leave 64 keys for D = 128 (with two P buffers) and 128 keys
+//    for D = 64 (one).
+//  * tanh: an odd polynomial on the FMA pipe (degree 11, |u| <= 1, within
+//    5e-7), chosen per warp and tile by the largest |u|; beyond it, 1 - 2 /
+//    (1 + e^(2u)), whose two special-function operations per score cost 3400
+//    cycles per 128 keys where the polynomial costs 1300.
 //  * The weights are rounded to 16 bits (the element type) before P V, the sum
 //    is taken before the rounding, in fp32.  A weight is then off by half a
 //    step of the type, independently of its neighbours, so the output's error
@@ -37,7 +47,8 @@
 //  * Few rows over long contexts: an item's key tiles are split over several
 //    CTAs, which leave partial (max, sum, output) and take a ticket; the last
 //    one joins them in order.
-//  * Tensor memory: S/P of tile t at columns 128 t, O of tile t at 256 + D t.
+//  * The output rows go through a staging buffer in shared memory, so that a
+//    warp writes whole 128-byte lines (row by row they cost 6400 cycles an item).
 //  * Every wait is bounded; tensor memory is released on every path.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -56,7 +67,6 @@ namespace pa {
 namespace {
 
 constexpr int kBM = 128;               // rows per tile (MMA M)
-constexpr int kBN = 128;               // keys per tile
 constexpr int kThreads = 384;          // 2 x 4 softmax warps, TMA warp, 2 MMA warps, 1 idle
 constexpr int kTmaWarp = 8;
 constexpr int kMmaWarp0 = 9;
@@ -64,7 +74,6 @@ constexpr int kMmaWarp0 = 9;
 // registers up to the eight softmax warps: 2 x 216 + 72 = 3 x 168.
 constexpr int kRegsSoftmax = 216, kRegsOther = 72;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kTmemO = 256;
 constexpr float kRaise = 8.f;
 constexpr float kBias = 6.f;           // weights are 2^(x - m + 6): at most 2^14
 constexpr int kMaskRing = 16;
@@ -75,6 +84,8 @@ constexpr int kCounters = 2 + 8 * kSplitTarget;   // queue head, CTAs done, a ti
 struct PrefillGroupedArgs {
     GroupedArgs g;
     float scale_log2, cap_log2, cap_in;
+    float cap_v;                       // v = cap_v (q . k) has v^2 < 2 iff |s / cap| < 1
+    float tanh_k[6];                   // there, x = v (k0 + k1 v^2 + ... + k5 v^10)
     int group, tpt;                    // heads per K/V head; tokens per tile
     int num_pairs, splits;
     int num_items;                     // num_pairs * splits * S * Hkv
@@ -96,19 +107,28 @@ struct Item {
 
 template <int D>
 struct Cfg {
+    static constexpr int BN = D == 64 ? 128 : 64;  // keys per tile
+    static constexpr int NP = D == 64 ? 1 : 2;     // P buffers per query tile
     static constexpr int kHalves = D / 64;
     static constexpr int kHalfQ = kBM * 128;
     static constexpr int kTileQ = kHalves * kHalfQ;
-    static constexpr int kHalfKV = kBN * 128;
+    static constexpr int kHalfKV = BN * 128;
     static constexpr int kTileKV = kHalves * kHalfKV;
-    static constexpr int kSlots = D == 64 ? 10 : 5;
+    static constexpr int kSlots = 8;
+    // tensor-memory columns
+    static constexpr uint32_t TM_S = 0, TM_P = 2 * BN, TM_O = D == 64 ? 384 : 256;
+    static_assert(TM_P + 2 * NP * BN / 2 <= TM_O && TM_O + 2 * D <= kTmemCols, "tensor memory");
+    static constexpr int kStagingWarp = 32 * 128;  // 32 rows x 64 dims
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_KV = 2 * kTileQ;
-    static constexpr int OFF_BAR = OFF_KV + kSlots * kTileKV;
+    static constexpr int OFF_STAGING = OFF_KV + kSlots * kTileKV;
+    static constexpr int OFF_BAR = OFF_STAGING + 8 * kStagingWarp;
     static constexpr int Q_FULL = 0, Q_EMPTY = 1, V_LAND = 2;
-    static constexpr int S_FULL = 3, P_FULL = 5, PV_DONE = 7, MMA_DONE = 9;
-    static constexpr int ITEM_FULL = 11, ITEM_EMPTY = 13;
-    static constexpr int KV_FULL = 15, KV_EMPTY = KV_FULL + kSlots;
+    static constexpr int S_FULL = 3, S_EMPTY = 5;          // [tile]
+    static constexpr int P_FULL = 7, PV_DONE = 11;         // [tile][P buffer]
+    static constexpr int MMA_DONE = 15;
+    static constexpr int ITEM_FULL = 17, ITEM_EMPTY = 19;
+    static constexpr int KV_FULL = 21, KV_EMPTY = KV_FULL + kSlots;
     static constexpr int kNumBars = KV_EMPTY + kSlots;
     static constexpr int OFF_TMEM = OFF_BAR + kNumBars * 8;
     static constexpr int OFF_FLAG = OFF_TMEM + 4;
@@ -160,6 +180,7 @@ __device__ __forceinline__ bool warp_all(bool v) { return __all_sync(0xffffffffu
 // Work item w: (pair level, split, sequence, K/V head), latest pairs first.
 // False for an empty item, or for a sequence whose lengths are inconsistent
 // (reported once).
+template <int kBN>
 __device__ __forceinline__ bool item_geometry(const PrefillGroupedArgs &p, int w, bool report,
                                               Item &it) {
     const GroupedArgs &a = p.g;
@@ -191,7 +212,7 @@ __device__ __forceinline__ bool item_geometry(const PrefillGroupedArgs &p, int w
     it.ctx = ctx;
     it.pre = max(0, min(pre_raw, ctx));
     it.first_pos = ctx - q_len + tok0;
-    // keys: [0, pre) and [lo, up), as a list of 128-key tiles
+    // keys: [0, pre) and [lo, up), as a list of key tiles
     const int last_tok = min(tok0 + 2 * p.tpt, q_len) - 1;
     const int up = max(ctx - q_len + last_tok + 1, it.pre);
     const int lo = a.window > 0 ? max(0, it.first_pos - a.window + 1) : 0;
@@ -208,11 +229,12 @@ __device__ __forceinline__ bool item_geometry(const PrefillGroupedArgs &p, int w
     const int up0 = max(min(it.first_pos + p.tpt, ctx), it.pre);
     const int end0 = (up0 + kBN - 1) / kBN;
     const int need0 = min(count, end0 <= it.na ? end0 : max(it.na, end0 - it.skip));
-    // one split per about sqrt(count / 2) key tiles: there, streaming a part
-    // and joining the others' partials take about equally long
+    // one split per about sqrt(count / 2) tiles of 128 keys: there, streaming a
+    // part and joining the others' partials take about equally long
     int parts = 1;
     if (p.splits > 1) {
-        const int per = max(2, static_cast<int>(ceilf(sqrtf(0.5f * count))));
+        constexpr float kUnit = 128.f / kBN;
+        const int per = static_cast<int>(ceilf(kUnit * fmaxf(2.f, sqrtf(0.5f * count / kUnit))));
         parts = min(p.splits, (count + per - 1) / per);
     }
     if (split >= parts) return false;
@@ -234,6 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                            const __grid_constant__ CUtensorMap tm_v,
                            const __grid_constant__ PrefillGroupedArgs p) {
     using C = Cfg<D>;
+    constexpr int kBN = C::BN;
     const GroupedArgs &a = p.g;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -249,7 +272,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kNumBars; ++i) {
             uint32_t count = 1;
-            if (i == C::P_FULL || i == C::P_FULL + 1) count = 4;              // softmax warps
+            if (i >= C::S_EMPTY && i < C::S_EMPTY + 2) count = 4;             // softmax warps
+            if (i >= C::P_FULL && i < C::P_FULL + 4) count = 4;
             if (i == C::ITEM_EMPTY || i == C::ITEM_EMPTY + 1) count = 10;     // 2 MMA threads, 8 warps
             if (i == C::Q_EMPTY || i >= C::KV_EMPTY) count = 2;               // both MMA threads
             mbar_init(&bar[i], count);
@@ -287,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0) w = static_cast<int>(atomicAdd(a.counters, 1u));
                     w = __shfl_sync(0xffffffffu, w, 0);
                     if (static_cast<unsigned>(w) >= static_cast<unsigned>(p.num_items)) break;
-                    if (item_geometry(p, w, lane == 0, it)) break;
+                    if (item_geometry<kBN>(p, w, lane == 0, it)) break;
                 }
                 const bool done = static_cast<unsigned>(w) >= static_cast<unsigned>(p.num_items);
                 const int slot = k % 2;
@@ -428,12 +452,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                 constexpr uint32_t idesc_pv = instr_desc(kBf16, true, D);
                 const uint32_t q_addr = smem_addr(smem + C::OFF_Q) + t * C::kTileQ;
                 const uint32_t kv_addr = smem_addr(smem + C::OFF_KV);
-                const uint32_t tm_s = tmem + t * kBN, tm_o = tmem + kTmemO + t * D;
+                const uint32_t tm_s = tmem + C::TM_S + t * kBN, tm_o = tmem + C::TM_O + t * D;
+                const uint32_t tm_p = tmem + C::TM_P + t * (C::NP * kBN / 2);
                 uint32_t g = 0;        // first slot of the item
-                uint32_t n = 0;        // key tiles of this query tile, over all items
+                uint32_t ns = 0;       // S products of this query tile, over all items
+                uint32_t np = 0;       // P V products
                 bool ok = true;
                 auto wait_slot = [&](uint32_t i) {
                     return mbar_wait(&bar[C::KV_FULL + i % C::kSlots], (i / C::kSlots) & 1, abort_flag, a.err);
+                };
+                // S of the key tile in slot i, once the scores before it are loaded
+                auto issue_s = [&](uint32_t i, bool last) {
+                    if (!wait_slot(i)) return false;
+                    if (ns > 0 && !mbar_wait(&bar[C::S_EMPTY + t], (ns - 1) & 1, abort_flag, a.err)) return false;
+                    tc_fence_after();
+                    const uint32_t ka = kv_addr + (i % C::kSlots) * C::kTileKV;
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks) {
+                        const int half = ks / 4, kk = ks % 4;
+                        mma_ss(tm_s, smem_desc(q_addr + half * C::kHalfQ + kk * 32, 16, 1024),
+                               smem_desc(ka + half * C::kHalfKV + kk * 32, 16, 1024), idesc_s, ks > 0);
+                    }
+                    mma_commit(&bar[C::S_FULL + t]);
+                    mma_commit(&bar[C::KV_EMPTY + i % C::kSlots]);
+                    if (last) mma_commit(&bar[C::Q_EMPTY]);
+                    ++ns;
+                    return true;
                 };
                 for (int k = 0; ok; ++k) {
                     const int slot = k % 2;
@@ -447,7 +491,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = mbar_wait(&bar[C::Q_FULL], k & 1, abort_flag, a.err);
                     if (!ok) break;
                     if (nk == 0) mbar_arrive(&bar[C::Q_EMPTY]);
-                    for (int j = 0; j < nkt; ++j, g += 2) {
+                    if (nk > 0) ok = issue_s(g, nk == 1);
+                    for (int j = 0; j < nkt && ok; ++j, g += 2) {
                         if (j >= nk) {   // not this tile's: hand both slots back
                             ok = wait_slot(g);
                             if (!ok) break;
@@ -457,33 +502,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                             mbar_arrive(&bar[C::KV_EMPTY + (g + 1) % C::kSlots]);
                             continue;
                         }
-                        // S of key tile j, once P V of the tile before is complete
-                        if (n > 0) ok = mbar_wait(&bar[C::PV_DONE + t], (n - 1) & 1, abort_flag, a.err);
-                        ok = ok && wait_slot(g);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint32_t ka = kv_addr + (g % C::kSlots) * C::kTileKV;
-#pragma unroll
-                        for (int ks = 0; ks < D / 16; ++ks) {
-                            const int half = ks / 4, kk = ks % 4;
-                            mma_ss(tm_s, smem_desc(q_addr + half * C::kHalfQ + kk * 32, 16, 1024),
-                                   smem_desc(ka + half * C::kHalfKV + kk * 32, 16, 1024), idesc_s, ks > 0);
-                        }
-                        mma_commit(&bar[C::S_FULL + t]);
-                        mma_commit(&bar[C::KV_EMPTY + g % C::kSlots]);
-                        if (j == nk - 1) mma_commit(&bar[C::Q_EMPTY]);
+                        if (j + 1 < nk) ok = issue_s(g + 2, j + 2 == nk);
                         // O += P V
-                        ok = wait_slot(g + 1) && mbar_wait(&bar[C::P_FULL + t], n & 1, abort_flag, a.err);
+                        const uint32_t buf = np % C::NP;
+                        ok = ok && wait_slot(g + 1) &&
+                             mbar_wait(&bar[C::P_FULL + t * 2 + buf], (np / C::NP) & 1, abort_flag, a.err);
                         if (!ok) break;
                         tc_fence_after();
                         const uint32_t va = kv_addr + ((g + 1) % C::kSlots) * C::kTileKV;
 #pragma unroll
                         for (int ks = 0; ks < kBN / 16; ++ks)
-                            mma_ts(tm_o, tm_s + ks * 8, smem_desc(va + ks * 2048, C::kHalfKV, 1024),
-                                   idesc_pv, j > 0 || ks > 0);
-                        mma_commit(&bar[C::PV_DONE + t]);
+                            mma_ts(tm_o, tm_p + buf * (kBN / 2) + ks * 8,
+                                   smem_desc(va + ks * 2048, C::kHalfKV, 1024), idesc_pv, j > 0 || ks > 0);
+                        mma_commit(&bar[C::PV_DONE + t * 2 + buf]);
                         mma_commit(&bar[C::KV_EMPTY + (g + 1) % C::kSlots]);
-                        ++n;
+                        ++np;
                     }
                 }
                 mma_commit(&bar[C::MMA_DONE + t]);
@@ -498,12 +531,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r = (warp % 4) * 32 + lane;
         const int tok = r / p.group, head = r - tok * p.group;   // within the tile
         const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp % 4) * 32) << 16);
-        const uint32_t s_col = lane_base + t * kBN;
-        const uint32_t o_col = lane_base + kTmemO + t * D;
+        const uint32_t s_col = lane_base + C::TM_S + t * kBN;
+        const uint32_t p_col = lane_base + C::TM_P + t * (C::NP * kBN / 2);
+        const uint32_t o_col = lane_base + C::TM_O + t * D;
+        uint8_t *staging = smem + C::OFF_STAGING + warp * C::kStagingWarp;
         const float c = p.scale_log2;
         const bool plain = !kCap && !kAlibi && c > 0.f;   // the scale goes into the exponent's FMA
         const float cm = plain ? c : 1.f;
-        const unsigned full = B == 8 ? 0xffffu : (B == 16 ? 0xffu : 0xfu);
+        const unsigned full = (1u << (kBN / B)) - 1;
         uint32_t n = 0;            // S tiles consumed
         uint32_t tiles = 0;        // key tiles of all items (mask ring)
         bool ok = true;
@@ -551,10 +586,31 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int e = 0; e < kBN; ++e) x[e] = __uint_as_float(u[e]);
                 }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar[C::S_EMPTY + t]);   // the next S may be written
                 if constexpr (kCap) {
+                    // v^2 < 2 for every score iff no bit pattern reaches that of 2
+                    uint32_t any = 0;
+                    const float cv = p.cap_v;
 #pragma unroll
-                    for (int e = 0; e < kBN; ++e)
-                        x[e] = p.cap_log2 - 2.f * p.cap_log2 * fast_rcp(1.f + fast_exp2(x[e] * p.cap_in));
+                    for (int e = 0; e < kBN; ++e) any |= __float_as_uint((x[e] * cv) * (x[e] * cv));
+                    if (warp_all(any < 0x40000000u)) {
+#pragma unroll
+                        for (int e = 0; e < kBN; e += 2) {
+                            float v0, v1, w0, w1, y0 = p.tanh_k[5], y1 = y0;
+                            mul2(v0, v1, x[e], x[e + 1], cv, cv);
+                            mul2(w0, w1, v0, v1, v0, v1);
+#pragma unroll
+                            for (int c2 = 4; c2 >= 0; --c2)
+                                fma2(y0, y1, y0, y1, w0, w1, p.tanh_k[c2], p.tanh_k[c2]);
+                            mul2(x[e], x[e + 1], v0, v1, y0, y1);
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < kBN; ++e)
+                            x[e] = p.cap_log2 - 2.f * p.cap_log2 * fast_rcp(1.f + fast_exp2(x[e] * p.cap_in));
+                    }
                 } else if (!plain) {
 #pragma unroll
                     for (int e = 0; e < kBN; ++e) x[e] *= c;
@@ -575,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int h = pos + 1 - k0, pr = pos < 0 ? 0 : pre_all - k0;
                     const int lw = a.window > 0 ? h - a.window : 0;
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
+                    for (int q = 0; q < kBN / 32; ++q) {
                         uint32_t vis = bits_below(pr - 32 * q) |
                                        (bits_below(h - 32 * q) & ~bits_below(lw - 32 * q));
                         if (have != full) vis &= present(have, q, B);
@@ -584,19 +640,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                             x[32 * q + e] = (vis >> e) & 1 ? x[32 * q + e] : -INFINITY;
                     }
                 }
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                float mx[8];
 #pragma unroll
-                for (int e = 0; e < kBN; e += 8)
+                for (int q = 0; q < 8; ++q) mx[q] = fmaxf(x[q], x[q + 8]);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) mx[q] = max3(mx[q], x[e + 2 * q], x[e + 2 * q + 1]);
-                const float top = max3(mx[0], mx[1], fmaxf(mx[2], mx[3])) * cm;
+                for (int e = 16; e < kBN; e += 8)
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) mx[q] = fmaxf(mx[q], x[e + q]);
+                const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                                        fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * cm;
+                const uint32_t buf = n % C::NP;
+                // the P buffer's last product (and, in order, all before it)
+                if (n >= C::NP) {
+                    ok = warp_all(mbar_wait(&bar[C::PV_DONE + t * 2 + buf], (n / C::NP - 1) & 1, abort_flag, a.err));
+                    if (!ok) break;
+                    tc_fence_after();
+                }
                 const bool raise = top > m + kRaise;
                 if (__any_sync(0xffffffffu, raise)) {
                     const float m_new = raise ? top : m;
                     const float alpha = m == m_new ? 1.f : fast_exp2(m - m_new);
                     m = m_new;
                     l *= alpha;
-                    if (j > 0) {   // O holds complete products: S waited for them
+                    if (j > 0) {   // O, once the product before is complete
+                        const uint32_t pb = (n - 1) % C::NP;
+                        ok = warp_all(mbar_wait(&bar[C::PV_DONE + t * 2 + pb], ((n - 1) / C::NP) & 1, abort_flag, a.err));
+                        if (!ok) break;
+                        tc_fence_after();
 #pragma unroll 1
                         for (int q = 0; q < D / 16; ++q) {
                             uint32_t ov[16];
@@ -628,43 +698,57 @@ __global__ void __launch_bounds__(kThreads, 1)
                         w[e / 2] = pack_pair<kBf16>(y[0], y[1]);
                         w[e / 2 + 1] = pack_pair<kBf16>(y[2], y[3]);
                     }
-                    tmem_st16(s_col + q * 16, w);
+                    tmem_st16(p_col + buf * (kBN / 2) + q * 16, w);
                 }
                 l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar[C::P_FULL + t]);
+                if (lane == 0) mbar_arrive(&bar[C::P_FULL + t * 2 + buf]);
             }
             if (!ok) break;
             if (nk > 0) {
-                ok = warp_all(mbar_wait(&bar[C::PV_DONE + t], (n - 1) & 1, abort_flag, a.err));
+                ok = warp_all(mbar_wait(&bar[C::PV_DONE + t * 2 + (n - 1) % C::NP], ((n - 1) / C::NP) & 1, abort_flag,
+                                        a.err));
                 if (!ok) break;
                 tc_fence_after();
             }
             const bool live = pos >= 0;
-            uint16_t *dst = a.out + (static_cast<size_t>(it->q_first + it->tok0 + t * p.tpt + tok) * a.num_q_heads +
-                                     it->hk * p.group + head) * D;
             const int splits = it->splits;
             if (splits == 1) {
                 const float inv = l > 0.f ? 1.f / l : 0.f;
+                // rows of the tile's output, from its first token's first head
+                uint16_t *base = a.out + (static_cast<size_t>(it->q_first + it->tok0 + t * p.tpt) * a.num_q_heads +
+                                          it->hk * p.group) * D;
+                const int my_row = live ? tok * a.num_q_heads + head : -1;
 #pragma unroll
-                for (int q = 0; q < D / 32; ++q) {
-                    uint32_t ov[32];
-                    tmem_ld32_nowait(o_col + q * 32, ov);
-                    tmem_ld_wait();
-                    if (live) {
+                for (int hf = 0; hf < C::kHalves; ++hf) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
+                    for (int q = 0; q < 2; ++q) {
+                        uint32_t ov[32];
+                        tmem_ld32_nowait(o_col + hf * 64 + q * 32, ov);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
                             uint4 v;
                             uint32_t *u = reinterpret_cast<uint32_t *>(&v);
 #pragma unroll
                             for (int z = 0; z < 4; ++z)
-                                u[z] = pack_pair<kBf16>(__uint_as_float(ov[e + 2 * z]) * inv,
-                                                        __uint_as_float(ov[e + 2 * z + 1]) * inv);
-                            *reinterpret_cast<uint4 *>(dst + q * 32 + e) = v;
+                                u[z] = pack_pair<kBf16>(__uint_as_float(ov[e * 8 + 2 * z]) * inv,
+                                                        __uint_as_float(ov[e * 8 + 2 * z + 1]) * inv);
+                            *reinterpret_cast<uint4 *>(staging + lane * 128 + (((q * 4 + e) ^ (lane & 7)) << 4)) = v;
                         }
                     }
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {   // four rows a step, 128 bytes of each
+                        const int rr = i * 4 + lane / 8, cc = lane % 8;
+                        const int row_at = __shfl_sync(0xffffffffu, my_row, rr);
+                        const uint4 v = *reinterpret_cast<const uint4 *>(staging + rr * 128 + ((cc ^ (rr & 7)) << 4));
+                        if (row_at >= 0)
+                            *reinterpret_cast<uint4 *>(base + static_cast<size_t>(row_at) * D + hf * 64 + cc * 8) = v;
+                    }
+                    __syncwarp();
                 }
                 tc_fence_before();
             } else {
@@ -699,6 +783,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 last = __shfl_sync(0xffffffffu, last, 0);
                 if (last && live) {
+                    uint16_t *dst = a.out + (static_cast<size_t>(it->q_first + it->tok0 + t * p.tpt + tok) * a.num_q_heads +
+                                             it->hk * p.group + head) * D;
                     __threadfence();
                     float top = -INFINITY;
                     for (int z = 0; z < splits; ++z)
@@ -792,6 +878,14 @@ cudaError_t launch_prefill_grouped(const GroupedArgs &args, int dtype, int head_
     p.cap_log2 = static_cast<float>(args.softcap * log2e);
     p.cap_in = args.softcap > 0.f ? static_cast<float>(2.0 * args.scale / args.softcap * log2e) : 0.f;
     p.group = Hq / Hk;
+    // tanh(u) / u in powers of u^2, for u^2 in [0, 1]: the interpolant at 400
+    // Chebyshev points, cut after the fifth power; with v^2 = 2 u^2
+    const double tanh_u[6] = {0.99999944213822956, -0.33329180320158908, 0.13282513809561988,
+                              -0.051635458658114801, 0.016776776240506608, -0.0030804092508174806};
+    const double u_to_v = 0.70710678118654752;
+    p.cap_v = args.softcap > 0.f ? static_cast<float>(args.scale / args.softcap / u_to_v) : 0.f;
+    for (int i = 0; i < 6; ++i)
+        p.tanh_k[i] = static_cast<float>(args.softcap * log2e * u_to_v * tanh_u[i] / (1 << i));
     p.tpt = kBM / p.group;
     const Plan pl = make_plan(args.num_seqs, Hk, p.group, args.max_q);
     const long long items = pl.base * pl.splits;
