@@ -4,35 +4,40 @@
 // Mathematics: for query row (token at position p, head g of K/V head h) and
 // key j, x_j = log2(e) f(scale q . k_j) with f the optional tanh cap and
 // distance bias, and o = sum_j 2^(x_j - m) v_j / sum_j 2^(x_j - m) over the
-// visible keys, in one pass over 128-key tiles with a reference m that is only
+// visible keys, in one pass over tiles of keys with a reference m that is only
 // raised when a tile's maximum exceeds it by more than 8 (a common factor of
 // weights and sum cancels, so m need not be the maximum).
 //
 // What bounds it: 4 D flops per (row, key) pair on the tensor cores, and one
 // ex2 per pair (three with the cap) on the special-function unit.
 //
-// How (persistent, one CTA per SM, 384 threads):
+// How (persistent, one CTA per SM, 512 threads):
 //  * A tile is 128 rows of (token, head) pairs: 128 / G tokens x the G heads of
 //    one K/V head, gathered by one tensor-map box of Q, so K and V are loaded
 //    and multiplied once for all heads that share them.  A work item is two
 //    such tiles, one K/V head, one sequence, and a range of key tiles.
-//  * Warp 8 (TMA) takes items from a queue, heaviest first, describes each to
-//    the other roles through a two-slot ring, and streams K and V tiles (the
-//    blocks named by the table, as 64-dim x block boxes) through one ring of
-//    slots K0 V0 K1 V1 ...
-//  * Warps 9 and 10 issue the products of query tile 0 and 1, one thread each:
-//    S = Q K^T into tensor memory, one key tile ahead (as soon as the softmax
-//    has loaded the scores before it), and O += P V (P read from tensor
-//    memory) once the softmax has stored P.  S, P and O have columns of their
-//    own, so no product waits for another one's operands: with P over S (128
-//    keys a tile), S had to wait for P V, and a step of both tiles took 5000
-//    cycles, of which the tensor core worked 2600.
+//  * Warp 8 takes items from a queue, heaviest first, describes each to the
+//    other roles through a two-slot ring, and streams Q and tiles of 64 keys of
+//    K; warp 13 streams V.  One copy brings a block of one head, in groups of 8
+//    keys x (64 dims, 64 dims), the operand layout of both products.  Issuing a
+//    copy takes about 100 cycles: with one warp for both and a copy per 64-dim
+//    half, 16 copies a tile took 1600 of its 2400 cycles.
+//  * Warps 9, 10 issue S = Q K^T of query tile 0 and 1 into one of two S/P
+//    buffers of tensor memory, ahead of the softmax, once the P V product that
+//    last read the buffer is complete; warps 11, 12 issue O += P V (P read from
+//    tensor memory) once the softmax has stored P.  One thread issues one
+//    tcgen05.mma per 90 to 110 cycles whatever its size, so the four streams
+//    have threads of their own: with S and P V of a tile issued by one thread,
+//    a step of 64 keys took 2600 cycles, all of them the thread's.
 //  * Warps 0-3 / 4-7 (softmax of tile 0 / 1): thread = row = tensor-memory
-//    lane.  Loads its scores, takes the maximum, exponentiates, and stores the
-//    weights as 16-bit values.
-//  * Tensor memory is what sets the key tile: S, P and O of two query tiles in
-//    512 columns leave 64 keys for D = 128 (with two P buffers) and 128 keys
-//    for D = 64 (one).
+//    lane.  Loads its 64 scores, exponentiates, and stores the weights as
+//    16-bit values over the scores.  Weights are first taken against the
+//    running reference as it is: a row sum of at most 2^14 proves that none of
+//    them is larger, and no maximum is needed.  Otherwise (always on a tile's
+//    first keys) the scores are loaded again, which P has not overwritten yet,
+//    and the maximum comes first.  With a distance bias the key tiles are taken
+//    from the row's own position backwards, so that scores fall along the way
+//    and the reference need not be raised at every tile.
 //  * tanh: an odd polynomial on the FMA pipe (degree 11, |u| <= 1, within
 //    5e-7), chosen per warp and tile by the largest |u|; beyond it, 1 - 2 /
 //    (1 + e^(2u)), whose two special-function operations per score cost 3400
@@ -67,12 +72,15 @@ namespace pa {
 namespace {
 
 constexpr int kBM = 128;               // rows per tile (MMA M)
-constexpr int kThreads = 384;          // 2 x 4 softmax warps, TMA warp, 2 MMA warps, 1 idle
-constexpr int kTmaWarp = 8;
-constexpr int kMmaWarp0 = 9;
-// Register split: launched at 168 per thread; the four producer warps give
-// registers up to the eight softmax warps: 2 x 216 + 72 = 3 x 168.
-constexpr int kRegsSoftmax = 216, kRegsOther = 72;
+constexpr int kBN = 64;                // keys per tile
+constexpr int kThreads = 512;          // 2 x 4 softmax warps, 2 TMA warps, 4 MMA warps, 2 idle
+constexpr int kTmaWarp = 8;            // items, Q, K
+constexpr int kVWarp = 13;
+constexpr int kSWarp0 = 9;
+constexpr int kPvWarp0 = 11;
+// Register split: launched at 128 per thread; the warpgroups of the TMA and
+// MMA warps give registers up to the softmax warps: 2 x 168 + 2 x 88 = 4 x 128.
+constexpr int kRegsSoftmax = 168, kRegsOther = 88;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRaise = 8.f;
 constexpr float kBias = 6.f;           // weights are 2^(x - m + 6): at most 2^14
@@ -107,29 +115,28 @@ struct Item {
 
 template <int D>
 struct Cfg {
-    static constexpr int BN = D == 64 ? 128 : 64;  // keys per tile
-    static constexpr int NP = D == 64 ? 1 : 2;     // P buffers per query tile
     static constexpr int kHalves = D / 64;
     static constexpr int kHalfQ = kBM * 128;
     static constexpr int kTileQ = kHalves * kHalfQ;
-    static constexpr int kHalfKV = BN * 128;
-    static constexpr int kTileKV = kHalves * kHalfKV;
-    static constexpr int kSlots = 8;
-    // tensor-memory columns
-    static constexpr uint32_t TM_S = 0, TM_P = 2 * BN, TM_O = D == 64 ? 384 : 256;
-    static_assert(TM_P + 2 * NP * BN / 2 <= TM_O && TM_O + 2 * D <= kTmemCols, "tensor memory");
+    static constexpr int kGroup = kHalves * 1024;  // 8 keys of a K or V tile
+    static constexpr int kTileKV = kBN / 8 * kGroup;
+    static constexpr int kSlots = D == 64 ? 6 : 4;  // tiles of K, and of V
+    // tensor memory: S/P buffer b of tile t at columns 128 t + 64 b, then O
+    static constexpr uint32_t TM_O = 256;
+    static_assert(TM_O + 2 * D <= kTmemCols, "tensor memory");
     static constexpr int kStagingWarp = 32 * 128;  // 32 rows x 64 dims
     static constexpr int OFF_Q = 0;
-    static constexpr int OFF_KV = 2 * kTileQ;
-    static constexpr int OFF_STAGING = OFF_KV + kSlots * kTileKV;
+    static constexpr int OFF_K = 2 * kTileQ;
+    static constexpr int OFF_V = OFF_K + kSlots * kTileKV;
+    static constexpr int OFF_STAGING = OFF_V + kSlots * kTileKV;
     static constexpr int OFF_BAR = OFF_STAGING + 8 * kStagingWarp;
     static constexpr int Q_FULL = 0, Q_EMPTY = 1, V_LAND = 2;
-    static constexpr int S_FULL = 3, S_EMPTY = 5;          // [tile]
-    static constexpr int P_FULL = 7, PV_DONE = 11;         // [tile][P buffer]
-    static constexpr int MMA_DONE = 15;
-    static constexpr int ITEM_FULL = 17, ITEM_EMPTY = 19;
-    static constexpr int KV_FULL = 21, KV_EMPTY = KV_FULL + kSlots;
-    static constexpr int kNumBars = KV_EMPTY + kSlots;
+    static constexpr int S_FULL = 3, P_FULL = 7, PV_DONE = 11;   // [tile][buffer]
+    static constexpr int MMA_DONE = 15;                          // [issuing thread]
+    static constexpr int ITEM_FULL = 19, ITEM_EMPTY = 21;
+    static constexpr int K_FULL = 23, V_FULL = K_FULL + kSlots;
+    static constexpr int K_EMPTY = V_FULL + kSlots, V_EMPTY = K_EMPTY + kSlots;
+    static constexpr int kNumBars = V_EMPTY + kSlots;
     static constexpr int OFF_TMEM = OFF_BAR + kNumBars * 8;
     static constexpr int OFF_FLAG = OFF_TMEM + 4;
     static constexpr int OFF_MASK = OFF_FLAG + 4;                   // uint32[kMaskRing]
@@ -180,7 +187,6 @@ __device__ __forceinline__ bool warp_all(bool v) { return __all_sync(0xffffffffu
 // Work item w: (pair level, split, sequence, K/V head), latest pairs first.
 // False for an empty item, or for a sequence whose lengths are inconsistent
 // (reported once).
-template <int kBN>
 __device__ __forceinline__ bool item_geometry(const PrefillGroupedArgs &p, int w, bool report,
                                               Item &it) {
     const GroupedArgs &a = p.g;
@@ -249,6 +255,34 @@ __device__ __forceinline__ bool item_geometry(const PrefillGroupedArgs &p, int w
     return true;
 }
 
+// A sequence's blocks of one K/V head, as the copies of K and V take them:
+// lane i holds block i of a key tile.  Only blocks that some query of the
+// sequence sees are read.
+struct KeyBlocks {
+    const int32_t *table;
+    int ctx, pre, lo_seq, num_blocks, heads, hk, b_shift, lane;
+    bool descending;
+    __device__ __forceinline__ KeyBlocks(const GroupedArgs &a, int s, int hk_, int ctx_, int pre_, int q_len,
+                                         int shift, int lane_, bool desc)
+        : table(a.block_tables + static_cast<size_t>(s) * a.max_blocks_per_seq), ctx(ctx_), pre(pre_),
+          lo_seq(a.window > 0 ? max(0, ctx_ - q_len - a.window + 1) : 0), num_blocks(a.num_blocks),
+          heads(a.num_kv_heads), hk(hk_), b_shift(shift), lane(lane_), descending(desc) {}
+    __device__ __forceinline__ int first_key(const Item &it, int j) const {
+        const int i = it.j0 + (descending ? it.nkt - 1 - j : j);
+        return kBN * (i < it.na ? i : i + it.skip);
+    }
+    // The lane's physical block of list entry j: -1 if it is not needed, -2 if
+    // its entry is bad.
+    __device__ __forceinline__ int entry(const Item &it, int j) const {
+        const int key = first_key(it, j) + (lane << b_shift);
+        if (lane >= (kBN >> b_shift) || key >= ctx || (key >= pre && key + (1 << b_shift) <= lo_seq)) return -1;
+        const int e = __ldg(table + (key >> b_shift));
+        return static_cast<unsigned>(e) < static_cast<unsigned>(num_blocks) ? e : -2;
+    }
+    // The block's first group of 8 keys in the cache.
+    __device__ __forceinline__ int group(int blk) const { return (blk * heads + hk) << (b_shift - 3); }
+};
+
 template <bool kBf16, int D, bool kCap, bool kAlibi>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_grouped_kernel(const __grid_constant__ CUtensorMap tm_q,
@@ -256,7 +290,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                            const __grid_constant__ CUtensorMap tm_v,
                            const __grid_constant__ PrefillGroupedArgs p) {
     using C = Cfg<D>;
-    constexpr int kBN = C::BN;
     const GroupedArgs &a = p.g;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -267,15 +300,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile uint32_t *mask_ring = reinterpret_cast<volatile uint32_t *>(smem + C::OFF_MASK);
     Item *items = reinterpret_cast<Item *>(smem + C::OFF_ITEM);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int B = a.block_size;
+    const int B = a.block_size, b_shift = B == 8 ? 3 : (B == 16 ? 4 : 5);
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kNumBars; ++i) {
             uint32_t count = 1;
-            if (i >= C::S_EMPTY && i < C::S_EMPTY + 2) count = 4;             // softmax warps
-            if (i >= C::P_FULL && i < C::P_FULL + 4) count = 4;
-            if (i == C::ITEM_EMPTY || i == C::ITEM_EMPTY + 1) count = 10;     // 2 MMA threads, 8 warps
-            if (i == C::Q_EMPTY || i >= C::KV_EMPTY) count = 2;               // both MMA threads
+            if (i >= C::P_FULL && i < C::P_FULL + 4) count = 4;               // softmax warps
+            if (i == C::ITEM_EMPTY || i == C::ITEM_EMPTY + 1) count = 13;     // 4 MMA threads, 8 softmax warps, V
+            if (i == C::Q_EMPTY || i >= C::K_EMPTY) count = 2;               // both tiles' threads
             mbar_init(&bar[i], count);
         }
         *abort_flag = 0;
@@ -297,12 +329,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
         if (warp == kTmaWarp) {
-            // -------------------------------------------------------- TMA
-            const int boxes = kBN / B;             // per K or V tile
-            uint32_t g = 0;                        // K and V tiles issued, over all items
-            uint32_t lands = 0, tiles = 0;
-            int k = 0;                             // items published
-            int q_loads = 0;
+            // -------------------------------------------------------- items, Q, K
+            uint32_t g = 0;                        // K tiles issued, over all items
+            int k = 0, q_loads = 0;                // items published, Q loads issued
             bool ok = true;
             for (;;) {
                 int w = 0;
@@ -311,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0) w = static_cast<int>(atomicAdd(a.counters, 1u));
                     w = __shfl_sync(0xffffffffu, w, 0);
                     if (static_cast<unsigned>(w) >= static_cast<unsigned>(p.num_items)) break;
-                    if (item_geometry<kBN>(p, w, lane == 0, it)) break;
+                    if (item_geometry(p, w, lane == 0, it)) break;
                 }
                 const bool done = static_cast<unsigned>(w) >= static_cast<unsigned>(p.num_items);
                 const int slot = k % 2;
@@ -325,46 +354,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive(&bar[C::ITEM_FULL + slot]);
                 }
                 if (done) break;
-                // blocks some query of the sequence sees (only those are read)
-                const int lo_seq = a.window > 0 ? max(0, it.ctx - it.q_len - a.window + 1) : 0;
-                const int32_t *table = a.block_tables + static_cast<size_t>(it.s) * a.max_blocks_per_seq;
-                // this lane's block of list entry j: its physical block, -1 if
-                // it is not needed, -2 if its entry is bad
-                auto look_up = [&](int j) {
-                    if (lane >= boxes || j >= it.nkt) return -1;
-                    const int i = it.j0 + j;
-                    const int key = kBN * (i < it.na ? i : i + it.skip) + lane * B;
-                    if (key >= it.ctx || (key >= it.pre && key + B <= lo_seq)) return -1;
-                    const int e = __ldg(table + key / B);
-                    return static_cast<unsigned>(e) < static_cast<unsigned>(a.num_blocks) ? e : -2;
-                };
-                int blk = look_up(0);
-                for (int j = 0; j < it.nkt && ok; ++j) {
-                    const int next = look_up(j + 1);
+                KeyBlocks blocks(a, it.s, it.hk, it.ctx, it.pre, it.q_len, b_shift, lane, kAlibi);
+                int blk = blocks.entry(it, 0);
+                for (int j = 0; j < it.nkt; ++j) {
+                    const int next = j + 1 < it.nkt ? blocks.entry(it, j + 1) : -1;
                     if (blk == -2) atomicOr(a.err, PA_DEVERR_TABLE);
                     const unsigned have = __ballot_sync(0xffffffffu, blk >= 0);
-                    const uint32_t bytes = __popc(have) * static_cast<uint32_t>(B * D * 2);
-                    const int i = it.j0 + j;
-                    const int k0 = kBN * (i < it.na ? i : i + it.skip);
-                    const int y = (blk * a.num_kv_heads + it.hk) * B;
-                    // ---- K
-                    int st = g % C::kSlots;
-                    ok = warp_all(mbar_wait(&bar[C::KV_EMPTY + st], ((g / C::kSlots) & 1) ^ 1, abort_flag, a.err));
+                    const int st = g % C::kSlots;
+                    ok = warp_all(mbar_wait(&bar[C::K_EMPTY + st], ((g / C::kSlots) & 1) ^ 1, abort_flag, a.err));
                     if (!ok) break;
                     if (lane == 0) {
-                        mask_ring[tiles % kMaskRing] = have;
-                        mbar_arrive_expect_tx(&bar[C::KV_FULL + st], bytes);
+                        mask_ring[g % kMaskRing] = have;
+                        mbar_arrive_expect_tx(&bar[C::K_FULL + st], __popc(have) * static_cast<uint32_t>(B * D * 2));
                     }
                     __syncwarp();
-                    if (blk >= 0) {
-                        uint8_t *dst = smem + C::OFF_KV + st * C::kTileKV + lane * (B * 128);
-#pragma unroll
-                        for (int hf = 0; hf < C::kHalves; ++hf)
-                            tma_load_2d(dst + hf * C::kHalfKV, &tm_k, hf * 64, y, &bar[C::KV_FULL + st]);
-                    }
+                    if (blk >= 0)
+                        tma_load_4d(smem + C::OFF_K + st * C::kTileKV + lane * (B / 8) * C::kGroup, &tm_k, 0, 0, 0,
+                                    blocks.group(blk), &bar[C::K_FULL + st]);
                     ++g;
-                    ++tiles;
-                    // ---- Q, once the previous item's S products are complete
+                    // Q, once the previous item's S products are complete
                     if (j == 0) {
                         if (k > 0) {
                             ok = warp_all(mbar_wait(&bar[C::Q_EMPTY], (k - 1) & 1, abort_flag, a.err));
@@ -383,49 +391,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ++q_loads;
                         __syncwarp();
                     }
-                    // ---- V
-                    st = g % C::kSlots;
-                    ok = warp_all(mbar_wait(&bar[C::KV_EMPTY + st], ((g / C::kSlots) & 1) ^ 1, abort_flag, a.err));
-                    if (!ok) break;
-                    uint8_t *vt = smem + C::OFF_KV + st * C::kTileKV;
-                    auto clear_row = [&](int r) {
-                        for (int c = lane; c < C::kHalves * 8; c += 32)
-                            *reinterpret_cast<uint4 *>(vt + (c / 8) * C::kHalfKV + r * 128 + (c % 8) * 16) =
-                                make_uint4(0, 0, 0, 0);
-                    };
-                    const unsigned full = boxes == 32 ? 0xffffffffu : (1u << boxes) - 1;
-                    if (have != full) {   // blocks that are not loaded: cleared up front
-                        for (int r = 0; r < kBN; ++r)
-                            if (!((have >> (r / B)) & 1)) clear_row(r);
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                        __syncwarp();
-                    }
-                    // rows of the context's last block past its end are cleared
-                    // once the copies have landed
-                    const int tail = it.ctx - k0;          // valid rows, if < kBN
-                    const bool land = tail < kBN && tail % B != 0 && ((have >> (tail / B)) & 1);
-                    uint64_t *vbar = land ? &bar[C::V_LAND] : &bar[C::KV_FULL + st];
-                    if (lane == 0) mbar_arrive_expect_tx(vbar, bytes);
-                    __syncwarp();
-                    if (blk >= 0) {
-#pragma unroll
-                        for (int hf = 0; hf < C::kHalves; ++hf)
-                            tma_load_2d(vt + hf * C::kHalfKV + lane * (B * 128), &tm_v, hf * 64, y, vbar);
-                    }
-                    ++g;
-                    if (land) {
-                        ok = warp_all(mbar_wait(&bar[C::V_LAND], lands & 1, abort_flag, a.err));
-                        if (!ok) {
-                            mbar_wait_drain(&bar[C::V_LAND], lands & 1);
-                            --g;   // nothing signals this slot's FULL barrier
-                            break;
-                        }
-                        ++lands;
-                        for (int r = tail; r < (tail / B + 1) * B; ++r) clear_row(r);
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&bar[C::KV_FULL + st]);
-                    }
                     blk = next;
                 }
                 if (!ok) break;
@@ -435,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) {   // let every copy already issued land
                     if (q_loads > 0) mbar_wait_drain(&bar[C::Q_FULL], (q_loads - 1) & 1);
                     for (uint32_t i = g > C::kSlots ? g - C::kSlots : 0; i < g; ++i)
-                        mbar_wait_drain(&bar[C::KV_FULL + i % C::kSlots], (i / C::kSlots) & 1);
+                        mbar_wait_drain(&bar[C::K_FULL + i % C::kSlots], (i / C::kSlots) & 1);
                 }
                 __threadfence();
                 if (atomicAdd(a.counters + 1, 1u) == gridDim.x - 1) {
@@ -444,41 +409,82 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             __syncwarp();
-        } else if (warp == kMmaWarp0 || warp == kMmaWarp0 + 1) {
+        } else if (warp == kVWarp) {
+            // -------------------------------------------------------- V
+            uint32_t g = 0, lands = 0;             // V tiles issued; of these, landed on V_LAND
+            bool ok = true;
+            for (int k = 0; ok; ++k) {
+                const int slot = k % 2;
+                ok = warp_all(mbar_wait(&bar[C::ITEM_FULL + slot], (k / 2) & 1, abort_flag, a.err));
+                if (!ok) break;
+                const Item it = items[slot];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar[C::ITEM_EMPTY + slot]);
+                if (it.done) break;
+                KeyBlocks blocks(a, it.s, it.hk, it.ctx, it.pre, it.q_len, b_shift, lane, kAlibi);
+                int blk = blocks.entry(it, 0);
+                for (int j = 0; j < it.nkt; ++j) {
+                    const int next = j + 1 < it.nkt ? blocks.entry(it, j + 1) : -1;
+                    const unsigned have = __ballot_sync(0xffffffffu, blk >= 0);
+                    const uint32_t bytes = __popc(have) * static_cast<uint32_t>(B * D * 2);
+                    const int st = g % C::kSlots;
+                    ok = warp_all(mbar_wait(&bar[C::V_EMPTY + st], ((g / C::kSlots) & 1) ^ 1, abort_flag, a.err));
+                    if (!ok) break;
+                    uint8_t *vt = smem + C::OFF_V + st * C::kTileKV;
+                    auto clear_row = [&](int r) {
+                        for (int c = lane; c < C::kHalves * 8; c += 32)
+                            *reinterpret_cast<uint4 *>(vt + (r / 8) * C::kGroup + (c / 8) * 1024 + (r % 8) * 128 +
+                                                       (c % 8) * 16) = make_uint4(0, 0, 0, 0);
+                    };
+                    if (have != (1u << (kBN >> b_shift)) - 1) {   // blocks that are not loaded: cleared up front
+                        for (int r = 0; r < kBN; ++r)
+                            if (!((have >> (r >> b_shift)) & 1)) clear_row(r);
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                    }
+                    // rows of the context's last block past its end are cleared
+                    // once the copies have landed
+                    const int tail = it.ctx - blocks.first_key(it, j);          // valid rows, if < kBN
+                    const bool land = tail < kBN && tail % B != 0 && ((have >> (tail >> b_shift)) & 1);
+                    uint64_t *vbar = land ? &bar[C::V_LAND] : &bar[C::V_FULL + st];
+                    if (lane == 0) mbar_arrive_expect_tx(vbar, bytes);
+                    __syncwarp();
+                    if (blk >= 0)
+                        tma_load_4d(vt + lane * (B / 8) * C::kGroup, &tm_v, 0, 0, 0, blocks.group(blk), vbar);
+                    if (land) {
+                        ok = warp_all(mbar_wait(&bar[C::V_LAND], lands & 1, abort_flag, a.err));
+                        if (!ok) {
+                            mbar_wait_drain(&bar[C::V_LAND], lands & 1);
+                            break;   // nothing will signal this slot's FULL barrier
+                        }
+                        ++lands;
+                        for (int r = tail; r < ((tail >> b_shift) + 1) * B; ++r) clear_row(r);
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bar[C::V_FULL + st]);
+                    }
+                    ++g;
+                    blk = next;
+                }
+            }
+            if (!ok && lane == 0)   // let every copy already issued land
+                for (uint32_t i = g > C::kSlots ? g - C::kSlots : 0; i < g; ++i)
+                    mbar_wait_drain(&bar[C::V_FULL + i % C::kSlots], (i / C::kSlots) & 1);
+            __syncwarp();
+        } else if (warp >= kSWarp0 && warp < kPvWarp0 + 2) {
             // -------------------------------------------------------- products
             if (lane == 0) {
-                const int t = warp - kMmaWarp0;
+                const bool is_s = warp < kPvWarp0;
+                const int t = warp - (is_s ? kSWarp0 : kPvWarp0);
                 constexpr uint32_t idesc_s = instr_desc(kBf16, false, kBN);
                 constexpr uint32_t idesc_pv = instr_desc(kBf16, true, D);
                 const uint32_t q_addr = smem_addr(smem + C::OFF_Q) + t * C::kTileQ;
-                const uint32_t kv_addr = smem_addr(smem + C::OFF_KV);
-                const uint32_t tm_s = tmem + C::TM_S + t * kBN, tm_o = tmem + C::TM_O + t * D;
-                const uint32_t tm_p = tmem + C::TM_P + t * (C::NP * kBN / 2);
-                uint32_t g = 0;        // first slot of the item
-                uint32_t ns = 0;       // S products of this query tile, over all items
-                uint32_t np = 0;       // P V products
+                const uint32_t kv_addr = smem_addr(smem + (is_s ? C::OFF_K : C::OFF_V));
+                uint64_t *kv_full = &bar[is_s ? C::K_FULL : C::V_FULL], *kv_empty = &bar[is_s ? C::K_EMPTY : C::V_EMPTY];
+                const uint32_t tm_s = tmem + t * 128, tm_o = tmem + C::TM_O + t * D;
+                uint32_t g = 0;              // K (V) tiles seen
+                uint32_t n = 0;              // products of this thread, over all items
                 bool ok = true;
-                auto wait_slot = [&](uint32_t i) {
-                    return mbar_wait(&bar[C::KV_FULL + i % C::kSlots], (i / C::kSlots) & 1, abort_flag, a.err);
-                };
-                // S of the key tile in slot i, once the scores before it are loaded
-                auto issue_s = [&](uint32_t i, bool last) {
-                    if (!wait_slot(i)) return false;
-                    if (ns > 0 && !mbar_wait(&bar[C::S_EMPTY + t], (ns - 1) & 1, abort_flag, a.err)) return false;
-                    tc_fence_after();
-                    const uint32_t ka = kv_addr + (i % C::kSlots) * C::kTileKV;
-#pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks) {
-                        const int half = ks / 4, kk = ks % 4;
-                        mma_ss(tm_s, smem_desc(q_addr + half * C::kHalfQ + kk * 32, 16, 1024),
-                               smem_desc(ka + half * C::kHalfKV + kk * 32, 16, 1024), idesc_s, ks > 0);
-                    }
-                    mma_commit(&bar[C::S_FULL + t]);
-                    mma_commit(&bar[C::KV_EMPTY + i % C::kSlots]);
-                    if (last) mma_commit(&bar[C::Q_EMPTY]);
-                    ++ns;
-                    return true;
-                };
                 for (int k = 0; ok; ++k) {
                     const int slot = k % 2;
                     ok = mbar_wait(&bar[C::ITEM_FULL + slot], (k / 2) & 1, abort_flag, a.err);
@@ -488,39 +494,52 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int nkt = it->nkt, nk = max(0, t == 0 ? it->nk0 : it->nk1);
                     mbar_arrive(&bar[C::ITEM_EMPTY + slot]);
                     if (done) break;
-                    ok = mbar_wait(&bar[C::Q_FULL], k & 1, abort_flag, a.err);
-                    if (!ok) break;
-                    if (nk == 0) mbar_arrive(&bar[C::Q_EMPTY]);
-                    if (nk > 0) ok = issue_s(g, nk == 1);
-                    for (int j = 0; j < nkt && ok; ++j, g += 2) {
-                        if (j >= nk) {   // not this tile's: hand both slots back
-                            ok = wait_slot(g);
-                            if (!ok) break;
-                            mbar_arrive(&bar[C::KV_EMPTY + g % C::kSlots]);
-                            ok = wait_slot(g + 1);
-                            if (!ok) break;
-                            mbar_arrive(&bar[C::KV_EMPTY + (g + 1) % C::kSlots]);
+                    if (is_s) {
+                        ok = mbar_wait(&bar[C::Q_FULL], k & 1, abort_flag, a.err);
+                        if (!ok) break;
+                        if (nk == 0) mbar_arrive(&bar[C::Q_EMPTY]);
+                    }
+                    for (int j = 0; j < nkt; ++j, ++g) {
+                        const uint32_t st = g % C::kSlots;
+                        ok = mbar_wait(kv_full + st, (g / C::kSlots) & 1, abort_flag, a.err);
+                        if (!ok) break;
+                        // the entries this query tile needs: the first nk in key order
+                        const int jj = kAlibi ? nkt - 1 - j : j;
+                        if (jj >= nk) {   // not this one: hand the slot back
+                            mbar_arrive(kv_empty + st);
                             continue;
                         }
-                        if (j + 1 < nk) ok = issue_s(g + 2, j + 2 == nk);
-                        // O += P V
-                        const uint32_t buf = np % C::NP;
-                        ok = ok && wait_slot(g + 1) &&
-                             mbar_wait(&bar[C::P_FULL + t * 2 + buf], (np / C::NP) & 1, abort_flag, a.err);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint32_t va = kv_addr + ((g + 1) % C::kSlots) * C::kTileKV;
+                        const uint32_t buf = n & 1, ph = (n >> 1) & 1;
+                        const uint32_t kv = kv_addr + st * C::kTileKV;
+                        if (is_s) {
+                            // the product that last read the buffer's P
+                            if (n >= 2) ok = mbar_wait(&bar[C::PV_DONE + t * 2 + buf], ph ^ 1, abort_flag, a.err);
+                            if (!ok) break;
+                            tc_fence_after();
 #pragma unroll
-                        for (int ks = 0; ks < kBN / 16; ++ks)
-                            mma_ts(tm_o, tm_p + buf * (kBN / 2) + ks * 8,
-                                   smem_desc(va + ks * 2048, C::kHalfKV, 1024), idesc_pv, j > 0 || ks > 0);
-                        mma_commit(&bar[C::PV_DONE + t * 2 + buf]);
-                        mma_commit(&bar[C::KV_EMPTY + (g + 1) % C::kSlots]);
-                        ++np;
+                            for (int ks = 0; ks < D / 16; ++ks) {
+                                const int half = ks / 4, kk = ks % 4;
+                                mma_ss(tm_s + buf * 64, smem_desc(q_addr + half * C::kHalfQ + kk * 32, 16, 1024),
+                                       smem_desc(kv + half * 1024 + kk * 32, 16, C::kGroup), idesc_s, ks > 0);
+                            }
+                            mma_commit(&bar[C::S_FULL + t * 2 + buf]);
+                            if (kAlibi ? jj == 0 : jj == nk - 1) mma_commit(&bar[C::Q_EMPTY]);
+                        } else {
+                            ok = mbar_wait(&bar[C::P_FULL + t * 2 + buf], ph, abort_flag, a.err);
+                            if (!ok) break;
+                            tc_fence_after();
+#pragma unroll
+                            for (int ks = 0; ks < kBN / 16; ++ks)
+                                mma_ts(tm_o, tm_s + buf * 64 + ks * 8, smem_desc(kv + ks * 2 * C::kGroup, 1024, C::kGroup),
+                                       idesc_pv, (kAlibi ? jj < nk - 1 : jj > 0) || ks > 0);
+                            mma_commit(&bar[C::PV_DONE + t * 2 + buf]);
+                        }
+                        mma_commit(kv_empty + st);
+                        ++n;
                     }
                 }
-                mma_commit(&bar[C::MMA_DONE + t]);
-                mbar_wait_drain(&bar[C::MMA_DONE + t], 0);
+                mma_commit(&bar[C::MMA_DONE + warp - kSWarp0]);
+                mbar_wait_drain(&bar[C::MMA_DONE + warp - kSWarp0], 0);
             }
             __syncwarp();
         }
@@ -531,14 +550,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r = (warp % 4) * 32 + lane;
         const int tok = r / p.group, head = r - tok * p.group;   // within the tile
         const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp % 4) * 32) << 16);
-        const uint32_t s_col = lane_base + C::TM_S + t * kBN;
-        const uint32_t p_col = lane_base + C::TM_P + t * (C::NP * kBN / 2);
+        const uint32_t s_cols = lane_base + t * 128;
         const uint32_t o_col = lane_base + C::TM_O + t * D;
         uint8_t *staging = smem + C::OFF_STAGING + warp * C::kStagingWarp;
         const float c = p.scale_log2;
-        const bool plain = !kCap && !kAlibi && c > 0.f;   // the scale goes into the exponent's FMA
-        const float cm = plain ? c : 1.f;
-        const unsigned full = (1u << (kBN / B)) - 1;
+        const unsigned full = (1u << (kBN >> b_shift)) - 1;
         uint32_t n = 0;            // S tiles consumed
         uint32_t tiles = 0;        // key tiles of all items (mask ring)
         bool ok = true;
@@ -552,7 +568,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool done = it->done;
             const int nk = t == 0 ? it->nk0 : it->nk1;
             if (done) break;
-            const uint32_t tile_base = tiles;
+            // descending: a tile that needs fewer entries skips the first ones
+            const uint32_t tile_base = tiles + (kAlibi ? it->nkt - max(nk, 0) : 0);
             tiles += it->nkt;
             if (nk < 0) {
                 __syncwarp();
@@ -564,20 +581,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 ? it->first_pos + t * p.tpt + tok
                                 : -1;
             const int pre_all = it->pre, na = it->na, skip = it->skip, j0 = it->j0;
+            const int last = j0 + max(nk, 0) - 1;
             // positions of the warp's rows, for tiles that need no mask
             const int wmin = __reduce_min_sync(0xffffffffu, pos);
             const int wmax = __reduce_max_sync(0xffffffffu, pos);
             float slope = 0.f;
             if constexpr (kAlibi)
                 slope = pos >= 0 ? __ldg(a.alibi_slopes + it->hk * p.group + head) * 1.4426950408889634f : 0.f;
-            float m = -INFINITY, l = 0.f;
+            // a row without a query takes no part (m = 0: no maximum is missing)
+            float m = pos >= 0 ? -INFINITY : 0.f, l = 0.f;
             for (int j = 0; j < nk; ++j, ++n) {
-                ok = warp_all(mbar_wait(&bar[C::S_FULL + t], n & 1, abort_flag, a.err));
+                const uint32_t buf = n & 1;
+                ok = warp_all(mbar_wait(&bar[C::S_FULL + t * 2 + buf], (n >> 1) & 1, abort_flag, a.err));
                 if (!ok) break;
                 tc_fence_after();
-                const int k0 = kBN * (j0 + j < na ? j0 + j : j0 + j + skip);
+                const uint32_t s_col = s_cols + buf * 64;
+                const int i = kAlibi ? last - j : j0 + j;   // list entry
+                const int k0 = kBN * (i < na ? i : i + skip);
+                const unsigned have = mask_ring[(tile_base + j) % kMaskRing];
+                const bool all_visible = have == full &&
+                                         (k0 + kBN <= pre_all ? wmin >= 0
+                                                              : k0 + kBN - 1 <= wmin &&
+                                                                    (a.window == 0 || k0 > wmax - a.window));
+                // The scores as they are in tensor memory.
                 float x[kBN];
-                {
+                auto load_raw = [&]() {
                     uint32_t u[kBN];
 #pragma unroll
                     for (int q = 0; q < kBN / 32; ++q)
@@ -585,122 +613,143 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_ld_wait();
 #pragma unroll
                     for (int e = 0; e < kBN; ++e) x[e] = __uint_as_float(u[e]);
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar[C::S_EMPTY + t]);   // the next S may be written
-                if constexpr (kCap) {
-                    // v^2 < 2 for every score iff no bit pattern reaches that of 2
+                };
+                // tanh's polynomial: v = cap_v x and its value over v, w = v^2
+                auto cap_poly = [&](float x0, float x1, float &v0, float &v1, float &y0, float &y1, uint32_t &any) {
+                    float w0, w1;
+                    mul2(v0, v1, x0, x1, p.cap_v, p.cap_v);
+                    mul2(w0, w1, v0, v1, v0, v1);
+                    any |= __float_as_uint(w0) | __float_as_uint(w1);
+                    y0 = y1 = p.tanh_k[5];
+#pragma unroll
+                    for (int i = 4; i >= 0; --i) fma2(y0, y1, y0, y1, w0, w1, p.tanh_k[i], p.tanh_k[i]);
+                };
+                uint32_t w[kBN / 2];       // the weights, packed
+                float sum = 0.f;
+                load_raw();
+                // First against the reference as it is, if every key is visible
+                // (and, for the distance bias, none is ahead of the row).
+                bool done_fast = false;
+                const bool fast = all_visible && (!kAlibi || k0 + kBN - 1 <= wmin) && warp_all(m != -INFINITY);
+                if (fast) {
+                    float sums[4] = {0.f, 0.f, 0.f, 0.f};
                     uint32_t any = 0;
-                    const float cv = p.cap_v;
+                    // exponent of key e: score + bias, the distance bias being
+                    // slope (k0 + e - pos), rising along the tile
+                    const float bias = kBias - m + (kAlibi ? slope * static_cast<float>(k0 - pos) : 0.f);
 #pragma unroll
-                    for (int e = 0; e < kBN; ++e) any |= __float_as_uint((x[e] * cv) * (x[e] * cv));
-                    if (warp_all(any < 0x40000000u)) {
+                    for (int e = 0; e < kBN; e += 2) {
+                        float y0, y1;
+                        float b0 = bias, b1 = bias;
+                        if constexpr (kAlibi) {
+                            b0 = fmaf(slope, static_cast<float>(e), bias);
+                            b1 = fmaf(slope, static_cast<float>(e + 1), bias);
+                        }
+                        if constexpr (kCap) {
+                            float v0, v1;
+                            cap_poly(x[e], x[e + 1], v0, v1, y0, y1, any);
+                            fma2(y0, y1, v0, v1, y0, y1, b0, b1);
+                        } else {
+                            fma2(y0, y1, x[e], x[e + 1], c, c, b0, b1);
+                        }
+                        y0 = fast_exp2(y0);
+                        y1 = fast_exp2(y1);
+                        add2(sums[e & 2], sums[(e & 2) + 1], sums[e & 2], sums[(e & 2) + 1], y0, y1);
+                        w[e / 2] = pack_pair<kBf16>(y0, y1);
+                    }
+                    sum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+                    // a sum of at most 2^14 proves that no weight is larger; v^2 < 2
+                    // that the polynomial holds (no bit pattern reaches that of 2)
+                    done_fast = warp_all(sum <= 16384.f && any < 0x40000000u);
+                    if (!done_fast) load_raw();
+                }
+                if (!done_fast) {
+                    // scores to the log2 domain
+                    if constexpr (kCap) {
+                        uint32_t any = 0;
 #pragma unroll
-                        for (int e = 0; e < kBN; e += 2) {
-                            float v0, v1, w0, w1, y0 = p.tanh_k[5], y1 = y0;
-                            mul2(v0, v1, x[e], x[e + 1], cv, cv);
-                            mul2(w0, w1, v0, v1, v0, v1);
+                        for (int e = 0; e < kBN; ++e)
+                            any |= __float_as_uint((x[e] * p.cap_v) * (x[e] * p.cap_v));
+                        if (warp_all(any < 0x40000000u)) {
 #pragma unroll
-                            for (int c2 = 4; c2 >= 0; --c2)
-                                fma2(y0, y1, y0, y1, w0, w1, p.tanh_k[c2], p.tanh_k[c2]);
-                            mul2(x[e], x[e + 1], v0, v1, y0, y1);
+                            for (int e = 0; e < kBN; e += 2) {
+                                float v0, v1, y0, y1;
+                                cap_poly(x[e], x[e + 1], v0, v1, y0, y1, any);
+                                mul2(x[e], x[e + 1], v0, v1, y0, y1);
+                            }
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < kBN; ++e)
+                                x[e] = p.cap_log2 - 2.f * p.cap_log2 * fast_rcp(1.f + fast_exp2(x[e] * p.cap_in));
                         }
                     } else {
 #pragma unroll
-                        for (int e = 0; e < kBN; ++e)
-                            x[e] = p.cap_log2 - 2.f * p.cap_log2 * fast_rcp(1.f + fast_exp2(x[e] * p.cap_in));
+                        for (int e = 0; e < kBN; ++e) x[e] *= c;
                     }
-                } else if (!plain) {
+                    if constexpr (kAlibi) {
+                        const float d0 = static_cast<float>(pos - k0);
 #pragma unroll
-                    for (int e = 0; e < kBN; ++e) x[e] *= c;
-                }
-                if constexpr (kAlibi) {
-                    const float d0 = static_cast<float>(pos - k0);
-#pragma unroll
-                    for (int e = 0; e < kBN; ++e) x[e] -= slope * fabsf(d0 - static_cast<float>(e));
-                }
-                const unsigned have = mask_ring[(tile_base + j) % kMaskRing];
-                const bool all_visible = have == full &&
-                                         (k0 + kBN <= pre_all ? wmin >= 0
-                                                             : k0 + kBN - 1 <= wmin &&
-                                                                   (a.window == 0 || k0 > wmax - a.window));
-                if (!all_visible) {
-                    // one bit per key: keys before pr, and from lw up to h (none
-                    // for a row without a query), in blocks that are there
-                    const int h = pos + 1 - k0, pr = pos < 0 ? 0 : pre_all - k0;
-                    const int lw = a.window > 0 ? h - a.window : 0;
-#pragma unroll
-                    for (int q = 0; q < kBN / 32; ++q) {
-                        uint32_t vis = bits_below(pr - 32 * q) |
-                                       (bits_below(h - 32 * q) & ~bits_below(lw - 32 * q));
-                        if (have != full) vis &= present(have, q, B);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            x[32 * q + e] = (vis >> e) & 1 ? x[32 * q + e] : -INFINITY;
+                        for (int e = 0; e < kBN; ++e) x[e] -= slope * fabsf(d0 - static_cast<float>(e));
                     }
-                }
-                float mx[8];
+                    if (!all_visible) {
+                        // one bit per key: keys before pr, and from lw up to h (none
+                        // for a row without a query), in blocks that are there
+                        const int h = pos + 1 - k0, pr = pos < 0 ? 0 : pre_all - k0;
+                        const int lw = a.window > 0 ? h - a.window : 0;
 #pragma unroll
-                for (int q = 0; q < 8; ++q) mx[q] = fmaxf(x[q], x[q + 8]);
+                        for (int q = 0; q < kBN / 32; ++q) {
+                            uint32_t vis = bits_below(pr - 32 * q) |
+                                           (bits_below(h - 32 * q) & ~bits_below(lw - 32 * q));
+                            if (have != full) vis &= present(have, q, B);
 #pragma unroll
-                for (int e = 16; e < kBN; e += 8)
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) mx[q] = fmaxf(mx[q], x[e + q]);
-                const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
-                                        fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * cm;
-                const uint32_t buf = n % C::NP;
-                // the P buffer's last product (and, in order, all before it)
-                if (n >= C::NP) {
-                    ok = warp_all(mbar_wait(&bar[C::PV_DONE + t * 2 + buf], (n / C::NP - 1) & 1, abort_flag, a.err));
-                    if (!ok) break;
-                    tc_fence_after();
-                }
-                const bool raise = top > m + kRaise;
-                if (__any_sync(0xffffffffu, raise)) {
-                    const float m_new = raise ? top : m;
-                    const float alpha = m == m_new ? 1.f : fast_exp2(m - m_new);
-                    m = m_new;
-                    l *= alpha;
-                    if (j > 0) {   // O, once the product before is complete
-                        const uint32_t pb = (n - 1) % C::NP;
-                        ok = warp_all(mbar_wait(&bar[C::PV_DONE + t * 2 + pb], ((n - 1) / C::NP) & 1, abort_flag, a.err));
-                        if (!ok) break;
-                        tc_fence_after();
-#pragma unroll 1
-                        for (int q = 0; q < D / 16; ++q) {
-                            uint32_t ov[16];
-                            tmem_ld16_nowait(o_col + q * 16, ov);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
-                            tmem_st16(o_col + q * 16, ov);
+                            for (int e = 0; e < 32; ++e)
+                                x[32 * q + e] = (vis >> e) & 1 ? x[32 * q + e] : -INFINITY;
                         }
                     }
-                }
-                const float bias = m == -INFINITY ? 0.f : kBias - m;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                    float mx[8];
 #pragma unroll
-                for (int q = 0; q < kBN / 32; ++q) {
-                    uint32_t w[16];
+                    for (int q = 0; q < 8; ++q) mx[q] = fmaxf(x[q], x[q + 8]);
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        float *y = x + q * 32 + e;
-                        fma2(y[0], y[1], y[0], y[1], cm, cm, bias, bias);
-                        fma2(y[2], y[3], y[2], y[3], cm, cm, bias, bias);
-                        y[0] = fast_exp2(y[0]);
-                        y[1] = fast_exp2(y[1]);
-                        y[2] = fast_exp2(y[2]);
-                        y[3] = fast_exp2(y[3]);
-                        add2(sum[0], sum[1], sum[0], sum[1], y[0], y[1]);
-                        add2(sum[2], sum[3], sum[2], sum[3], y[2], y[3]);
-                        w[e / 2] = pack_pair<kBf16>(y[0], y[1]);
-                        w[e / 2 + 1] = pack_pair<kBf16>(y[2], y[3]);
+                    for (int e = 16; e < kBN; e += 8)
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) mx[q] = fmaxf(mx[q], x[e + q]);
+                    const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                                            fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
+                    const bool raise = top > m + kRaise;
+                    if (__any_sync(0xffffffffu, raise)) {
+                        const float m_new = raise ? top : m;
+                        const float alpha = m == m_new ? 1.f : fast_exp2(m - m_new);
+                        m = m_new;
+                        l *= alpha;
+                        if (j > 0) {   // O, once the product before is complete
+                            ok = warp_all(mbar_wait(&bar[C::PV_DONE + t * 2 + (buf ^ 1)], ((n - 1) >> 1) & 1,
+                                                    abort_flag, a.err));
+                            if (!ok) break;
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int q = 0; q < D / 16; ++q) {
+                                uint32_t ov[16];
+                                tmem_ld16_nowait(o_col + q * 16, ov);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int e = 0; e < 16; ++e)
+                                    ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+                                tmem_st16(o_col + q * 16, ov);
+                            }
+                        }
                     }
-                    tmem_st16(p_col + buf * (kBN / 2) + q * 16, w);
+                    const float bias = m == -INFINITY ? 0.f : kBias - m;
+                    float sums[2] = {0.f, 0.f};
+#pragma unroll
+                    for (int e = 0; e < kBN; e += 2) {
+                        const float y0 = fast_exp2(x[e] + bias), y1 = fast_exp2(x[e + 1] + bias);
+                        add2(sums[0], sums[1], sums[0], sums[1], y0, y1);
+                        w[e / 2] = pack_pair<kBf16>(y0, y1);
+                    }
+                    sum = sums[0] + sums[1];
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                l += sum;
+                tmem_st32(s_col, w);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
@@ -708,8 +757,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!ok) break;
             if (nk > 0) {
-                ok = warp_all(mbar_wait(&bar[C::PV_DONE + t * 2 + (n - 1) % C::NP], ((n - 1) / C::NP) & 1, abort_flag,
-                                        a.err));
+                ok = warp_all(mbar_wait(&bar[C::PV_DONE + t * 2 + ((n - 1) & 1)], ((n - 1) >> 1) & 1, abort_flag, a.err));
                 if (!ok) break;
                 tc_fence_after();
             }
@@ -901,13 +949,14 @@ cudaError_t launch_prefill_grouped(const GroupedArgs &args, int dtype, int head_
                                   static_cast<cuuint64_t>(args.total_q)};
     const cuuint64_t q_strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(Hq) * D * 2};
     const cuuint32_t q_box[3] = {64, static_cast<cuuint32_t>(p.group), static_cast<cuuint32_t>(p.tpt)};
-    const cuuint64_t kv_dims[2] = {static_cast<cuuint64_t>(D),
-                                   static_cast<cuuint64_t>(args.num_blocks) * Hk * B};
-    const cuuint64_t kv_strides[1] = {static_cast<cuuint64_t>(D) * 2};
-    const cuuint32_t kv_box[2] = {64, static_cast<cuuint32_t>(B)};
+    // groups of 8 keys x 64-dim halves x keys x dims: a box is one block of a head
+    const cuuint64_t kv_dims[4] = {64, 8, static_cast<cuuint64_t>(D / 64),
+                                   static_cast<cuuint64_t>(args.num_blocks) * Hk * (B / 8)};
+    const cuuint64_t kv_strides[3] = {static_cast<cuuint64_t>(D) * 2, 128, static_cast<cuuint64_t>(D) * 16};
+    const cuuint32_t kv_box[4] = {64, 8, static_cast<cuuint32_t>(D / 64), static_cast<cuuint32_t>(B / 8)};
     if (!encode(&tm_q, bf16, args.q, 3, q_dims, q_strides, q_box) ||
-        !encode(&tm_k, bf16, args.k_cache, 2, kv_dims, kv_strides, kv_box) ||
-        !encode(&tm_v, bf16, args.v_cache, 2, kv_dims, kv_strides, kv_box))
+        !encode(&tm_k, bf16, args.k_cache, 4, kv_dims, kv_strides, kv_box) ||
+        !encode(&tm_v, bf16, args.v_cache, 4, kv_dims, kv_strides, kv_box))
         return cudaErrorInvalidValue;
     const bool cap = args.softcap > 0.f, alibi = args.alibi_slopes != nullptr;
     const Kernel kernel = bf16 ? (D == 64 ? pick<true, 64>(cap, alibi) : pick<true, 128>(cap, alibi))
