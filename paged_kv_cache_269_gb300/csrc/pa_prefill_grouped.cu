@@ -32,8 +32,8 @@
 //  * Warps 0-3 / 4-7 (softmax of tile 0 / 1): thread = row = tensor-memory
 //    lane.  Loads its 64 scores, exponentiates, and stores the weights as
 //    16-bit values over the scores.  Weights are first taken against the
-//    running reference as it is: a row sum of at most 2^14 proves that none of
-//    them is larger, and no maximum is needed.  Otherwise (always on a tile's
+//    running reference as it is: a small enough row sum proves that all of them
+//    fit the type, and no maximum is needed.  Otherwise (always on a tile's
 //    first keys) the scores are loaded again, which P has not overwritten yet,
 //    and the maximum comes first.  With a distance bias the key tiles are taken
 //    from the row's own position backwards, so that scores fall along the way
@@ -63,6 +63,7 @@
 #include <stdint.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "pa_device.cuh"
 #include "pa_internal.h"
@@ -82,8 +83,12 @@ constexpr int kPvWarp0 = 11;
 // MMA warps give registers up to the softmax warps: 2 x 168 + 2 x 88 = 4 x 128.
 constexpr int kRegsSoftmax = 168, kRegsOther = 88;
 constexpr uint32_t kTmemCols = 512;
-constexpr float kRaise = 8.f;
-constexpr float kBias = 6.f;           // weights are 2^(x - m + 6): at most 2^14
+constexpr float kRaise = 8.f;          // where a maximum is taken, it is kept if it is this near
+// Weights are 2^(x - m + bias).  fp16 holds at most 2^16: a row sum of up to
+// 2^15 proves every weight fits; bf16 has the exponent range of fp32, and its
+// reference hardly ever has to be raised.
+constexpr float kBias = 4.f;
+template <bool kBf16> constexpr float kMostSum = kBf16 ? 1.1529215e18f : 32768.f;   // 2^60, 2^15
 constexpr int kMaskRing = 16;
 // Work is split over keys while there are fewer items than SMs (152).
 constexpr int kSplitTarget = 152;
@@ -555,6 +560,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint8_t *staging = smem + C::OFF_STAGING + warp * C::kStagingWarp;
         const float c = p.scale_log2;
         const unsigned full = (1u << (kBN >> b_shift)) - 1;
+        // the polynomial's coefficients as pairs, kept in registers (volatile: not
+        // built again at each use, which took as many moves as products)
+        uint64_t tanh2[6], cap_v2;
+        if constexpr (kCap) {
+#pragma unroll
+            for (int i = 0; i < 6; ++i) tanh2[i] = keep_pair(p.tanh_k[i]);
+            cap_v2 = keep_pair(p.cap_v);
+        }
         uint32_t n = 0;            // S tiles consumed
         uint32_t tiles = 0;        // key tiles of all items (mask ring)
         bool ok = true;
@@ -615,25 +628,41 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int e = 0; e < kBN; ++e) x[e] = __uint_as_float(u[e]);
                 };
                 // tanh's polynomial: v = cap_v x and its value over v, w = v^2
-                auto cap_poly = [&](float x0, float x1, float &v0, float &v1, float &y0, float &y1, uint32_t &any) {
-                    float w0, w1;
-                    mul2(v0, v1, x0, x1, p.cap_v, p.cap_v);
-                    mul2(w0, w1, v0, v1, v0, v1);
-                    any |= __float_as_uint(w0) | __float_as_uint(w1);
-                    y0 = y1 = p.tanh_k[5];
+                auto cap_poly = [&](float x0, float x1, uint64_t &v, uint64_t &y, uint32_t &any) {
+                    v = mul_pair(make_pair(x0, x1), cap_v2);
+                    const uint64_t w2 = mul_pair(v, v);
+                    any |= static_cast<uint32_t>(w2) | static_cast<uint32_t>(w2 >> 32);
+                    y = fma_pair(tanh2[5], w2, tanh2[4]);
 #pragma unroll
-                    for (int i = 4; i >= 0; --i) fma2(y0, y1, y0, y1, w0, w1, p.tanh_k[i], p.tanh_k[i]);
+                    for (int i = 3; i >= 0; --i) y = fma_pair(y, w2, tanh2[i]);
+                };
+                // cap tanh(s / cap) + bias by 1 - 2 / (1 + e^(2 s / cap)), in log2 units
+                auto cap_mufu = [&](float s, float b) {
+                    return fmaf(-2.f * p.cap_log2, fast_rcp(1.f + fast_exp2(s * p.cap_in)), p.cap_log2 + b);
+                };
+                // One bit per key: keys before pr, and from lw up to h (none for a row
+                // without a query), in blocks that are there.
+                auto visible = [&](uint32_t (&vis)[kBN / 32]) {
+                    const int h = pos + 1 - k0, pr = pos < 0 ? 0 : pre_all - k0;
+                    const int lw = a.window > 0 ? h - a.window : 0;
+#pragma unroll
+                    for (int q = 0; q < kBN / 32; ++q) {
+                        vis[q] = bits_below(pr - 32 * q) | (bits_below(h - 32 * q) & ~bits_below(lw - 32 * q));
+                        if (have != full) vis[q] &= present(have, q, B);
+                    }
                 };
                 uint32_t w[kBN / 2];       // the weights, packed
                 float sum = 0.f;
                 load_raw();
-                // First against the reference as it is, if every key is visible
-                // (and, for the distance bias, none is ahead of the row).
+                // First against the reference as it is (with the distance bias: if no
+                // visible key is ahead of the row).
                 bool done_fast = false;
-                const bool fast = all_visible && (!kAlibi || k0 + kBN - 1 <= wmin) && warp_all(m != -INFINITY);
-                if (fast) {
+                const bool fast = (!kAlibi || pre_all <= k0 || k0 + kBN - 1 <= wmin) && warp_all(m != -INFINITY);
+                uint32_t any = 0;
+                auto weights = [&](auto masked) {
+                    uint32_t vis[kBN / 32];
+                    if constexpr (decltype(masked)::value) visible(vis);
                     float sums[4] = {0.f, 0.f, 0.f, 0.f};
-                    uint32_t any = 0;
                     // exponent of key e: score + bias, the distance bias being
                     // slope (k0 + e - pos), rising along the tile
                     const float bias = kBias - m + (kAlibi ? slope * static_cast<float>(k0 - pos) : 0.f);
@@ -646,11 +675,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                             b1 = fmaf(slope, static_cast<float>(e + 1), bias);
                         }
                         if constexpr (kCap) {
-                            float v0, v1;
-                            cap_poly(x[e], x[e + 1], v0, v1, y0, y1, any);
-                            fma2(y0, y1, v0, v1, y0, y1, b0, b1);
+                            if (e % 8 == 6) {
+                                // one pair in four by the special-function unit, which
+                                // has time left: its two operations take 12 cycles an
+                                // element, the polynomial's products 10 of the FMA pipe
+                                y0 = cap_mufu(x[e], b0);
+                                y1 = cap_mufu(x[e + 1], b1);
+                            } else {
+                                uint64_t v, y;
+                                cap_poly(x[e], x[e + 1], v, y, any);
+                                split_pair(fma_pair(v, y, make_pair(b0, b1)), y0, y1);
+                            }
                         } else {
                             fma2(y0, y1, x[e], x[e + 1], c, c, b0, b1);
+                        }
+                        if constexpr (decltype(masked)::value) {
+                            y0 = (vis[e / 32] >> (e % 32)) & 1 ? y0 : -INFINITY;
+                            y1 = (vis[e / 32] >> (e % 32 + 1)) & 1 ? y1 : -INFINITY;
                         }
                         y0 = fast_exp2(y0);
                         y1 = fast_exp2(y1);
@@ -658,9 +699,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         w[e / 2] = pack_pair<kBf16>(y0, y1);
                     }
                     sum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
-                    // a sum of at most 2^14 proves that no weight is larger; v^2 < 2
+                };
+                if (fast) {
+                    if (all_visible)
+                        weights(std::false_type{});
+                    else
+                        weights(std::true_type{});
+                    // the sum bounds every weight; v^2 < 2
                     // that the polynomial holds (no bit pattern reaches that of 2)
-                    done_fast = warp_all(sum <= 16384.f && any < 0x40000000u);
+                    done_fast = warp_all(sum <= kMostSum<kBf16> && any < 0x40000000u);
                     if (!done_fast) load_raw();
                 }
                 if (!done_fast) {
@@ -673,14 +720,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (warp_all(any < 0x40000000u)) {
 #pragma unroll
                             for (int e = 0; e < kBN; e += 2) {
-                                float v0, v1, y0, y1;
-                                cap_poly(x[e], x[e + 1], v0, v1, y0, y1, any);
-                                mul2(x[e], x[e + 1], v0, v1, y0, y1);
+                                uint64_t v, y;
+                                cap_poly(x[e], x[e + 1], v, y, any);
+                                split_pair(mul_pair(v, y), x[e], x[e + 1]);
                             }
                         } else {
 #pragma unroll
                             for (int e = 0; e < kBN; ++e)
-                                x[e] = p.cap_log2 - 2.f * p.cap_log2 * fast_rcp(1.f + fast_exp2(x[e] * p.cap_in));
+                                x[e] = cap_mufu(x[e], 0.f);
                         }
                     } else {
 #pragma unroll
@@ -692,19 +739,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int e = 0; e < kBN; ++e) x[e] -= slope * fabsf(d0 - static_cast<float>(e));
                     }
                     if (!all_visible) {
-                        // one bit per key: keys before pr, and from lw up to h (none
-                        // for a row without a query), in blocks that are there
-                        const int h = pos + 1 - k0, pr = pos < 0 ? 0 : pre_all - k0;
-                        const int lw = a.window > 0 ? h - a.window : 0;
+                        uint32_t vis[kBN / 32];
+                        visible(vis);
 #pragma unroll
-                        for (int q = 0; q < kBN / 32; ++q) {
-                            uint32_t vis = bits_below(pr - 32 * q) |
-                                           (bits_below(h - 32 * q) & ~bits_below(lw - 32 * q));
-                            if (have != full) vis &= present(have, q, B);
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                x[32 * q + e] = (vis >> e) & 1 ? x[32 * q + e] : -INFINITY;
-                        }
+                        for (int e = 0; e < kBN; ++e)
+                            x[e] = (vis[e / 32] >> (e % 32)) & 1 ? x[e] : -INFINITY;
                     }
                     float mx[8];
 #pragma unroll
