@@ -25,10 +25,12 @@
 //  * Warps 9, 10 issue S = Q K^T of query tile 0 and 1 into one of two S/P
 //    buffers of tensor memory, ahead of the softmax, once the P V product that
 //    last read the buffer is complete; warps 11, 12 issue O += P V (P read from
-//    tensor memory) once the softmax has stored P.  One thread issues one
-//    tcgen05.mma per 90 to 110 cycles whatever its size, so the four streams
-//    have threads of their own: with S and P V of a tile issued by one thread,
-//    a step of 64 keys took 2600 cycles, all of them the thread's.
+//    tensor memory) once the softmax has stored P.  A thread's stream of
+//    tcgen05.mma is bound by its own issue and waits, so the four streams have
+//    warps of their own: with S and P V of a tile issued by one thread, a step
+//    of 64 keys took 2600 cycles, all of them the thread's.  The issuing lane
+//    is an elected one (1552 TFLOP/s on an 8192-token prompt; 1416 under
+//    `lane == 0`, where every operand is moved to a uniform register first).
 //  * Warps 0-3 / 4-7 (softmax of tile 0 / 1): thread = row = tensor-memory
 //    lane.  Loads its 64 scores, exponentiates, and stores the weights as
 //    16-bit values over the scores.  Weights are first taken against the
@@ -478,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
         } else if (warp >= kSWarp0 && warp < kPvWarp0 + 2) {
             // -------------------------------------------------------- products
-            if (lane == 0) {
+            if (elect_one()) {
                 const bool is_s = warp < kPvWarp0;
                 const int t = warp - (is_s ? kSWarp0 : kPvWarp0);
                 constexpr uint32_t idesc_s = instr_desc(kBf16, false, kBN);

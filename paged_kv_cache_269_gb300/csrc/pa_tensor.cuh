@@ -22,6 +22,15 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo, uint
     return d;
 }
 
+// One lane of a converged warp.  Under this predicate the compiler keeps
+// operands of tcgen05 and bulk copies in uniform registers; under `lane == 0`
+// it moves them there for each instruction.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
 // D (tensor memory) [+]= A (shared memory) * B (shared memory)
 __device__ __forceinline__ void mma_ss(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t idesc,
                                        bool accumulate) {
