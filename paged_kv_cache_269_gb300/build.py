@@ -4,6 +4,10 @@ Each translation unit under csrc/ is compiled by nvcc in parallel for
 `-gencode arch=compute_103a,code=sm_103a` only, then linked into
 paged_kv_cache_269_gb300/_lib/libpa.so with the static CUDA runtime.
 A rebuild happens when any source or header is newer than the library.
+
+build_marshal() compiles csrc/py/pa_marshal.cpp, the Python module that calls
+libpa for the grouped operators without interpreted checks, against the
+installed torch's headers.
 """
 from __future__ import annotations
 
@@ -81,6 +85,34 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
     return LIB_PATH
+
+
+MARSHAL_SRC = os.path.join(CSRC, "py", "pa_marshal.cpp")
+MARSHAL_PATH = os.path.join(LIB_DIR, "pa_marshal.so")
+
+
+def build_marshal(force: bool = False) -> str:
+    """Compile (if needed) and return the path of the marshalling module."""
+    import sysconfig
+
+    import torch
+    inputs = (MARSHAL_SRC, os.path.join(INCLUDE, "pa.h"), __file__, torch.__file__)
+    if not force and os.path.exists(MARSHAL_PATH) and all(
+            os.path.getmtime(p) <= os.path.getmtime(MARSHAL_PATH) for p in inputs):
+        return MARSHAL_PATH
+    os.makedirs(LIB_DIR, exist_ok=True)
+    base = os.path.dirname(torch.__file__)
+    inc = os.path.join(base, "include")
+    tmp = MARSHAL_PATH + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", MARSHAL_SRC, "-o", tmp,
+           "-I", INCLUDE, "-I", inc, "-I", os.path.join(inc, "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], "-L", os.path.join(base, "lib"), "-ltorch_python",
+           "-ltorch_cpu", "-lc10", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {MARSHAL_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, MARSHAL_PATH)
+    return MARSHAL_PATH
 
 
 if __name__ == "__main__":

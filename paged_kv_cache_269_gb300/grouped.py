@@ -18,17 +18,38 @@ import ctypes
 import functools
 
 torch = Tensor = _I32 = _F32 = _U8 = _raw_stream = _package = None
+_marshal = None        # the compiled marshalling module: one call per operator
+_get_device = _capturing = None
+_addresses: dict = {}  # of the library's functions, for _marshal
 
 
 def _init():
     """Imports what the calls need, at the first one (the package itself, with
     its block manager, works without torch)."""
-    global torch, Tensor, _I32, _F32, _U8, _raw_stream, _package
+    global torch, Tensor, _I32, _F32, _U8, _raw_stream, _package, _marshal, _get_device, _capturing
+    import importlib.util
+
     import torch as torch_
     import paged_kv_cache_269_gb300 as package
     torch, Tensor, _package = torch_, torch_.Tensor, package
     _I32, _F32, _U8 = torch.int32, torch.float32, torch.uint8
-    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    c = torch._C
+    if not all(hasattr(c, n) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice",
+                                       "_cuda_isCurrentStreamCapturing")):
+        return             # a torch without CUDA: the checks refuse every tensor
+    if not torch.cuda.is_available():
+        return
+    torch.cuda.init()
+    _raw_stream, _get_device = c._cuda_getCurrentRawStream, c._cuda_getDevice
+    _capturing = c._cuda_isCurrentStreamCapturing
+    l = package.lib()
+    for name in ("pa_rope_and_cache", "pa_decode_grouped", "pa_decode_grouped_workspace_bytes",
+                 "pa_decode_grouped_counters_bytes", "pa_prefill_grouped",
+                 "pa_prefill_grouped_workspace_bytes", "pa_prefill_grouped_counters_bytes"):
+        _addresses[name] = ctypes.cast(getattr(l, name), ctypes.c_void_p).value
+    spec = importlib.util.spec_from_file_location("pa_marshal", package._build.build_marshal())
+    _marshal = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(_marshal)
 
 
 class AttnOpts(ctypes.Structure):
@@ -161,6 +182,15 @@ def rope_and_cache(q_out, q, k, v, k_cache, v_cache, positions, cos_sin, slot_ma
     (i, i + rotary_dim / 2).  slot < 0 skips the token's k and v, a negative
     position the whole token."""
     pa = _pa()
+    if _marshal is not None:
+        device = _get_device()
+        rc = _marshal.rope(q_out, q, k, v, k_cache, v_cache, positions, cos_sin, slot_mapping, interleaved,
+                           device, _raw_stream(device) if stream is None else stream.cuda_stream,
+                           _addresses["pa_rope_and_cache"])
+        if rc == 0:
+            return q_out
+        if rc is not None:
+            pa._check(rc, "pa_rope_and_cache")
     index, dev, code, et, (N, H, B, D) = _caches(k_cache, v_cache)
     if torch.cuda.current_device() != index:
         with torch.cuda.device(index):
@@ -239,6 +269,21 @@ def _buffers_for(index, stream, counters_bytes, workspace_bytes):
                 ws = torch.empty(nw, dtype=_U8, device=index)
             _buffers[key] = (ctr, ws, nc, nw)
             return ctr, ws
+
+
+def _known_buffers(stream, counters, workspace):
+    """(device, stream handle, counters, workspace) for a call that can be
+    marshalled as it stands: the caller's buffers, or the stream's cached ones
+    outside a capture; counters None otherwise."""
+    device = _get_device()
+    handle = _raw_stream(device) if stream is None else stream.cuda_stream
+    if counters is None or workspace is None:
+        got = _buffers.get((device, handle))
+        if got is None or stream is not None or _capturing():
+            return device, handle, None, None
+        return (device, handle, got[0] if counters is None else counters,
+                got[1] if workspace is None else workspace)
+    return device, handle, counters, workspace
 
 
 def reset_counters():
@@ -348,6 +393,18 @@ def decode_grouped(out, q, k_cache, v_cache, block_tables, context_lens, scale, 
     (uint8) and counters (zeroed int32): see the _bytes functions; by default
     cached per stream, or taken from the graph's pool inside a capture."""
     pa = _pa()
+    if _marshal is not None:
+        device, handle, counters_, workspace_ = _known_buffers(stream, counters, workspace)
+        if counters_ is not None:
+            rc = _marshal.decode(out, q, k_cache, v_cache, block_tables, context_lens, scale, softcap,
+                                 alibi_slopes, window, prefix_lens, counters_, workspace_, device, handle,
+                                 _addresses["pa_decode_grouped"],
+                                 _addresses["pa_decode_grouped_workspace_bytes"],
+                                 _addresses["pa_decode_grouped_counters_bytes"])
+            if rc == 0:
+                return out
+            if rc is not None:
+                pa._check(rc, "pa_decode_grouped")
     index, dev, S, Hq, sizes, MB, rows, head, dims, opts = _attention_args(
         "decode_grouped", out, q, k_cache, v_cache, block_tables, context_lens, softcap, alibi_slopes,
         window, prefix_lens)
@@ -380,6 +437,18 @@ def prefill_grouped(out, q, k_cache, v_cache, block_tables, context_lens, query_
     The rest as decode_grouped; a query at position p sees keys up to p, and
     the first prefix_lens[s] keys wherever it stands."""
     pa = _pa()
+    if _marshal is not None and max_query_len is not None:
+        device, handle, counters_, workspace_ = _known_buffers(stream, counters, workspace)
+        if counters_ is not None:
+            rc = _marshal.prefill(out, q, k_cache, v_cache, block_tables, context_lens, scale, softcap,
+                                  alibi_slopes, window, prefix_lens, counters_, workspace_, device, handle,
+                                  query_start, max_query_len, _addresses["pa_prefill_grouped"],
+                                  _addresses["pa_prefill_grouped_workspace_bytes"],
+                                  _addresses["pa_prefill_grouped_counters_bytes"])
+            if rc == 0:
+                return out
+            if rc is not None:
+                pa._check(rc, "pa_prefill_grouped")
     index, dev, S, Hq, sizes, MB, rows, head, dims, opts = _attention_args(
         "prefill_grouped", out, q, k_cache, v_cache, block_tables, context_lens, softcap, alibi_slopes,
         window, prefix_lens)

@@ -4,21 +4,30 @@ import pytest
 import torch
 
 import paged_kv_cache_269_gb300 as pa
+from paged_kv_cache_269_gb300 import grouped
 from grouped_ref import make_case, reference, rope_bound, rotate
 
 pytestmark = pytest.mark.gpu
 F16, BF16 = torch.float16, torch.bfloat16
 
 
-@pytest.fixture(scope="module")
-def dev():
+@pytest.fixture(scope="module", params=["marshalled", "checked"])
+def dev(request):
+    """Each test runs through the compiled marshalling module, and through the
+    Python checks that take over from it."""
     if not torch.cuda.is_available():
         pytest.skip("no CUDA device")
     d = torch.device("cuda", 0)
     torch.cuda.set_device(d)
     pa.lib()
     pa.device_errors()
-    return d
+    grouped._pa()
+    known = grouped._marshal
+    assert known is not None
+    if request.param == "checked":
+        grouped._marshal = None
+    yield d
+    grouped._marshal = known
 
 
 def to_dev(c, dev):
@@ -429,6 +438,50 @@ def test_rope_errors(dev):
         pa.rope_and_cache(qo, q.float(), k, v, *args)
     with pytest.raises(pa.PaError):
         pa.rope_and_cache(qo, q, k, v, kc, vc, args[2], pa.rope_table(5000, 24, device=dev), args[4])
+
+
+def test_marshalled_calls_leave_odd_ones_to_the_checks(dev):
+    """What the marshalling module does not take as it stands gets the Python
+    checks' answer: an error, or the call made another way."""
+    c = make_case(60, [40, 7], [1, 1], 4, 2, 64, 16, F16)
+    d = to_dev(c, dev)
+    out = torch.empty_like(d["q"])
+    args = [out, d["q"], d["k_cache"], d["v_cache"], d["tables"], d["lens"], c.scale]
+
+    def refused(kind, i, value, **kw):
+        bad = list(args)
+        bad[i] = value
+        with pytest.raises(kind):
+            pa.decode_grouped(*bad, **kw)
+
+    refused(ValueError, 0, out[:1])
+    refused(TypeError, 1, d["q"].float())
+    refused(ValueError, 1, c.q)                                    # on the host
+    refused(TypeError, 2, d["k_cache"].float())
+    refused(ValueError, 3, d["v_cache"][:-1])
+    refused(ValueError, 3, d["v_cache"].transpose(2, 3))
+    refused(TypeError, 4, d["tables"].long())
+    refused(ValueError, 5, d["lens"][:1])
+    refused(ValueError, 5, d["lens"].repeat(4)[::4])               # strided
+    refused(TypeError, 5, None)
+    refused(ValueError, 6, c.scale, alibi_slopes=torch.ones(3, device=dev))
+    refused(TypeError, 6, c.scale, prefix_lens=torch.zeros(2, device=dev))
+    refused(pa.PaError, 6, c.scale, window=-1)
+    refused(pa.PaError, 6, c.scale, softcap=-2.0)
+    refused(pa.PaError, 6, float("nan"))
+    refused(pa.PaError, 6, c.scale, workspace=torch.empty(16, dtype=torch.uint8, device=dev),
+            counters=torch.zeros(8192, dtype=torch.int32, device=dev))
+    empty = [t[:0] for t in (out, d["q"])] + args[2:4] + [d["tables"][:0], d["lens"][:0], c.scale]
+    assert pa.decode_grouped(*empty).shape[0] == 0
+    assert pa.device_errors() == 0
+    check(c, run_decode(c, d), False)
+    none = torch.empty(0, 4, 64, dtype=F16, device=dev)
+    kv = torch.empty(0, 2, 64, dtype=F16, device=dev)
+    i0 = torch.empty(0, dtype=torch.int32, device=dev)
+    pa.rope_and_cache(none, none, kv, kv, d["k_cache"], d["v_cache"], i0, pa.rope_table(8, 64, device=dev), i0)
+    pa.prefill_grouped(none, none, d["k_cache"], d["v_cache"], d["tables"][:0], d["lens"][:0],
+                       torch.zeros(1, dtype=torch.int32, device=dev), c.scale)
+    assert pa.device_errors() == 0
 
 
 # ------------------------------------------------------------------ together
