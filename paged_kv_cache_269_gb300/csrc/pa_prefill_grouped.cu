@@ -338,14 +338,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp == kTmaWarp) {
             // -------------------------------------------------------- items, Q, K
             uint32_t g = 0;                        // K tiles issued, over all items
+            bool first_item = true;
             int k = 0, q_loads = 0;                // items published, Q loads issued
             bool ok = true;
             for (;;) {
                 int w = 0;
                 Item it;
                 for (;;) {
-                    if (lane == 0) w = static_cast<int>(atomicAdd(a.counters, 1u));
-                    w = __shfl_sync(0xffffffffu, w, 0);
+                    // the first item by the CTA's index, the rest from the queue
+                    if (first_item) {
+                        w = blockIdx.x;
+                        first_item = false;
+                    } else {
+                        if (lane == 0) w = static_cast<int>(gridDim.x + atomicAdd(a.counters, 1u));
+                        w = __shfl_sync(0xffffffffu, w, 0);
+                    }
                     if (static_cast<unsigned>(w) >= static_cast<unsigned>(p.num_items)) break;
                     if (item_geometry(p, w, lane == 0, it)) break;
                 }
@@ -361,8 +368,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive(&bar[C::ITEM_FULL + slot]);
                 }
                 if (done) break;
+                auto load_q = [&]() {
+                    if (lane == 0) {
+                        const int nt = it.nk1 >= 0 ? 2 : 1;
+                        mbar_arrive_expect_tx(&bar[C::Q_FULL],
+                                              static_cast<uint32_t>(nt * p.tpt * p.group * D * 2));
+                        for (int t = 0; t < nt; ++t)
+                            for (int hf = 0; hf < C::kHalves; ++hf)
+                                tma_load_3d(smem + C::OFF_Q + t * C::kTileQ + hf * C::kHalfQ, &tm_q, hf * 64,
+                                            it.hk * p.group, it.q_first + it.tok0 + t * p.tpt, &bar[C::Q_FULL]);
+                    }
+                    ++q_loads;
+                    __syncwarp();
+                };
                 KeyBlocks blocks(a, it.s, it.hk, it.ctx, it.pre, it.q_len, b_shift, lane, kAlibi);
                 int blk = blocks.entry(it, 0);
+                // Q at once where the previous item's S products are complete
+                if (k == 0 || warp_all(mbar_test(&bar[C::Q_EMPTY], (k - 1) & 1))) load_q();
                 for (int j = 0; j < it.nkt; ++j) {
                     const int next = j + 1 < it.nkt ? blocks.entry(it, j + 1) : -1;
                     if (blk == -2) atomicOr(a.err, PA_DEVERR_TABLE);
@@ -379,24 +401,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tma_load_4d(smem + C::OFF_K + st * C::kTileKV + lane * (B / 8) * C::kGroup, &tm_k, 0, 0, 0,
                                     blocks.group(blk), &bar[C::K_FULL + st]);
                     ++g;
-                    // Q, once the previous item's S products are complete
-                    if (j == 0) {
-                        if (k > 0) {
-                            ok = warp_all(mbar_wait(&bar[C::Q_EMPTY], (k - 1) & 1, abort_flag, a.err));
-                            if (!ok) break;
-                        }
-                        if (lane == 0) {
-                            const int nt = it.nk1 >= 0 ? 2 : 1;
-                            mbar_arrive_expect_tx(&bar[C::Q_FULL],
-                                                  static_cast<uint32_t>(nt * p.tpt * p.group * D * 2));
-                            for (int t = 0; t < nt; ++t)
-                                for (int hf = 0; hf < C::kHalves; ++hf)
-                                    tma_load_3d(smem + C::OFF_Q + t * C::kTileQ + hf * C::kHalfQ, &tm_q,
-                                                hf * 64, it.hk * p.group,
-                                                it.q_first + it.tok0 + t * p.tpt, &bar[C::Q_FULL]);
-                        }
-                        ++q_loads;
-                        __syncwarp();
+                    // Q, unless it could be loaded first
+                    if (j == 0 && q_loads == k) {
+                        ok = warp_all(mbar_wait(&bar[C::Q_EMPTY], (k - 1) & 1, abort_flag, a.err));
+                        if (!ok) break;
+                        load_q();
                     }
                     blk = next;
                 }
@@ -875,26 +884,49 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint16_t *dst = a.out + (static_cast<size_t>(it->q_first + it->tok0 + t * p.tpt + tok) * a.num_q_heads +
                                              it->hk * p.group + head) * D;
                     __threadfence();
-                    float top = -INFINITY;
-                    for (int z = 0; z < splits; ++z)
-                        top = fmaxf(top, __ldcg(base + static_cast<size_t>(z) * 2 * kPart + D * kBM));
-                    float total = 0.f;
-                    for (int z = 0; z < splits; ++z) {
-                        const float *src = base + static_cast<size_t>(z) * 2 * kPart;
-                        const float mz = __ldcg(src + D * kBM);
-                        total += (mz == -INFINITY ? 0.f : fast_exp2(mz - top)) * __ldcg(src + (D + 1) * kBM);
+                    // four splits at a time, so that their loads share a round trip
+                    // (one by one, joining three took 13000 cycles)
+                    constexpr int kZ = 4;
+                    auto part = [&](int z) {
+                        return base + static_cast<size_t>(min(z, splits - 1)) * 2 * kPart;
+                    };
+                    float top = -INFINITY, total = 0.f;
+                    for (int z0 = 0; z0 < splits; z0 += kZ) {
+                        float mz[kZ], lz[kZ], t2 = top;
+#pragma unroll
+                        for (int z = 0; z < kZ; ++z) {
+                            mz[z] = __ldcg(part(z0 + z) + D * kBM);
+                            lz[z] = __ldcg(part(z0 + z) + (D + 1) * kBM);
+                        }
+#pragma unroll
+                        for (int z = 0; z < kZ; ++z) t2 = fmaxf(t2, mz[z]);
+                        if (top != -INFINITY) total *= fast_exp2(top - t2);
+                        top = t2;
+#pragma unroll
+                        for (int z = 0; z < kZ; ++z)
+                            if (z0 + z < splits && mz[z] != -INFINITY) total += fast_exp2(mz[z] - top) * lz[z];
                     }
                     const float inv = total > 0.f ? 1.f / total : 0.f;
+#pragma unroll 1
                     for (int q = 0; q < D / 16; ++q) {
                         float acc[16];
 #pragma unroll
                         for (int e = 0; e < 16; ++e) acc[e] = 0.f;
-                        for (int z = 0; z < splits; ++z) {
-                            const float *src = base + static_cast<size_t>(z) * 2 * kPart;
-                            const float mz = __ldcg(src + D * kBM);
-                            const float f = mz == -INFINITY ? 0.f : fast_exp2(mz - top);
+#pragma unroll 1
+                        for (int z0 = 0; z0 < splits; z0 += kZ) {
+                            float v[kZ][16], f[kZ];
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) acc[e] += f * __ldcg(src + (q * 16 + e) * kBM);
+                            for (int z = 0; z < kZ; ++z) {
+                                f[z] = __ldcg(part(z0 + z) + D * kBM);
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) v[z][e] = __ldcg(part(z0 + z) + (q * 16 + e) * kBM);
+                            }
+#pragma unroll
+                            for (int z = 0; z < kZ; ++z) {
+                                f[z] = z0 + z < splits && f[z] != -INFINITY ? fast_exp2(f[z] - top) : 0.f;
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) acc[e] += f[z] * v[z][e];
+                            }
                         }
 #pragma unroll
                         for (int e = 0; e < 16; e += 8) {
