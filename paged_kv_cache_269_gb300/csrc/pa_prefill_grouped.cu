@@ -54,8 +54,11 @@
 //  * Few rows over long contexts: an item's key tiles are split over several
 //    CTAs, which leave partial (max, sum, output) and take a ticket; the last
 //    one joins them in order.
-//  * The output rows go through a staging buffer in shared memory, so that a
-//    warp writes whole 128-byte lines (row by row they cost 6400 cycles an item).
+//  * The output rows go through a staging buffer in shared memory and leave as
+//    one tensor copy per warp and 64 dims, while the softmax goes on with the
+//    next item (row by row they cost 6400 cycles an item, by coalesced stores
+//    3800).  Rows that are not 32 of whole tokens (a ragged end, or G that does
+//    not divide 32) take the coalesced stores.
 //  * Every wait is bounded; tensor memory is released on every path.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -103,6 +106,7 @@ struct PrefillGroupedArgs {
     float tanh_k[6];                   // there, x = v (k0 + k1 v^2 + ... + k5 v^10)
     int group, tpt;                    // heads per K/V head; tokens per tile
     int num_pairs, splits;
+    int store_boxes;                   // a warp's 32 rows are whole tokens: tm_out applies
     int num_items;                     // num_pairs * splits * S * Hkv
     float *partials;                   // [item without split][split][tile][D + 2][128]
 };
@@ -295,6 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefill_grouped_kernel(const __grid_constant__ CUtensorMap tm_q,
                            const __grid_constant__ CUtensorMap tm_k,
                            const __grid_constant__ CUtensorMap tm_v,
+                           const __grid_constant__ CUtensorMap tm_out,
                            const __grid_constant__ PrefillGroupedArgs p) {
     using C = Cfg<D>;
     const GroupedArgs &a = p.g;
@@ -819,8 +824,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint16_t *base = a.out + (static_cast<size_t>(it->q_first + it->tok0 + t * p.tpt) * a.num_q_heads +
                                           it->hk * p.group) * D;
                 const int my_row = live ? tok * a.num_q_heads + head : -1;
-#pragma unroll
+                const bool whole = p.store_boxes && warp_all(live);
+#pragma unroll 1
                 for (int hf = 0; hf < C::kHalves; ++hf) {
+                    // the last copy out of the staging rows has read them
+                    if (lane == 0) bulk_wait_read();
+                    __syncwarp();
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
                         uint32_t ov[32];
@@ -837,14 +846,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                             *reinterpret_cast<uint4 *>(staging + lane * 128 + (((q * 4 + e) ^ (lane & 7)) << 4)) = v;
                         }
                     }
+                    if (whole) {
+                        // 32 rows of whole tokens leave as one copy
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0)
+                            tma_store_3d(&tm_out, hf * 64, it->hk * p.group,
+                                         it->q_first + it->tok0 + t * p.tpt + (r - lane) / p.group, staging);
+                        continue;
+                    }
                     __syncwarp();
+                    // four rows a step, 128 bytes of each; all loads before the
+                    // stores, which the compiler cannot tell apart from them
+                    uint4 v[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {   // four rows a step, 128 bytes of each
-                        const int rr = i * 4 + lane / 8, cc = lane % 8;
-                        const int row_at = __shfl_sync(0xffffffffu, my_row, rr);
-                        const uint4 v = *reinterpret_cast<const uint4 *>(staging + rr * 128 + ((cc ^ (rr & 7)) << 4));
+                    for (int i = 0; i < 8; ++i) {
+                        const int rr = i * 4 + lane / 8;
+                        v[i] = *reinterpret_cast<const uint4 *>(staging + rr * 128 + (((lane % 8) ^ (rr & 7)) << 4));
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int row_at = __shfl_sync(0xffffffffu, my_row, i * 4 + lane / 8);
                         if (row_at >= 0)
-                            *reinterpret_cast<uint4 *>(base + static_cast<size_t>(row_at) * D + hf * 64 + cc * 8) = v;
+                            *reinterpret_cast<uint4 *>(base + static_cast<size_t>(row_at) * D + hf * 64 +
+                                                       (lane % 8) * 8) = v[i];
                     }
                     __syncwarp();
                 }
@@ -943,6 +968,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[C::ITEM_EMPTY + slot]);
         }
+        if (lane == 0) bulk_wait_all();   // copies out of shared memory that this CTA still holds
     }
     tc_fence_before();
     __syncthreads();
@@ -966,7 +992,7 @@ Plan make_plan(int num_seqs, int num_kv_heads, int group, int max_q) {
     return pl;
 }
 
-using Kernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, PrefillGroupedArgs);
+using Kernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, PrefillGroupedArgs);
 template <bool kBf16, int D>
 Kernel pick(bool cap, bool alibi) {
     return cap ? (alibi ? prefill_grouped_kernel<kBf16, D, true, true> : prefill_grouped_kernel<kBf16, D, true, false>)
@@ -1017,17 +1043,21 @@ cudaError_t launch_prefill_grouped(const GroupedArgs &args, int dtype, int head_
     p.num_items = static_cast<int>(items);
     p.partials = static_cast<float *>(args.workspace);
 
-    CUtensorMap tm_q, tm_k, tm_v;
+    p.store_boxes = 32 % p.group == 0;
+    CUtensorMap tm_q, tm_k, tm_v, tm_out;
     const cuuint64_t q_dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(Hq),
                                   static_cast<cuuint64_t>(args.total_q)};
     const cuuint64_t q_strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(Hq) * D * 2};
     const cuuint32_t q_box[3] = {64, static_cast<cuuint32_t>(p.group), static_cast<cuuint32_t>(p.tpt)};
+    const cuuint32_t out_box[3] = {64, static_cast<cuuint32_t>(p.store_boxes ? p.group : 1),
+                                   static_cast<cuuint32_t>(p.store_boxes ? 32 / p.group : 1)};
     // groups of 8 keys x 64-dim halves x keys x dims: a box is one block of a head
     const cuuint64_t kv_dims[4] = {64, 8, static_cast<cuuint64_t>(D / 64),
                                    static_cast<cuuint64_t>(args.num_blocks) * Hk * (B / 8)};
     const cuuint64_t kv_strides[3] = {static_cast<cuuint64_t>(D) * 2, 128, static_cast<cuuint64_t>(D) * 16};
     const cuuint32_t kv_box[4] = {64, 8, static_cast<cuuint32_t>(D / 64), static_cast<cuuint32_t>(B / 8)};
     if (!encode(&tm_q, bf16, args.q, 3, q_dims, q_strides, q_box) ||
+        !encode(&tm_out, bf16, args.out, 3, q_dims, q_strides, out_box) ||
         !encode(&tm_k, bf16, args.k_cache, 4, kv_dims, kv_strides, kv_box) ||
         !encode(&tm_v, bf16, args.v_cache, 4, kv_dims, kv_strides, kv_box))
         return cudaErrorInvalidValue;
@@ -1062,7 +1092,7 @@ cudaError_t launch_prefill_grouped(const GroupedArgs &args, int dtype, int head_
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    void *params[] = {&tm_q, &tm_k, &tm_v, &p};
+    void *params[] = {&tm_q, &tm_k, &tm_v, &tm_out, &p};
     return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void *>(kernel), params);
 }
 
