@@ -94,6 +94,7 @@ constexpr float kRaise = 8.f;          // where a maximum is taken, it is kept i
 // reference hardly ever has to be raised.
 constexpr float kBias = 4.f;
 template <bool kBf16> constexpr float kMostSum = kBf16 ? 1.1529215e18f : 32768.f;   // 2^60, 2^15
+constexpr float kFar = 1e30f;
 constexpr int kMaskRing = 16;
 // Work is split over keys while there are fewer items than SMs (152).
 constexpr int kSplitTarget = 152;
@@ -131,21 +132,21 @@ struct Cfg {
     static constexpr int kTileQ = kHalves * kHalfQ;
     static constexpr int kGroup = kHalves * 1024;  // 8 keys of a K or V tile
     static constexpr int kTileKV = kBN / 8 * kGroup;
-    static constexpr int kSlots = D == 64 ? 6 : 4;  // tiles of K, and of V
-    // tensor memory: S/P buffer b of tile t at columns 128 t + 64 b, then O
-    static constexpr uint32_t TM_O = 256;
+    static constexpr int kSlots = D == 64 ? 8 : 3;  // tiles of K, and of V
+    // tensor memory: S/P buffer b of tile t at columns 64 (kBufs t + b), then O.
+    // A third buffer (head_dim 64 leaves room) takes P V out of the next S's way.
+    static constexpr uint32_t kBufs = D == 64 ? 3 : 2;
+    static constexpr uint32_t TM_O = 2 * kBufs * 64;
     static_assert(TM_O + 2 * D <= kTmemCols, "tensor memory");
-    static constexpr int kStagingWarp = 32 * 128;  // 32 rows x 64 dims
-    static constexpr int OFF_Q = 0;
-    static constexpr int OFF_K = 2 * kTileQ;
+    static constexpr int OFF_Q = 0;                              // [item parity][tile]
+    static constexpr int OFF_K = 4 * kTileQ;
     static constexpr int OFF_V = OFF_K + kSlots * kTileKV;
-    static constexpr int OFF_STAGING = OFF_V + kSlots * kTileKV;
-    static constexpr int OFF_BAR = OFF_STAGING + 8 * kStagingWarp;
-    static constexpr int Q_FULL = 0, Q_EMPTY = 1, V_LAND = 2;
-    static constexpr int S_FULL = 3, P_FULL = 7, PV_DONE = 11;   // [tile][buffer]
-    static constexpr int MMA_DONE = 15;                          // [issuing thread]
-    static constexpr int ITEM_FULL = 19, ITEM_EMPTY = 21;
-    static constexpr int K_FULL = 23, V_FULL = K_FULL + kSlots;
+    static constexpr int OFF_BAR = OFF_V + kSlots * kTileKV;
+    static constexpr int Q_FULL = 0, V_LAND = 2;                 // Q_FULL: [item parity]
+    static constexpr int S_FULL = 3, P_FULL = 9, PV_DONE = 15;   // [tile][buffer]
+    static constexpr int MMA_DONE = 21;                          // [issuing thread]
+    static constexpr int ITEM_FULL = 25, ITEM_EMPTY = 27;
+    static constexpr int K_FULL = 29, V_FULL = K_FULL + kSlots;
     static constexpr int K_EMPTY = V_FULL + kSlots, V_EMPTY = K_EMPTY + kSlots;
     static constexpr int kNumBars = V_EMPTY + kSlots;
     static constexpr int OFF_TMEM = OFF_BAR + kNumBars * 8;
@@ -317,9 +318,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kNumBars; ++i) {
             uint32_t count = 1;
-            if (i >= C::P_FULL && i < C::P_FULL + 4) count = 4;               // softmax warps
+            if (i >= C::P_FULL && i < C::P_FULL + 6) count = 4;               // softmax warps
             if (i == C::ITEM_EMPTY || i == C::ITEM_EMPTY + 1) count = 13;     // 4 MMA threads, 8 softmax warps, V
-            if (i == C::Q_EMPTY || i >= C::K_EMPTY) count = 2;               // both tiles' threads
+            if (i >= C::K_EMPTY) count = 2;               // both tiles' threads
             mbar_init(&bar[i], count);
         }
         *abort_flag = 0;
@@ -344,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // -------------------------------------------------------- items, Q, K
             uint32_t g = 0;                        // K tiles issued, over all items
             bool first_item = true;
-            int k = 0, q_loads = 0;                // items published, Q loads issued
+            int k = 0, q_loads = 0;                // items whose K is issued, Q loads issued
             bool ok = true;
             for (;;) {
                 int w = 0;
@@ -373,23 +374,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive(&bar[C::ITEM_FULL + slot]);
                 }
                 if (done) break;
-                auto load_q = [&]() {
-                    if (lane == 0) {
-                        const int nt = it.nk1 >= 0 ? 2 : 1;
-                        mbar_arrive_expect_tx(&bar[C::Q_FULL],
-                                              static_cast<uint32_t>(nt * p.tpt * p.group * D * 2));
-                        for (int t = 0; t < nt; ++t)
-                            for (int hf = 0; hf < C::kHalves; ++hf)
-                                tma_load_3d(smem + C::OFF_Q + t * C::kTileQ + hf * C::kHalfQ, &tm_q, hf * 64,
-                                            it.hk * p.group, it.q_first + it.tok0 + t * p.tpt, &bar[C::Q_FULL]);
-                    }
-                    ++q_loads;
-                    __syncwarp();
-                };
+                // Q into the buffer of the item before the last, whose roles are done
+                if (lane == 0) {
+                    const int nt = it.nk1 >= 0 ? 2 : 1;
+                    mbar_arrive_expect_tx(&bar[C::Q_FULL + slot],
+                                          static_cast<uint32_t>(nt * p.tpt * p.group * D * 2));
+                    for (int t = 0; t < nt; ++t)
+                        for (int hf = 0; hf < C::kHalves; ++hf)
+                            tma_load_3d(smem + C::OFF_Q + (slot * 2 + t) * C::kTileQ + hf * C::kHalfQ, &tm_q,
+                                        hf * 64, it.hk * p.group, it.q_first + it.tok0 + t * p.tpt,
+                                        &bar[C::Q_FULL + slot]);
+                }
+                ++q_loads;
+                __syncwarp();
                 KeyBlocks blocks(a, it.s, it.hk, it.ctx, it.pre, it.q_len, b_shift, lane, kAlibi);
                 int blk = blocks.entry(it, 0);
-                // Q at once where the previous item's S products are complete
-                if (k == 0 || warp_all(mbar_test(&bar[C::Q_EMPTY], (k - 1) & 1))) load_q();
                 for (int j = 0; j < it.nkt; ++j) {
                     const int next = j + 1 < it.nkt ? blocks.entry(it, j + 1) : -1;
                     if (blk == -2) atomicOr(a.err, PA_DEVERR_TABLE);
@@ -406,12 +405,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tma_load_4d(smem + C::OFF_K + st * C::kTileKV + lane * (B / 8) * C::kGroup, &tm_k, 0, 0, 0,
                                     blocks.group(blk), &bar[C::K_FULL + st]);
                     ++g;
-                    // Q, unless it could be loaded first
-                    if (j == 0 && q_loads == k) {
-                        ok = warp_all(mbar_wait(&bar[C::Q_EMPTY], (k - 1) & 1, abort_flag, a.err));
-                        if (!ok) break;
-                        load_q();
-                    }
                     blk = next;
                 }
                 if (!ok) break;
@@ -419,7 +412,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (lane == 0) {
                 if (!ok) {   // let every copy already issued land
-                    if (q_loads > 0) mbar_wait_drain(&bar[C::Q_FULL], (q_loads - 1) & 1);
+                    for (int i = max(0, k - 1); i <= k; ++i)   // item k's Q may be on its way
+                        if (i < q_loads) mbar_wait_drain(&bar[C::Q_FULL + (i & 1)], (i >> 1) & 1);
                     for (uint32_t i = g > C::kSlots ? g - C::kSlots : 0; i < g; ++i)
                         mbar_wait_drain(&bar[C::K_FULL + i % C::kSlots], (i / C::kSlots) & 1);
                 }
@@ -499,10 +493,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int t = warp - (is_s ? kSWarp0 : kPvWarp0);
                 constexpr uint32_t idesc_s = instr_desc(kBf16, false, kBN);
                 constexpr uint32_t idesc_pv = instr_desc(kBf16, true, D);
-                const uint32_t q_addr = smem_addr(smem + C::OFF_Q) + t * C::kTileQ;
                 const uint32_t kv_addr = smem_addr(smem + (is_s ? C::OFF_K : C::OFF_V));
                 uint64_t *kv_full = &bar[is_s ? C::K_FULL : C::V_FULL], *kv_empty = &bar[is_s ? C::K_EMPTY : C::V_EMPTY];
-                const uint32_t tm_s = tmem + t * 128, tm_o = tmem + C::TM_O + t * D;
+                const uint32_t tm_s = tmem + t * C::kBufs * 64, tm_o = tmem + C::TM_O + t * D;
                 uint32_t g = 0;              // K (V) tiles seen
                 uint32_t n = 0;              // products of this thread, over all items
                 bool ok = true;
@@ -516,10 +509,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive(&bar[C::ITEM_EMPTY + slot]);
                     if (done) break;
                     if (is_s) {
-                        ok = mbar_wait(&bar[C::Q_FULL], k & 1, abort_flag, a.err);
+                        ok = mbar_wait(&bar[C::Q_FULL + slot], (k / 2) & 1, abort_flag, a.err);
                         if (!ok) break;
-                        if (nk == 0) mbar_arrive(&bar[C::Q_EMPTY]);
                     }
+                    const uint32_t q_addr = smem_addr(smem + C::OFF_Q) + (slot * 2 + t) * C::kTileQ;
                     for (int j = 0; j < nkt; ++j, ++g) {
                         const uint32_t st = g % C::kSlots;
                         ok = mbar_wait(kv_full + st, (g / C::kSlots) & 1, abort_flag, a.err);
@@ -530,11 +523,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                             mbar_arrive(kv_empty + st);
                             continue;
                         }
-                        const uint32_t buf = n & 1, ph = (n >> 1) & 1;
+                        const uint32_t buf = n % C::kBufs, ph = (n / C::kBufs) & 1;
                         const uint32_t kv = kv_addr + st * C::kTileKV;
                         if (is_s) {
                             // the product that last read the buffer's P
-                            if (n >= 2) ok = mbar_wait(&bar[C::PV_DONE + t * 2 + buf], ph ^ 1, abort_flag, a.err);
+                            if (n >= C::kBufs) ok = mbar_wait(&bar[C::PV_DONE + t * 3 + buf], ph ^ 1, abort_flag, a.err);
                             if (!ok) break;
                             tc_fence_after();
 #pragma unroll
@@ -543,17 +536,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 mma_ss(tm_s + buf * 64, smem_desc(q_addr + half * C::kHalfQ + kk * 32, 16, 1024),
                                        smem_desc(kv + half * 1024 + kk * 32, 16, C::kGroup), idesc_s, ks > 0);
                             }
-                            mma_commit(&bar[C::S_FULL + t * 2 + buf]);
-                            if (kAlibi ? jj == 0 : jj == nk - 1) mma_commit(&bar[C::Q_EMPTY]);
+                            mma_commit(&bar[C::S_FULL + t * 3 + buf]);
                         } else {
-                            ok = mbar_wait(&bar[C::P_FULL + t * 2 + buf], ph, abort_flag, a.err);
+                            ok = mbar_wait(&bar[C::P_FULL + t * 3 + buf], ph, abort_flag, a.err);
                             if (!ok) break;
                             tc_fence_after();
 #pragma unroll
                             for (int ks = 0; ks < kBN / 16; ++ks)
                                 mma_ts(tm_o, tm_s + buf * 64 + ks * 8, smem_desc(kv + ks * 2 * C::kGroup, 1024, C::kGroup),
                                        idesc_pv, (kAlibi ? jj < nk - 1 : jj > 0) || ks > 0);
-                            mma_commit(&bar[C::PV_DONE + t * 2 + buf]);
+                            mma_commit(&bar[C::PV_DONE + t * 3 + buf]);
                         }
                         mma_commit(kv_empty + st);
                         ++n;
@@ -571,9 +563,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r = (warp % 4) * 32 + lane;
         const int tok = r / p.group, head = r - tok * p.group;   // within the tile
         const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp % 4) * 32) << 16);
-        const uint32_t s_cols = lane_base + t * 128;
+        const uint32_t s_cols = lane_base + t * C::kBufs * 64;
         const uint32_t o_col = lane_base + C::TM_O + t * D;
-        uint8_t *staging = smem + C::OFF_STAGING + warp * C::kStagingWarp;
         const float c = p.scale_log2;
         const unsigned full = (1u << (kBN >> b_shift)) - 1;
         // the polynomial's coefficients as pairs, kept in registers (volatile: not
@@ -584,6 +575,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 6; ++i) tanh2[i] = keep_pair(p.tanh_k[i]);
             cap_v2 = keep_pair(p.cap_v);
         }
+        // The item before: its slot and its Q buffer, which holds the staged rows,
+        // are handed back once the copies out of it have read them.
+        int pending = -1;
+        auto release = [&]() {
+            if (pending >= 0 && lane == 0) {
+                bulk_wait_read();
+                mbar_arrive(&bar[C::ITEM_EMPTY + pending]);
+            }
+            pending = -1;
+        };
         uint32_t n = 0;            // S tiles consumed
         uint32_t tiles = 0;        // key tiles of all items (mask ring)
         bool ok = true;
@@ -597,12 +598,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool done = it->done;
             const int nk = t == 0 ? it->nk0 : it->nk1;
             if (done) break;
+            // the tile's Q is done with when its last S is: then the warp's output
+            // rows are staged there
+            uint8_t *staging = smem + C::OFF_Q + (slot * 2 + t) * C::kTileQ + (warp % 4) * (C::kTileQ / 4);
             // descending: a tile that needs fewer entries skips the first ones
             const uint32_t tile_base = tiles + (kAlibi ? it->nkt - max(nk, 0) : 0);
             tiles += it->nkt;
             if (nk < 0) {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar[C::ITEM_EMPTY + slot]);
+                release();
+                pending = slot;
                 continue;
             }
             // the row's position, -1 for a row without a query
@@ -620,8 +624,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // a row without a query takes no part (m = 0: no maximum is missing)
             float m = pos >= 0 ? -INFINITY : 0.f, l = 0.f;
             for (int j = 0; j < nk; ++j, ++n) {
-                const uint32_t buf = n & 1;
-                ok = warp_all(mbar_wait(&bar[C::S_FULL + t * 2 + buf], (n >> 1) & 1, abort_flag, a.err));
+                const uint32_t buf = n % C::kBufs;
+                ok = warp_all(mbar_wait(&bar[C::S_FULL + t * 3 + buf], (n / C::kBufs) & 1, abort_flag, a.err));
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t s_col = s_cols + buf * 64;
@@ -677,7 +681,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t any = 0;
                 auto weights = [&](auto masked) {
                     uint32_t vis[kBN / 32];
-                    if constexpr (decltype(masked)::value) visible(vis);
+                    if constexpr (decltype(masked)::value == 2) visible(vis);
+                    const float edge = (static_cast<float>(pos - k0) + 0.5f) * kFar;
                     float sums[4] = {0.f, 0.f, 0.f, 0.f};
                     // exponent of key e: score + bias, the distance bias being
                     // slope (k0 + e - pos), rising along the tile
@@ -705,7 +710,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         } else {
                             fma2(y0, y1, x[e], x[e + 1], c, c, b0, b1);
                         }
-                        if constexpr (decltype(masked)::value) {
+                        if constexpr (decltype(masked)::value == 1) {
+                            // keys up to the row's own: kFar (pos + 1/2 - key) is far above
+                            // every exponent for them, and far below for the rest
+                            y0 = fminf(y0, edge - static_cast<float>(e) * kFar);
+                            y1 = fminf(y1, edge - static_cast<float>(e + 1) * kFar);
+                        }
+                        if constexpr (decltype(masked)::value == 2) {
                             y0 = (vis[e / 32] >> (e % 32)) & 1 ? y0 : -INFINITY;
                             y1 = (vis[e / 32] >> (e % 32 + 1)) & 1 ? y1 : -INFINITY;
                         }
@@ -718,9 +729,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 };
                 if (fast) {
                     if (all_visible)
-                        weights(std::false_type{});
+                        weights(std::integral_constant<int, 0>{});
+                    else if (have == full && a.window == 0 && pre_all <= k0)
+                        weights(std::integral_constant<int, 1>{});
                     else
-                        weights(std::true_type{});
+                        weights(std::integral_constant<int, 2>{});
                     // the sum bounds every weight; v^2 < 2
                     // that the polynomial holds (no bit pattern reaches that of 2)
                     done_fast = warp_all(sum <= kMostSum<kBf16> && any < 0x40000000u);
@@ -777,8 +790,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         m = m_new;
                         l *= alpha;
                         if (j > 0) {   // O, once the product before is complete
-                            ok = warp_all(mbar_wait(&bar[C::PV_DONE + t * 2 + (buf ^ 1)], ((n - 1) >> 1) & 1,
-                                                    abort_flag, a.err));
+                            ok = warp_all(mbar_wait(&bar[C::PV_DONE + t * 3 + (n - 1) % C::kBufs],
+                                                    ((n - 1) / C::kBufs) & 1, abort_flag, a.err));
                             if (!ok) break;
                             tc_fence_after();
 #pragma unroll 1
@@ -808,11 +821,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar[C::P_FULL + t * 2 + buf]);
+                if (lane == 0) mbar_arrive(&bar[C::P_FULL + t * 3 + buf]);
+                if (j == 0) release();
             }
             if (!ok) break;
             if (nk > 0) {
-                ok = warp_all(mbar_wait(&bar[C::PV_DONE + t * 2 + ((n - 1) & 1)], ((n - 1) >> 1) & 1, abort_flag, a.err));
+                ok = warp_all(mbar_wait(&bar[C::PV_DONE + t * 3 + (n - 1) % C::kBufs], ((n - 1) / C::kBufs) & 1, abort_flag,
+                                        a.err));
                 if (!ok) break;
                 tc_fence_after();
             }
@@ -820,60 +835,58 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int splits = it->splits;
             if (splits == 1) {
                 const float inv = l > 0.f ? 1.f / l : 0.f;
-                // rows of the tile's output, from its first token's first head
-                uint16_t *base = a.out + (static_cast<size_t>(it->q_first + it->tok0 + t * p.tpt) * a.num_q_heads +
-                                          it->hk * p.group) * D;
-                const int my_row = live ? tok * a.num_q_heads + head : -1;
                 const bool whole = p.store_boxes && warp_all(live);
-#pragma unroll 1
+#pragma unroll
                 for (int hf = 0; hf < C::kHalves; ++hf) {
-                    // the last copy out of the staging rows has read them
-                    if (lane == 0) bulk_wait_read();
-                    __syncwarp();
+                    uint32_t ov[64];
+                    tmem_ld32_nowait(o_col + hf * 64, *reinterpret_cast<uint32_t(*)[32]>(&ov[0]));
+                    tmem_ld32_nowait(o_col + hf * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&ov[32]));
+                    tmem_ld_wait();
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        uint32_t ov[32];
-                        tmem_ld32_nowait(o_col + hf * 64 + q * 32, ov);
-                        tmem_ld_wait();
+                    for (int e = 0; e < 8; ++e) {
+                        uint4 v;
+                        uint32_t *u = reinterpret_cast<uint32_t *>(&v);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            uint4 v;
-                            uint32_t *u = reinterpret_cast<uint32_t *>(&v);
-#pragma unroll
-                            for (int z = 0; z < 4; ++z)
-                                u[z] = pack_pair<kBf16>(__uint_as_float(ov[e * 8 + 2 * z]) * inv,
-                                                        __uint_as_float(ov[e * 8 + 2 * z + 1]) * inv);
-                            *reinterpret_cast<uint4 *>(staging + lane * 128 + (((q * 4 + e) ^ (lane & 7)) << 4)) = v;
-                        }
+                        for (int z = 0; z < 4; ++z)
+                            u[z] = pack_pair<kBf16>(__uint_as_float(ov[e * 8 + 2 * z]) * inv,
+                                                    __uint_as_float(ov[e * 8 + 2 * z + 1]) * inv);
+                        *reinterpret_cast<uint4 *>(staging + hf * 4096 + lane * 128 + ((e ^ (lane & 7)) << 4)) = v;
                     }
-                    if (whole) {
-                        // 32 rows of whole tokens leave as one copy
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                        __syncwarp();
-                        if (lane == 0)
-                            tma_store_3d(&tm_out, hf * 64, it->hk * p.group,
-                                         it->q_first + it->tok0 + t * p.tpt + (r - lane) / p.group, staging);
-                        continue;
-                    }
-                    __syncwarp();
-                    // four rows a step, 128 bytes of each; all loads before the
-                    // stores, which the compiler cannot tell apart from them
-                    uint4 v[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int rr = i * 4 + lane / 8;
-                        v[i] = *reinterpret_cast<const uint4 *>(staging + rr * 128 + (((lane % 8) ^ (rr & 7)) << 4));
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int row_at = __shfl_sync(0xffffffffu, my_row, i * 4 + lane / 8);
-                        if (row_at >= 0)
-                            *reinterpret_cast<uint4 *>(base + static_cast<size_t>(row_at) * D + hf * 64 +
-                                                       (lane % 8) * 8) = v[i];
-                    }
-                    __syncwarp();
                 }
                 tc_fence_before();
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (whole) {   // 32 rows of whole tokens leave as tensor copies
+                    if (lane == 0) {
+                        const int z = it->q_first + it->tok0 + t * p.tpt + tok;   // lane 0 holds the first row
+                        for (int hf = 0; hf < C::kHalves; ++hf)
+                            tma_store_3d(&tm_out, hf * 64, it->hk * p.group, z, staging + hf * 4096);
+                    }
+                } else {
+                    // rows of the tile's output, from its first token's first head
+                    uint16_t *base = a.out + (static_cast<size_t>(it->q_first + it->tok0 + t * p.tpt) * a.num_q_heads +
+                                              it->hk * p.group) * D;
+                    const int my_row = live ? tok * a.num_q_heads + head : -1;
+#pragma unroll 1
+                    for (int hf = 0; hf < C::kHalves; ++hf) {
+                        // four rows a step, 128 bytes of each; all loads before the
+                        // stores, which the compiler cannot tell apart from them
+                        uint4 v[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int rr = i * 4 + lane / 8;
+                            v[i] = *reinterpret_cast<const uint4 *>(staging + hf * 4096 + rr * 128 +
+                                                                    (((lane % 8) ^ (rr & 7)) << 4));
+                        }
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int row_at = __shfl_sync(0xffffffffu, my_row, i * 4 + lane / 8);
+                            if (row_at >= 0)
+                                *reinterpret_cast<uint4 *>(base + static_cast<size_t>(row_at) * D + hf * 64 +
+                                                           (lane % 8) * 8) = v[i];
+                        }
+                    }
+                }
             } else {
                 // a partial: [split][tile][D + 2][128 rows]
                 constexpr size_t kPart = static_cast<size_t>(D + 2) * kBM;
@@ -966,7 +979,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bar[C::ITEM_EMPTY + slot]);
+            release();             // (an item without key tiles)
+            pending = slot;
         }
         if (lane == 0) bulk_wait_all();   // copies out of shared memory that this CTA still holds
     }
