@@ -59,10 +59,6 @@ constexpr int kW = 4;                  // warps per CTA
 constexpr int kThreads = kW * 32;
 constexpr int kChunks = 512;           // entries of the CTA's prefix over the sequences
 constexpr int kMaxCtas = 640;          // bounds the partial slots (2 per CTA)
-#ifndef PA_DG_COST
-#define PA_DG_COST 4
-#endif
-constexpr int kUnitCost = PA_DG_COST;
 constexpr float kRaise = 8.f;
 constexpr float kBias = 6.f;           // weights are 2^(x - m + 6)
 
@@ -70,6 +66,7 @@ struct DecodeGroupedArgs {
     GroupedArgs g;
     float scale_log2;                  // plain scores: x = scale_log2 (q . k)
     float cap_log2, cap_in;            // capped: x = cap_log2 tanh(...), 2^(cap_in q.k) = e^(2 s / cap)
+    float cap_v, tanh_k[6];            // as a polynomial (fill_tanh), where |s / cap| < 1
     int group, chunks;                 // heads per K/V head; chunks of heads per K/V head
     int chunk_shift;                   // sequences per prefix entry: 2^chunk_shift
     float *partials;                   // [2 * kMaxCtas][heads * (D + 2)]
@@ -146,11 +143,11 @@ __device__ __forceinline__ uint32_t pack_pair(float a, float b) {
 // A sequence's visible keys as tiles of TK keys: tile i covers keys from
 // TK * (i < na ? i : i + skip); [lo, ctx) and [0, pre) are visible.
 // `len` is what a unit takes of the line: its tiles, and what its end costs a
-// CTA (merging the warps, a partial's ticket; 1.5 us), in tiles' time.
+// CTA (kCost, in tiles' time).
 struct Geo {
     int ctx, lo, pre, na, skip, nt, len;
 };
-template <int TK>
+template <int TK, int kCost>
 __device__ __forceinline__ Geo make_geo(const GroupedArgs &a, int ctx, int pre_raw) {
     Geo g;
     g.ctx = ctx;
@@ -164,7 +161,7 @@ __device__ __forceinline__ Geo make_geo(const GroupedArgs &a, int ctx, int pre_r
         g.skip = first - g.na;
         g.nt = g.na + total - first;
     }
-    g.len = g.nt > 0 ? g.nt + kUnitCost : 0;
+    g.len = g.nt > 0 ? g.nt + kCost : 0;
     return g;
 }
 
@@ -181,7 +178,7 @@ __device__ __forceinline__ int load_pre(const GroupedArgs &a, int s) {
 // A position on the line: tile `idx` of unit `unit` of sequence s.  A unit is
 // one (K/V head, chunk of query heads); the lanes hold the lengths of 32
 // sequences.
-template <int TK>
+template <int TK, int kCost>
 struct Cursor {
     int s, unit, idx;
     Geo g;
@@ -192,7 +189,7 @@ struct Cursor {
         pre_l = load_pre(a, base + lane);
     }
     __device__ __forceinline__ void set_geo(const GroupedArgs &a) {
-        g = make_geo<TK>(a, __shfl_sync(0xffffffffu, ctx_l, s & 31),
+        g = make_geo<TK, kCost>(a, __shfl_sync(0xffffffffu, ctx_l, s & 31),
                          __shfl_sync(0xffffffffu, pre_l, s & 31));
     }
     // The next sequence with tiles (or s = num_seqs, nt = 0).
@@ -231,12 +228,13 @@ struct Cfg {
     static constexpr int kHeads = 8 * NT;
     static constexpr int kMat = TK * D * 2;            // bytes of a K (or V) tile
     static constexpr int kStage = 2 * kMat;
-    
-#ifdef PA_STG
-    static constexpr int kStages = PA_STG;
-#else
-    static constexpr int kStages = D == 64 ? 3 : 2;
-#endif
+    // more bytes in flight do not help (a third stage for D = 128 made 256 long
+    // sequences 7 % slower); for D = 64 there is room for one
+    static constexpr int kStages = D == 64 && NT == 1 ? 3 : 2;
+    // what a unit's end (merging the warps, a partial's ticket; 1.5 us) costs in
+    // tiles' time: 64 sequences 61.3 us uncounted, 57.1 at 4; 16 heads 69.5 at 4,
+    // 66.0 at 8
+    static constexpr int kCost = 4 * NT;
     static constexpr int kRow = D + 4;                 // floats of a merge row (no bank conflicts)
     static constexpr int OFF_O = kW * kStages * kStage;
     static constexpr int OFF_ML = OFF_O + kW * kHeads * kRow * 4;
@@ -245,7 +243,7 @@ struct Cfg {
     static constexpr int OFF_MASK = OFF_BAR + (kW * kStages + 1) * 8;   // rings, partial written
     static constexpr int OFF_FLAG = OFF_MASK + kW * kStages * 4;
     static constexpr int kBytes = OFF_FLAG + 16 + 1024;  // + alignment slack
-    static constexpr int kCtasPerSm = 233472 / (kBytes + 1024) < 1 ? 1 : 233472 / (kBytes + 1024);
+    static constexpr int kCtasPerSm = 2 * (kBytes + 1024) <= 233472 ? 2 : 1;
 };
 
 // Takes the ticket of a partial that the CTA left (one warp; the partial's
@@ -317,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                           const __grid_constant__ CUtensorMap tm_v,
                           const __grid_constant__ DecodeGroupedArgs p) {
     using C = Cfg<D, NT>;
-    constexpr int TK = C::TK, MT = C::MT, KS = D / 16, kHeads = C::kHeads;
+    constexpr int TK = C::TK, kCost = C::kCost, MT = C::MT, KS = D / 16, kHeads = C::kHeads;
     const GroupedArgs &a = p.g;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -360,14 +358,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // The line's length, and prefix[c], the tiles of the sequences before chunk
     // c.  Up to 32 sequences need no prefix: a warp's lanes hold them.
-    Cursor<TK> cons;
+    Cursor<TK, kCost> cons;
     cons.base = -1;
     const bool small = a.num_seqs <= 32;
     long long total;
     if (small) {
         cons.s = 0;
         cons.load_group(a, lane);
-        total = static_cast<long long>(make_geo<TK>(a, cons.ctx_l, cons.pre_l).len) * units;
+        total = static_cast<long long>(make_geo<TK, kCost>(a, cons.ctx_l, cons.pre_l).len) * units;
 #pragma unroll
         for (int o = 16; o > 0; o /= 2) total += __shfl_xor_sync(0xffffffffu, total, o);
         __syncthreads();                              // the barriers are set up
@@ -383,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int s0 = c << p.chunk_shift;
                 const int s1 = min(a.num_seqs, (c + 1) << p.chunk_shift);
                 for (int s = s0; s < s1; ++s)
-                    n += make_geo<TK>(a, load_ctx(a, s), load_pre(a, s)).len;
+                    n += make_geo<TK, kCost>(a, load_ctx(a, s), load_pre(a, s)).len;
             }
             v[i] = n * units;
         }
@@ -437,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             cons.s = s;
             if ((s & ~31) != cons.base) cons.load_group(a, lane);
             const long long n = lane >= (s & 31)
-                                    ? static_cast<long long>(make_geo<TK>(a, cons.ctx_l, cons.pre_l).len) * units
+                                    ? static_cast<long long>(make_geo<TK, kCost>(a, cons.ctx_l, cons.pre_l).len) * units
                                     : 0;
             long long run = n;
 #pragma unroll
@@ -468,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int RB = B == 8 ? 8 : 16;
     const int rb_shift = B == 8 ? 3 : 4;
     const int boxes = TK / RB;
-    Cursor<TK> prod = cons;
+    Cursor<TK, kCost> prod = cons;
     int at = 0;                              // tile of the piece `prod` is at
     // the lane's box of tile `at`: physical block (-1: not needed, -2: needed
     // but its entry is bad) and row within the block
@@ -632,6 +630,45 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool partial = have != (1u << boxes) - 1 || k0 + TK > g.ctx ||
                                  (k0 < g.lo && k0 + TK > g.pre);
             bool raise = false;
+            if (a.softcap > 0.f) {
+                // by the polynomial if that holds for every score of the tile: a large
+                // cap would lose the low bits of small scores in 1 - 2 / (1 + e^(2u))
+                bool far = false;
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float v = sc[mt][nt][e] * p.cap_v;
+                            far |= !(v * v < 2.f);
+                        }
+                far = __any_sync(0xffffffffu, far);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            float &x = sc[mt][nt][e];
+                            if (far) {
+                                x = p.cap_log2 - 2.f * p.cap_log2 * fast_rcp(1.f + fast_exp2(x * p.cap_in));
+                            } else {
+                                const float v = x * p.cap_v, w = v * v;
+                                float y = p.tanh_k[5];
+#pragma unroll
+                                for (int i = 4; i >= 0; --i) y = fmaf(y, w, p.tanh_k[i]);
+                                x = v * y;
+                            }
+                        }
+            } else {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sc[mt][nt][e] *= p.scale_log2;
+            }
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -639,10 +676,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         float x = sc[mt][nt][e];
-                        if (a.softcap > 0.f)
-                            x = p.cap_log2 - 2.f * p.cap_log2 * fast_rcp(1.f + fast_exp2(x * p.cap_in));
-                        else
-                            x *= p.scale_log2;
                         const int key = k0 + mt * 16 + row + (e >= 2 ? 8 : 0);
                         if (a.alibi_slopes) x -= slope[nt][e & 1] * static_cast<float>(g.ctx - 1 - key);
                         if (partial) {
@@ -895,6 +928,7 @@ cudaError_t launch_decode_grouped(const GroupedArgs &args, int dtype, int head_d
     p.scale_log2 = static_cast<float>(args.scale * log2e);
     p.cap_log2 = static_cast<float>(args.softcap * log2e);
     p.cap_in = args.softcap > 0.f ? static_cast<float>(2.0 * args.scale / args.softcap * log2e) : 0.f;
+    fill_tanh(args.scale, args.softcap, &p.cap_v, p.tanh_k);
     p.group = args.num_q_heads / Hk;
     const int per = heads_per_chunk(head_dim, p.group);
     p.chunks = (p.group + per - 1) / per;

@@ -1039,14 +1039,7 @@ cudaError_t launch_prefill_grouped(const GroupedArgs &args, int dtype, int head_
     p.cap_log2 = static_cast<float>(args.softcap * log2e);
     p.cap_in = args.softcap > 0.f ? static_cast<float>(2.0 * args.scale / args.softcap * log2e) : 0.f;
     p.group = Hq / Hk;
-    // tanh(u) / u in powers of u^2, for u^2 in [0, 1]: the interpolant at 400
-    // Chebyshev points, cut after the fifth power; with v^2 = 2 u^2
-    const double tanh_u[6] = {0.99999944213822956, -0.33329180320158908, 0.13282513809561988,
-                              -0.051635458658114801, 0.016776776240506608, -0.0030804092508174806};
-    const double u_to_v = 0.70710678118654752;
-    p.cap_v = args.softcap > 0.f ? static_cast<float>(args.scale / args.softcap / u_to_v) : 0.f;
-    for (int i = 0; i < 6; ++i)
-        p.tanh_k[i] = static_cast<float>(args.softcap * log2e * u_to_v * tanh_u[i] / (1 << i));
+    fill_tanh(args.scale, args.softcap, &p.cap_v, p.tanh_k);
     p.tpt = kBM / p.group;
     const Plan pl = make_plan(args.num_seqs, Hk, p.group, args.max_q);
     const long long items = pl.base * pl.splits;
