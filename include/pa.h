@@ -505,8 +505,9 @@ typedef struct pa_attn_opts {
  * behind may be freed and their entries hold anything.  A used entry outside
  * [0, N) flags PA_DEVERR_TABLE and its keys are left out.
  * PA_ERR_SHAPE if num_q_heads is not a positive multiple of H, N * H * B or
- * S * num_q_heads exceeds INT32_MAX, window < 0, or softcap is negative or
- * not finite.
+ * S * num_q_heads exceeds INT32_MAX, max_blocks_per_seq * B exceeds 2^30, S
+ * exceeds 2^28, window < 0, or softcap is negative or not finite.  out must not
+ * overlap the inputs.
  *
  * Each K and V row is read once for all query heads that share it (in chunks
  * of 16 heads; of 8 for D = 256).  Scores, softmax and sums are fp32; the

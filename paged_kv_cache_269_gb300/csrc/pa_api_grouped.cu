@@ -31,13 +31,14 @@ int check_opts(const pa_attn_opts *o) {
     return PA_OK;
 }
 
-// Products that the kernels hold in 32 bits.
+// Products that the kernels hold in 32 bits (positions and counts of
+// sequences with room for a tile past the end).
 int check_ranges(const pa_dims *dims, int32_t num_q_heads, int32_t max_blocks_per_seq) {
     const long long lim = 0x7fffffffLL;
     const long long slots = static_cast<long long>(dims->num_blocks) * dims->block_size;
     if (max_blocks_per_seq <= 0 || slots > lim || slots * dims->num_heads > lim ||
-        static_cast<long long>(max_blocks_per_seq) * dims->block_size > lim ||
-        static_cast<long long>(dims->num_seqs) * num_q_heads > lim)
+        static_cast<long long>(max_blocks_per_seq) * dims->block_size > (1LL << 30) ||
+        dims->num_seqs > (1 << 28) || static_cast<long long>(dims->num_seqs) * num_q_heads > lim)
         return PA_ERR_SHAPE;
     return PA_OK;
 }
@@ -57,7 +58,8 @@ GroupedArgs make_args(void *out, const void *q, const void *k_cache, const void 
     a.prefix_lens = opts ? opts->prefix_lens : nullptr;
     a.scale = scale;
     a.softcap = opts ? opts->softcap : 0.f;
-    a.window = opts ? opts->window : 0;
+    // a window as long as any context limits nothing
+    a.window = opts && opts->window < max_blocks_per_seq * dims->block_size ? opts->window : 0;
     a.num_seqs = dims->num_seqs;
     a.num_q_heads = num_q_heads;
     a.num_kv_heads = dims->num_heads;
@@ -220,7 +222,8 @@ int pa_prefill_grouped(void *out, const void *q, const void *k_cache, const void
     if (rc != PA_OK) return rc;
     if (!isfinite(scale) || total_query_tokens < 0 || max_query_len < 0) return PA_ERR_SHAPE;
     // work items (query tiles x sequences x K/V heads) are counted in 32 bits
-    if ((static_cast<long long>(max_query_len) + 1) * num_q_heads * dims->num_seqs > 0x7fffffffLL * 64LL)
+    if (prefill_grouped_items(dims->num_seqs, dims->num_heads, num_q_heads / dims->num_heads, max_query_len) >
+        0x7fffffffLL - 4096)
         return PA_ERR_SHAPE;
     if (dims->num_seqs == 0 || total_query_tokens == 0 || max_query_len == 0) return PA_OK;
     if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens || !query_start)

@@ -175,6 +175,7 @@ size_t decode_grouped_counters_bytes(int num_seqs, int num_kv_heads, int group, 
 size_t prefill_grouped_workspace_bytes(int num_seqs, int num_kv_heads, int group, int head_dim,
                                        int max_query_len);
 size_t prefill_grouped_counters_bytes();
+long long prefill_grouped_items(int num_seqs, int num_kv_heads, int group, int max_query_len);
 cudaError_t launch_decode_grouped(const GroupedArgs &args, int dtype, int head_dim, int num_sms,
                                   cudaStream_t stream);
 cudaError_t launch_prefill_grouped(const GroupedArgs &args, int dtype, int head_dim, int num_sms,

@@ -326,6 +326,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         *abort_flag = 0;
         mbar_init_fence();
     }
+    // rows that no copy of Q fills (G that does not divide 128): zero, so that
+    // nothing left there slows their warp down
+    const int filled = p.tpt * p.group;
+    if (filled < kBM) {
+        for (int i = threadIdx.x; i < (kBM - filled) * 8 * C::kHalves * 4; i += kThreads) {
+            const int c = i % 8, rr = filled + i / 8 % (kBM - filled), hq = i / 8 / (kBM - filled);
+            *reinterpret_cast<uint4 *>(smem + C::OFF_Q + hq * C::kHalfQ + rr * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
     if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_addr(const_cast<uint32_t *>(tmem_slot))),
@@ -1026,6 +1036,11 @@ size_t prefill_grouped_workspace_bytes(int num_seqs, int num_kv_heads, int group
     return static_cast<size_t>(pl.base) * pl.splits * 2 * (head_dim + 2) * kBM * sizeof(float);
 }
 
+long long prefill_grouped_items(int num_seqs, int num_kv_heads, int group, int max_query_len) {
+    const Plan pl = make_plan(num_seqs, num_kv_heads, group, max_query_len);
+    return pl.base * pl.splits;
+}
+
 size_t prefill_grouped_counters_bytes() { return (kCounters * 4 + 255) / 256 * 256; }
 
 cudaError_t launch_prefill_grouped(const GroupedArgs &args, int dtype, int head_dim, int num_sms,
@@ -1042,9 +1057,7 @@ cudaError_t launch_prefill_grouped(const GroupedArgs &args, int dtype, int head_
     fill_tanh(args.scale, args.softcap, &p.cap_v, p.tanh_k);
     p.tpt = kBM / p.group;
     const Plan pl = make_plan(args.num_seqs, Hk, p.group, args.max_q);
-    const long long items = pl.base * pl.splits;
-    // the queue head runs past the end by at most one per CTA
-    if (items > 0x7fffffffLL - 4096) return cudaErrorInvalidConfiguration;
+    const long long items = pl.base * pl.splits;   // fits an int (the caller checks), with room past the end
     p.num_pairs = static_cast<int>(pl.pairs);
     p.splits = pl.splits;
     p.num_items = static_cast<int>(items);

@@ -351,6 +351,111 @@ def test_prefill_in_graphs_and_reproducible(dev):
     assert pa.device_errors() == 0
 
 
+# ------------------------------------------------------------------ extremes
+
+@pytest.mark.parametrize("cap", [0.5, 1000.0, 1e6])
+def test_small_and_large_caps(dev, cap):
+    """Scores far past a small cap, and a cap so large that it does nothing."""
+    decode(make_case(70, [90, 300], [1, 1], 8, 2, 128, 16, F16, cap=cap, q_scale=3.0), dev)
+    prefill(make_case(71, [90, 300], [90, 40], 8, 2, 128, 16, BF16, cap=cap, q_scale=3.0), dev)
+
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 1023, 1024])
+def test_windows_as_long_as_the_context(dev, window):
+    c = make_case(72, [1024, 700, 3], [1] * 3, 6, 2, 64, 16, F16, window=window)
+    decode(c, dev)
+    prefill(make_case(73, [1024, 300], [600, 300], 6, 2, 64, 16, F16, window=window), dev)
+
+
+def test_values_that_no_query_sees(dev):
+    """NaN and infinities in keys outside a decode's window, in slots past the
+    context, and (keys) in front of a prompt's later rows."""
+    c = make_case(74, [300], [1], 8, 2, 128, 16, BF16, window=40)
+    for j in range(260):
+        blk = int(c.tables[0, j // 16])
+        if blk >= 0:
+            c.k_cache[blk, :, j % 16] = float("nan")
+            c.v_cache[blk, :, j % 16] = float("inf")
+    got = run_decode(c, to_dev(c, dev))
+    assert pa.device_errors() == 0
+    keep = torch.arange(260, 300)
+    blk, off = c.tables[0, keep // 16].long(), keep % 16
+    for h in range(2):
+        K, V = c.k_cache[blk, h, off].double(), c.v_cache[blk, h, off].double()
+        for g in range(4):
+            w = torch.softmax(c.q[0, 4 * h + g].double() @ K.T * c.scale, -1)
+            o, mag = w @ V, w @ V.abs()
+            # the fp32 dot product's part of the bound, and the output's rounding
+            tol = 2.0 ** -8 * o.abs() + 2e-3 * mag
+            assert ((got[0, 4 * h + g].cpu().double() - o).abs() <= tol).all()
+
+
+def test_nan_queries_stay_in_their_rows(dev):
+    c = make_case(75, [70, 200], [70, 33], 6, 2, 128, 16, F16)
+    d = to_dev(c, dev)
+    d["q"][10, 3] = float("nan")
+    got = run_prefill(c, d)
+    assert torch.isnan(got[10, 3]).all()
+    got[10, 3] = run_prefill(c, to_dev(c, dev))[10, 3]
+    check(c, got, True)
+    c = make_case(76, [70, 200], [1, 1], 6, 2, 128, 16, F16)
+    d = to_dev(c, dev)
+    d["q"][1, 2] = float("nan")
+    got = run_decode(c, d)
+    assert torch.isnan(got[1, 2]).all()
+    got[1, 2] = run_decode(c, to_dev(c, dev))[1, 2]
+    check(c, got, False)
+
+
+def test_caches_past_32_bit_offsets(dev):
+    """Blocks at the end of a pool of more than 2^32 bytes and 2^31 elements."""
+    H, B, D = 8, 16, 128
+    N = 2 ** 31 // (H * B * D) + 64
+    kc = torch.empty(N, H, B, D, dtype=F16, device=dev)
+    vc = torch.empty(N, H, B, D, dtype=F16, device=dev)
+    assert kc.numel() > 2 ** 31
+    c = make_case(77, [50, 90], [1, 33], 16, H, D, B, F16, extra_blocks=0)
+    n = c.k_cache.shape[0]
+    kc[N - n:], vc[N - n:] = c.k_cache.to(dev), c.v_cache.to(dev)
+    d = to_dev(c, dev)
+    d["k_cache"], d["v_cache"] = kc, vc
+    d["tables"] = torch.where((d["tables"] >= 0) & (d["tables"] < n), d["tables"] + (N - n), d["tables"])
+    got = run_prefill(c, d)
+    check(c, got, True)
+    c2 = make_case(77, [50, 90], [1, 1], 16, H, D, B, F16, extra_blocks=0)
+    d2 = dict(d, q=c2.q.to(dev))
+    c2.k_cache, c2.v_cache, c2.tables = c.k_cache, c.v_cache, c.tables
+    check(c2, run_decode(c2, d2), False)
+    q = torch.randn(3, 16, D, device=dev).to(F16)
+    k, v = torch.randn(3, H, D, device=dev).to(F16), torch.randn(3, H, D, device=dev).to(F16)
+    slots = torch.tensor([N * B - 1, N * B - 17, (N - 1) * B], dtype=torch.int32, device=dev)
+    pos = torch.zeros(3, dtype=torch.int32, device=dev)             # angle 0: K as it is
+    pa.rope_and_cache(torch.empty_like(q), q, k, v, kc, vc, pos, pa.rope_table(4, 128, device=dev), slots)
+    assert torch.equal(kc[N - 1, :, 15], k[0]) and torch.equal(vc[N - 2, :, 15], v[1])
+    assert torch.equal(kc[N - 1, :, 0], k[2])
+    assert pa.device_errors() == 0
+
+
+def test_decode_at_the_edges_of_a_cta_s_piece(dev):
+    """Every way a context can meet the pieces: many of one tile, one of many,
+    sequences of no tokens between them."""
+    g = torch.Generator().manual_seed(8)
+    for seed, S in ((80, 33), (81, 600)):
+        ctx = [0 if torch.rand(1, generator=g) < 0.3 else int(torch.randint(1, 90, (1,), generator=g)) for _ in range(S)]
+        ctx[S // 2] = 5000
+        decode(make_case(seed, ctx, [1] * S, 4, 2, 128, 16, F16), dev)
+    decode(make_case(82, [0, 0, 0], [1] * 3, 4, 2, 128, 16, F16), dev)
+
+
+def test_single_tokens_prefill_like_decode(dev):
+    """One new token per sequence through both calls."""
+    c = make_case(83, [1, 64, 65, 700], [1] * 4, 8, 2, 128, 16, F16, alibi=True)
+    d = to_dev(c, dev)
+    a, b = run_decode(c, d), run_prefill(c, d)
+    check(c, a, False)
+    check(c, b, True)
+
+
 # ------------------------------------------------------------------ rope
 
 def rope_inputs(seed, T, Hq, H, D, B, rot, dtype, packed, far=5000):
