@@ -543,6 +543,12 @@ size_t pa_decode_grouped_counters_bytes(const pa_dims *dims, int32_t num_q_heads
  * call sees a key may hold anything, and so may key rows from ctx_s on; V rows
  * of the other keys must be finite (a weight of zero times a NaN is NaN).
  *
+ * Scores, softmax and sums are fp32; the weights are rounded to the element
+ * type once before the P V product (pa_prefill carries a second 16-bit term).
+ * An output element is then off by at most u (|o| + sum_j p_j |v_j|) plus the
+ * fp32 terms, u = 2^-11 for fp16 and 2^-8 for bf16; over a tensor the error is
+ * about 1.4 times that of rounding the exact result.
+ *
  * Built for head_dim 64 and 128, block_size 8, 16 and 32, fp16 and bf16, up
  * to 128 query heads per K/V head (PA_ERR_UNSUPPORTED otherwise).
  */
