@@ -253,8 +253,7 @@ __device__ __forceinline__ bool take_ticket(const DecodeGroupedArgs &p, int s, i
     uint32_t last = 0;
     if (lane == 0) {
         uint32_t *ticket = p.g.counters + 2 + static_cast<size_t>(s) * units + unit;
-        __threadfence();   // the CTA's partial, ordered before its ticket
-        last = atomicAdd(ticket, 1u) == static_cast<uint32_t>(others);
+        last = ticket_add(ticket, 1u) == static_cast<uint32_t>(others);
         if (last) atomicExch(ticket, 0u);
     }
     return __shfl_sync(0xffffffffu, last, 0) != 0;
@@ -867,7 +866,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (warp == kW - 1) {
                     ok = ok && __all_sync(0xffffffffu, mbar_wait(part_bar, 0, abort_flag, a.err));
                     if (ok && take_ticket(p, s, units, unit, i1 - i0, lane)) {
-                        __threadfence();
                         join_unit<kBf16, D, kHeads>(p, s, unit, i0, i1, lane, 32);
                     }
                 }
@@ -875,7 +873,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncthreads();
                 if (warp == 0) {
                     const bool last = take_ticket(p, s, units, unit, i1 - i0, lane);
-                    __threadfence();
                     if (lane == 0) *last_flag = last;
                 }
                 __syncthreads();

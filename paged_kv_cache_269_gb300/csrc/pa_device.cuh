@@ -179,6 +179,16 @@ __device__ __forceinline__ void allow_dependents_to_launch() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// Adds to a word in global memory with release and acquire order at device
+// scope: what the thread's CTA wrote before (and a barrier ordered before the
+// call) is visible to whoever sees the addition, and the other way round.  A
+// __threadfence on both sides orders more and takes longer.
+__device__ __forceinline__ uint32_t ticket_add(uint32_t *word, uint32_t v) {
+    uint32_t old;
+    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], %2;" : "=r"(old) : "l"(word), "r"(v) : "memory");
+    return old;
+}
+
 // Global loads that bypass L1: used for partial results written by other CTAs
 // of the same launch.
 __device__ __forceinline__ float2 ld_cg_f2(const float2 *p) { return __ldcg(p); }

@@ -919,19 +919,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mine[(D + 1) * kBM] = l;
                 }
                 // the warp's 32 rows are joined by the warp of the last split
-                __threadfence();
                 __syncwarp();
                 uint32_t last = 0;
                 if (lane == 0) {
                     uint32_t *ticket = a.counters + 2 + it->slot * 8 + warp;
-                    last = atomicAdd(ticket, 1u) == static_cast<uint32_t>(splits - 1);
+                    last = ticket_add(ticket, 1u) == static_cast<uint32_t>(splits - 1);
                     if (last) atomicExch(ticket, 0u);
                 }
                 last = __shfl_sync(0xffffffffu, last, 0);
                 if (last && live) {
                     uint16_t *dst = a.out + (static_cast<size_t>(it->q_first + it->tok0 + t * p.tpt + tok) * a.num_q_heads +
                                              it->hk * p.group + head) * D;
-                    __threadfence();
                     // four splits at a time, so that their loads share a round trip
                     // (one by one, joining three took 13000 cycles)
                     constexpr int kZ = 4;
