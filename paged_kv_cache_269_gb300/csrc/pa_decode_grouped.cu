@@ -372,6 +372,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr int kPer = kChunks / kThreads;      // neighbouring entries per thread
         const int nchunks = (a.num_seqs + (1 << p.chunk_shift) - 1) >> p.chunk_shift;
         long long v[kPer], sum = 0;
+        if (p.chunk_shift == 0) {     // an entry is a sequence: all loads at once
+            int ctx[kPer], pre[kPer];
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                ctx[i] = load_ctx(a, threadIdx.x * kPer + i);
+                pre[i] = load_pre(a, threadIdx.x * kPer + i);
+            }
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                v[i] = static_cast<long long>(make_geo<TK, kCost>(a, ctx[i], pre[i]).len) * units;
+        } else
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int c = threadIdx.x * kPer + i;
