@@ -619,19 +619,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 pending = slot;
                 continue;
             }
-            // the row's position, -1 for a row without a query
-            const int pos = tok < min(p.tpt, it->q_len - it->tok0 - t * p.tpt)
-                                ? it->first_pos + t * p.tpt + tok
-                                : -1;
+            // The row's position.  A row without a query stands where the warp's last
+            // query does, so that it costs the warp no mask, and is not written; in
+            // a warp without any, every row is at -1 and sees nothing.
+            const bool live = tok < min(p.tpt, it->q_len - it->tok0 - t * p.tpt);
+            const int own = live ? it->first_pos + t * p.tpt + tok : -1;
+            const int wmax = __reduce_max_sync(0xffffffffu, own);
+            const int pos = live ? own : wmax;
+            const int wmin = __reduce_min_sync(0xffffffffu, pos);
             const int pre_all = it->pre, na = it->na, skip = it->skip, j0 = it->j0;
             const int last = j0 + max(nk, 0) - 1;
-            // positions of the warp's rows, for tiles that need no mask
-            const int wmin = __reduce_min_sync(0xffffffffu, pos);
-            const int wmax = __reduce_max_sync(0xffffffffu, pos);
             float slope = 0.f;
             if constexpr (kAlibi)
                 slope = pos >= 0 ? __ldg(a.alibi_slopes + it->hk * p.group + head) * 1.4426950408889634f : 0.f;
-            // a row without a query takes no part (m = 0: no maximum is missing)
+            // (m = 0 where nothing is seen: no maximum is missing)
             float m = pos >= 0 ? -INFINITY : 0.f, l = 0.f;
             for (int j = 0; j < nk; ++j, ++n) {
                 const uint32_t buf = n % C::kBufs;
@@ -841,7 +842,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 tc_fence_after();
             }
-            const bool live = pos >= 0;
             const int splits = it->splits;
             if (splits == 1) {
                 const float inv = l > 0.f ? 1.f / l : 0.f;
