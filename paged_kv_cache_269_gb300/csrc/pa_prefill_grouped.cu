@@ -98,7 +98,7 @@ constexpr float kFar = 1e30f;
 constexpr int kMaskRing = 16;
 // Work is split over keys while there are fewer items than SMs (152).
 constexpr int kSplitTarget = 152;
-constexpr int kCounters = 2 + 8 * kSplitTarget;   // queue head, CTAs done, a ticket per (item, warp)
+constexpr int kCounters = 2 + 2 * kSplitTarget;   // queue head, CTAs done, a ticket per (item, tile)
 
 struct PrefillGroupedArgs {
     GroupedArgs g;
@@ -122,6 +122,7 @@ struct Item {
     int nk0, nk1;                      // of which tile 0 / 1 needs the first nk
     int split, splits;                 // this split, of how many
     int slot;                          // item without its split (partials, tickets)
+    int joins;                         // bit t: parity of tile t's split items so far
     int s;
 };
 
@@ -146,12 +147,14 @@ struct Cfg {
     static constexpr int S_FULL = 3, P_FULL = 9, PV_DONE = 15;   // [tile][buffer]
     static constexpr int MMA_DONE = 21;                          // [issuing thread]
     static constexpr int ITEM_FULL = 25, ITEM_EMPTY = 27;
-    static constexpr int K_FULL = 29, V_FULL = K_FULL + kSlots;
+    static constexpr int PARTS = 29, TICKET = 31;                // [tile]
+    static constexpr int K_FULL = 33, V_FULL = K_FULL + kSlots;
     static constexpr int K_EMPTY = V_FULL + kSlots, V_EMPTY = K_EMPTY + kSlots;
     static constexpr int kNumBars = V_EMPTY + kSlots;
     static constexpr int OFF_TMEM = OFF_BAR + kNumBars * 8;
     static constexpr int OFF_FLAG = OFF_TMEM + 4;
-    static constexpr int OFF_MASK = OFF_FLAG + 4;                   // uint32[kMaskRing]
+    static constexpr int OFF_LAST = OFF_FLAG + 4;                   // int[2]
+    static constexpr int OFF_MASK = OFF_LAST + 8;                   // uint32[kMaskRing]
     static constexpr int OFF_ITEM = OFF_MASK + kMaskRing * 4;       // Item[2]
     static constexpr int kSmemBytes = OFF_ITEM + 2 * static_cast<int>(sizeof(Item)) + 1024;
     static_assert(kSmemBytes <= 232448, "shared memory");
@@ -295,7 +298,11 @@ struct KeyBlocks {
     __device__ __forceinline__ int group(int blk) const { return (blk * heads + hk) << (b_shift - 3); }
 };
 
-template <bool kBf16, int D, bool kCap, bool kAlibi>
+// kSplit: the call has key splits.  A call without them runs a kernel that leaves
+// out the code that writes and joins partials, which the softmax warps' loop pays
+// for although it does not run (one prompt of 8192 tokens: 348 us with it, 333
+// without).
+template <bool kBf16, int D, bool kCap, bool kAlibi, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_grouped_kernel(const __grid_constant__ CUtensorMap tm_q,
                            const __grid_constant__ CUtensorMap tm_k,
@@ -310,6 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *bar = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(smem + C::OFF_TMEM);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_FLAG);
+    volatile int *last_flag = reinterpret_cast<volatile int *>(smem + C::OFF_LAST);
     volatile uint32_t *mask_ring = reinterpret_cast<volatile uint32_t *>(smem + C::OFF_MASK);
     Item *items = reinterpret_cast<Item *>(smem + C::OFF_ITEM);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -318,7 +326,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kNumBars; ++i) {
             uint32_t count = 1;
-            if (i >= C::P_FULL && i < C::P_FULL + 6) count = 4;               // softmax warps
+            if ((i >= C::P_FULL && i < C::P_FULL + 6) || i == C::PARTS || i == C::PARTS + 1)
+                count = 4;                                    // softmax warps
             if (i == C::ITEM_EMPTY || i == C::ITEM_EMPTY + 1) count = 13;     // 4 MMA threads, 8 softmax warps, V
             if (i >= C::K_EMPTY) count = 2;               // both tiles' threads
             mbar_init(&bar[i], count);
@@ -356,6 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t g = 0;                        // K tiles issued, over all items
             bool first_item = true;
             int k = 0, q_loads = 0;                // items whose K is issued, Q loads issued
+            int joins = 0;                         // bit t: parity of tile t's split items
             bool ok = true;
             for (;;) {
                 int w = 0;
@@ -374,6 +384,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const bool done = static_cast<unsigned>(w) >= static_cast<unsigned>(p.num_items);
                 const int slot = k % 2;
+                it.joins = joins;
+                if (!done && it.splits > 1) joins ^= it.nk1 >= 0 ? 3 : 1;
                 ok = warp_all(mbar_wait(&bar[C::ITEM_EMPTY + slot], ((k / 2) & 1) ^ 1, abort_flag, a.err));
                 if (!ok) break;
                 if (lane == 0) {
@@ -842,8 +854,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 tc_fence_after();
             }
-            const int splits = it->splits;
-            if (splits == 1) {
+            const int splits = kSplit ? it->splits : 1;
+            if (!kSplit || splits == 1) {
                 const float inv = l > 0.f ? 1.f / l : 0.f;
                 const bool whole = p.store_boxes && warp_all(live);
 #pragma unroll
@@ -897,7 +909,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
-            } else {
+            } else if constexpr (kSplit) {
                 // a partial: [split][tile][D + 2][128 rows]
                 constexpr size_t kPart = static_cast<size_t>(D + 2) * kBM;
                 float *base = p.partials + (static_cast<size_t>(it->slot) * p.splits * 2 + t) * kPart + r;
@@ -918,23 +930,36 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mine[D * kBM] = m;
                     mine[(D + 1) * kBM] = l;
                 }
-                // the warp's 32 rows are joined by the warp of the last split
+                // The tile's four warps take one ticket, and those of the last split
+                // join all of them, a quarter of the dims each (each its own 32 rows,
+                // a few rows kept one warp: 4 tokens of 8 heads took 44 us over 32000
+                // keys, and take 30).
                 __syncwarp();
-                uint32_t last = 0;
-                if (lane == 0) {
-                    uint32_t *ticket = a.counters + 2 + it->slot * 8 + warp;
-                    last = ticket_add(ticket, 1u) == static_cast<uint32_t>(splits - 1);
-                    if (last) atomicExch(ticket, 0u);
+                if (lane == 0) mbar_arrive(&bar[C::PARTS + t]);
+                if (warp % 4 == 0) {
+                    ok = warp_all(mbar_wait(&bar[C::PARTS + t], (it->joins >> t) & 1, abort_flag, a.err));
+                    if (!ok) break;
+                    if (lane == 0) {
+                        uint32_t *ticket = a.counters + 2 + it->slot * 2 + t;
+                        const bool last = ticket_add(ticket, 1u) == static_cast<uint32_t>(splits - 1);
+                        if (last) atomicExch(ticket, 0u);
+                        last_flag[t] = last;
+                        mbar_arrive(&bar[C::TICKET + t]);
+                    }
                 }
-                last = __shfl_sync(0xffffffffu, last, 0);
-                if (last && live) {
-                    uint16_t *dst = a.out + (static_cast<size_t>(it->q_first + it->tok0 + t * p.tpt + tok) * a.num_q_heads +
-                                             it->hk * p.group + head) * D;
+                ok = warp_all(mbar_wait(&bar[C::TICKET + t], (it->joins >> t) & 1, abort_flag, a.err));
+                if (!ok) break;
+                const int ntok = min(p.tpt, it->q_len - it->tok0 - t * p.tpt);
+                for (int r0 = 0; last_flag[t] && r0 < ntok * p.group; r0 += 32) {
+                    const int rr = min(r0 + lane, ntok * p.group - 1);
+                    const float *rows = base - r + rr;
+                    uint16_t *dst = a.out + (static_cast<size_t>(it->q_first + it->tok0 + t * p.tpt + rr / p.group) *
+                                                 a.num_q_heads + it->hk * p.group + rr % p.group) * D;
                     // four splits at a time, so that their loads share a round trip
                     // (one by one, joining three took 13000 cycles)
                     constexpr int kZ = 4;
                     auto part = [&](int z) {
-                        return base + static_cast<size_t>(min(z, splits - 1)) * 2 * kPart;
+                        return rows + static_cast<size_t>(min(z, splits - 1)) * 2 * kPart;
                     };
                     float top = -INFINITY, total = 0.f;
                     for (int z0 = 0; z0 < splits; z0 += kZ) {
@@ -954,7 +979,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     const float inv = total > 0.f ? 1.f / total : 0.f;
 #pragma unroll 1
-                    for (int q = 0; q < D / 16; ++q) {
+                    for (int d0 = warp % 4 * (D / 4); d0 < (warp % 4 + 1) * (D / 4); d0 += 16) {
                         float acc[16];
 #pragma unroll
                         for (int e = 0; e < 16; ++e) acc[e] = 0.f;
@@ -965,7 +990,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             for (int z = 0; z < kZ; ++z) {
                                 f[z] = __ldcg(part(z0 + z) + D * kBM);
 #pragma unroll
-                                for (int e = 0; e < 16; ++e) v[z][e] = __ldcg(part(z0 + z) + (q * 16 + e) * kBM);
+                                for (int e = 0; e < 16; ++e) v[z][e] = __ldcg(part(z0 + z) + (d0 + e) * kBM);
                             }
 #pragma unroll
                             for (int z = 0; z < kZ; ++z) {
@@ -974,14 +999,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 for (int e = 0; e < 16; ++e) acc[e] += f[z] * v[z][e];
                             }
                         }
+                        if (r0 + lane < ntok * p.group) {
 #pragma unroll
-                        for (int e = 0; e < 16; e += 8) {
-                            uint4 v;
-                            uint32_t *u = reinterpret_cast<uint32_t *>(&v);
+                            for (int e = 0; e < 16; e += 8) {
+                                uint4 v;
+                                uint32_t *u = reinterpret_cast<uint32_t *>(&v);
 #pragma unroll
-                            for (int z = 0; z < 4; ++z)
-                                u[z] = pack_pair<kBf16>(acc[e + 2 * z] * inv, acc[e + 2 * z + 1] * inv);
-                            *reinterpret_cast<uint4 *>(dst + q * 16 + e) = v;
+                                for (int z = 0; z < 4; ++z)
+                                    u[z] = pack_pair<kBf16>(acc[e + 2 * z] * inv, acc[e + 2 * z + 1] * inv);
+                                *reinterpret_cast<uint4 *>(dst + d0 + e) = v;
+                            }
                         }
                     }
                 }
@@ -1015,10 +1042,17 @@ Plan make_plan(int num_seqs, int num_kv_heads, int group, int max_q) {
 }
 
 using Kernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, PrefillGroupedArgs);
-template <bool kBf16, int D>
+template <bool kBf16, int D, bool kSplit>
 Kernel pick(bool cap, bool alibi) {
-    return cap ? (alibi ? prefill_grouped_kernel<kBf16, D, true, true> : prefill_grouped_kernel<kBf16, D, true, false>)
-               : (alibi ? prefill_grouped_kernel<kBf16, D, false, true> : prefill_grouped_kernel<kBf16, D, false, false>);
+    return cap ? (alibi ? prefill_grouped_kernel<kBf16, D, true, true, kSplit>
+                        : prefill_grouped_kernel<kBf16, D, true, false, kSplit>)
+               : (alibi ? prefill_grouped_kernel<kBf16, D, false, true, kSplit>
+                        : prefill_grouped_kernel<kBf16, D, false, false, kSplit>);
+}
+template <bool kSplit>
+Kernel pick(bool bf16, int D, bool cap, bool alibi) {
+    return bf16 ? (D == 64 ? pick<true, 64, kSplit>(cap, alibi) : pick<true, 128, kSplit>(cap, alibi))
+                : (D == 64 ? pick<false, 64, kSplit>(cap, alibi) : pick<false, 128, kSplit>(cap, alibi));
 }
 
 }  // namespace
@@ -1080,8 +1114,8 @@ cudaError_t launch_prefill_grouped(const GroupedArgs &args, int dtype, int head_
         !encode(&tm_v, bf16, args.v_cache, 4, kv_dims, kv_strides, kv_box))
         return cudaErrorInvalidValue;
     const bool cap = args.softcap > 0.f, alibi = args.alibi_slopes != nullptr;
-    const Kernel kernel = bf16 ? (D == 64 ? pick<true, 64>(cap, alibi) : pick<true, 128>(cap, alibi))
-                               : (D == 64 ? pick<false, 64>(cap, alibi) : pick<false, 128>(cap, alibi));
+    const bool split = pl.splits > 1;
+    const Kernel kernel = split ? pick<true>(bf16, D, cap, alibi) : pick<false>(bf16, D, cap, alibi);
     const int smem = D == 64 ? Cfg<64>::kSmemBytes : Cfg<128>::kSmemBytes;
     // the kernel's shared-memory limit, once per device and variant
     int device = 0;
@@ -1090,8 +1124,8 @@ cudaError_t launch_prefill_grouped(const GroupedArgs &args, int dtype, int head_
     if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
     {
         static std::mutex mu;
-        static bool ready[64][16] = {};
-        const int which = (bf16 ? 8 : 0) + (D == 64 ? 0 : 4) + (cap ? 2 : 0) + (alibi ? 1 : 0);
+        static bool ready[64][32] = {};
+        const int which = (bf16 ? 8 : 0) + (D == 64 ? 0 : 4) + (cap ? 2 : 0) + (alibi ? 1 : 0) + (split ? 16 : 0);
         std::lock_guard<std::mutex> lock(mu);
         if (!ready[device][which]) {
             e = cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel),
