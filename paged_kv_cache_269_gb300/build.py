@@ -52,7 +52,7 @@ def up_to_date() -> bool:
 
 
 def compile_flags(extra=()):
-    return ["-O3", "-std=c++17", *ARCH, "-split-compile=4", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE,
+    return ["-O3", "-std=c++17", *ARCH, "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE,
             "-I", CSRC, *extra]
 
 

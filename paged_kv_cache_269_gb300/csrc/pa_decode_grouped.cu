@@ -66,7 +66,7 @@ struct DecodeGroupedArgs {
     GroupedArgs g;
     float scale_log2;                  // plain scores: x = scale_log2 (q . k)
     float cap_log2, cap_in;            // capped: x = cap_log2 tanh(...), 2^(cap_in q.k) = e^(2 s / cap)
-    float cap_v, tanh_k[6];            // as a polynomial (fill_tanh), where |s / cap| < 1
+    float cap_v, tanh_k[5];            // as a polynomial (fill_tanh), where |s / cap| < 0.8
     int group, chunks;                 // heads per K/V head; chunks of heads per K/V head
     int chunk_shift;                   // sequences per prefix entry: 2^chunk_shift
     float *partials;                   // [2 * kMaxCtas][heads * (D + 2)]
@@ -665,9 +665,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 x = p.cap_log2 - 2.f * p.cap_log2 * fast_rcp(1.f + fast_exp2(x * p.cap_in));
                             } else {
                                 const float v = x * p.cap_v, w = v * v;
-                                float y = p.tanh_k[5];
+                                float y = p.tanh_k[4];
 #pragma unroll
-                                for (int i = 4; i >= 0; --i) y = fmaf(y, w, p.tanh_k[i]);
+                                for (int i = 3; i >= 0; --i) y = fmaf(y, w, p.tanh_k[i]);
                                 x = v * y;
                             }
                         }

@@ -40,7 +40,7 @@
 //    and the maximum comes first.  With a distance bias the key tiles are taken
 //    from the row's own position backwards, so that scores fall along the way
 //    and the reference need not be raised at every tile.
-//  * tanh: an odd polynomial on the FMA pipe (degree 11, |u| <= 1, within
+//  * tanh: an odd polynomial on the FMA pipe (degree 9, |u| <= 0.8, within
 //    5e-7), chosen per warp and tile by the largest |u|; beyond it, 1 - 2 /
 //    (1 + e^(2u)), whose two special-function operations per score cost 3400
 //    cycles per 128 keys where the polynomial costs 1300.
@@ -103,8 +103,8 @@ constexpr int kCounters = 2 + 2 * kSplitTarget;   // queue head, CTAs done, a ti
 struct PrefillGroupedArgs {
     GroupedArgs g;
     float scale_log2, cap_log2, cap_in;
-    float cap_v;                       // v = cap_v (q . k) has v^2 < 2 iff |s / cap| < 1
-    float tanh_k[6];                   // there, x = v (k0 + k1 v^2 + ... + k5 v^10)
+    float cap_v;                       // v = cap_v (q . k) has v^2 < 2 iff |s / cap| < 0.8
+    float tanh_k[5];                   // there, x = v (k0 + k1 v^2 + ... + k4 v^8)
     int group, tpt;                    // heads per K/V head; tokens per tile
     int num_pairs, splits;
     int store_boxes;                   // a warp's 32 rows are whole tokens: tm_out applies
@@ -591,10 +591,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const unsigned full = (1u << (kBN >> b_shift)) - 1;
         // the polynomial's coefficients as pairs, kept in registers (volatile: not
         // built again at each use, which took as many moves as products)
-        uint64_t tanh2[6], cap_v2;
+        uint64_t tanh2[5], cap_v2;
         if constexpr (kCap) {
 #pragma unroll
-            for (int i = 0; i < 6; ++i) tanh2[i] = keep_pair(p.tanh_k[i]);
+            for (int i = 0; i < 5; ++i) tanh2[i] = keep_pair(p.tanh_k[i]);
             cap_v2 = keep_pair(p.cap_v);
         }
         // The item before: its slot and its Q buffer, which holds the staged rows,
@@ -675,9 +675,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     v = mul_pair(make_pair(x0, x1), cap_v2);
                     const uint64_t w2 = mul_pair(v, v);
                     any |= static_cast<uint32_t>(w2) | static_cast<uint32_t>(w2 >> 32);
-                    y = fma_pair(tanh2[5], w2, tanh2[4]);
+                    y = fma_pair(tanh2[4], w2, tanh2[3]);
 #pragma unroll
-                    for (int i = 3; i >= 0; --i) y = fma_pair(y, w2, tanh2[i]);
+                    for (int i = 2; i >= 0; --i) y = fma_pair(y, w2, tanh2[i]);
                 };
                 // cap tanh(s / cap) + bias by 1 - 2 / (1 + e^(2 s / cap)), in log2 units
                 auto cap_mufu = [&](float s, float b) {
@@ -711,7 +711,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // slope (k0 + e - pos), rising along the tile
                     const float bias = kBias - m + (kAlibi ? slope * static_cast<float>(k0 - pos) : 0.f);
 #pragma unroll
-                    for (int e = 0; e < kBN; e += 2) {
+                    for (int z = 0; z < kBN / 2; ++z) {
+                        // pairs 8 apart in turn (in their order: capped 511 us instead
+                        // of 503, head_dim 64 327 instead of 324, at 8192 tokens)
+                        const int e = z / 8 * 16 + z % 2 * 8 + z / 2 % 4 * 2;
                         float y0, y1;
                         float b0 = bias, b1 = bias;
                         if constexpr (kAlibi) {
@@ -719,10 +722,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                             b1 = fmaf(slope, static_cast<float>(e + 1), bias);
                         }
                         if constexpr (kCap) {
-                            if (e % 8 == 6) {
+                            if (e % 8 == 0) {
                                 // one pair in four by the special-function unit, which
-                                // has time left: its two operations take 12 cycles an
-                                // element, the polynomial's products 10 of the FMA pipe
+                                // has time left (8192 tokens: none 540 us, one in eight
+                                // 543, in four 503, in three 516, 3 in 8 521)
                                 y0 = cap_mufu(x[e], b0);
                                 y1 = cap_mufu(x[e + 1], b1);
                             } else {
