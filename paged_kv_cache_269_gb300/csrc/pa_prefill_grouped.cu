@@ -8,8 +8,17 @@
 // raised when a tile's maximum exceeds it by more than 8 (a common factor of
 // weights and sum cancels, so m need not be the maximum).
 //
-// What bounds it: 4 D flops per (row, key) pair on the tensor cores, and one
-// ex2 per pair (three with the cap) on the special-function unit.
+// What bounds it: 4 D flops per (row, key) pair on the tensor cores; beside
+// them the softmax warps spend an ex2 a pair on the special-function unit, and
+// with the cap a polynomial of 6 products on the FMA pipe.
+//
+// Measured (32 heads on 4, one prompt of 8192 tokens, bf16): head_dim 128 333 us,
+// 1650 TFLOP/s, 0.86 of this GPU's largest library product, the products bound;
+// with distance biases 358 us; with the cap 503 us, 1093 TFLOP/s, the softmax
+// warps bound (FMA pipe, and two warps a scheduler to hide latencies); head_dim
+// 64 324 us, 847 TFLOP/s, the softmax again, with half the products a pair.  16
+// prompts of 333 to 1024 tokens, 32 heads on 8: 79 us, 840 TFLOP/s: the first
+// key tile of an item and its output cost as much as several tiles.
 //
 // How (persistent, one CTA per SM, 512 threads):
 //  * A tile is 128 rows of (token, head) pairs: 128 / G tokens x the G heads of
@@ -22,14 +31,14 @@
 //    keys x (64 dims, 64 dims), the operand layout of both products.  Issuing a
 //    copy takes about 100 cycles: with one warp for both and a copy per 64-dim
 //    half, 16 copies a tile took 1600 of its 2400 cycles.
-//  * Warps 9, 10 issue S = Q K^T of query tile 0 and 1 into one of two S/P
-//    buffers of tensor memory, ahead of the softmax, once the P V product that
+//  * Warps 9, 10 issue S = Q K^T of query tile 0 and 1 into the next of two S/P
+//    buffers of tensor memory (three at head_dim 64, where there is room), ahead of the softmax, once the P V product that
 //    last read the buffer is complete; warps 11, 12 issue O += P V (P read from
 //    tensor memory) once the softmax has stored P.  A thread's stream of
 //    tcgen05.mma is bound by its own issue and waits, so the four streams have
 //    warps of their own: with S and P V of a tile issued by one thread, a step
 //    of 64 keys took 2600 cycles, all of them the thread's.  The issuing lane
-//    is an elected one (1552 TFLOP/s on an 8192-token prompt; 1416 under
+//    is an elected one (at first 1552 TFLOP/s on that prompt, 1416 under
 //    `lane == 0`, where every operand is moved to a uniform register first).
 //  * Warps 0-3 / 4-7 (softmax of tile 0 / 1): thread = row = tensor-memory
 //    lane.  Loads its 64 scores, exponentiates, and stores the weights as
@@ -51,14 +60,20 @@
 //    second 16-bit term would cost half as much tensor work again.
 //  * V rows that no query may see (past the context, or of blocks that are not
 //    loaded) are cleared, since a zero weight times a NaN is NaN.
-//  * Few rows over long contexts: an item's key tiles are split over several
-//    CTAs, which leave partial (max, sum, output) and take a ticket; the last
-//    one joins them in order.
-//  * The output rows go through a staging buffer in shared memory and leave as
-//    one tensor copy per warp and 64 dims, while the softmax goes on with the
-//    next item (row by row they cost 6400 cycles an item, by coalesced stores
-//    3800).  Rows that are not 32 of whole tokens (a ragged end, or G that does
-//    not divide 32) take the coalesced stores.
+//  * Masks: tiles that every row of a warp sees whole take no mask; the causal
+//    diagonal is one bound per key under a minimum; windows, prefixes and blocks
+//    that are missing take a bit mask and a select a key.  A row without a query
+//    stands where its warp's last one does, so that it adds no mask (5 prompts
+//    of 517 to 2500 tokens, three heads to one: 67 us, and 49 so).
+//  * Few rows over long contexts: while there are fewer items than SMs, an
+//    item's key tiles are split over several CTAs, which leave partial (max,
+//    sum, output) and take a ticket; the last one joins them in order.
+//  * Q has two buffers, so that the next item's is there when its turn comes.
+//    The output rows are staged in their item's Q, whose products are complete,
+//    and leave as one tensor copy per warp and 64 dims, while the softmax goes
+//    on with the next item (row by row they cost 6400 cycles an item, by
+//    coalesced stores 3800).  Rows that are not 32 of whole tokens (a ragged
+//    end, or G that does not divide 32) take the coalesced stores.
 //  * Every wait is bounded; tensor memory is released on every path.
 #include <cuda.h>
 #include <cuda_bf16.h>
