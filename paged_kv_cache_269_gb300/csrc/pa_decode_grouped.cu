@@ -82,7 +82,7 @@ struct DecodeGroupedArgs {
     GroupedArgs g;
     float scale_log2;                  // plain scores: x = scale_log2 (q . k)
     float cap_log2, cap_in;            // capped: x = cap_log2 tanh(...), 2^(cap_in q.k) = e^(2 s / cap)
-    float cap_v, tanh_k[5];            // as a polynomial (fill_tanh), where |s / cap| < 0.8
+    float cap_v, tanh_k[5];            // as a polynomial (fill_tanh), where |s / cap| < 0.75
     int group, chunks;                 // heads per K/V head; chunks of heads per K/V head
     int chunk_shift;                   // sequences per prefix entry: 2^chunk_shift
     float *partials;                   // [2 * kMaxCtas][heads * (D + 2)]

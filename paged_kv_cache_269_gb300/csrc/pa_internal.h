@@ -156,15 +156,16 @@ struct GroupedArgs {
 };
 
 // softcap * tanh(scale x / softcap) in log2 units, as v (k0 + k1 v^2 + .. + k4
-// v^8) with v = cap_v x, where u = |scale x / softcap| < 0.8, that is v^2 < 2.
-// The odd polynomial of degree 9 with the least largest error on [0, 0.8] (a
-// linear program over 3000 points): off by at most 3.5e-7, 4.5e-7 evaluated in
-// fp32.  A term more would hold up to u = 1, a step of the softmax more for
-// every score; scores that far out take the exponential form instead.
+// v^8) with v = cap_v x, where u = |scale x / softcap| < 0.75, that is v^2 < 2.
+// The odd polynomial of degree 9 with the least largest relative error on
+// [0, 0.75] (a linear program over 3000 points): off by at most 6e-7 of the
+// value and 4e-7 in all, as one of degree 11 would be up to u = 1.  That term
+// is a step of the softmax more for every score; scores that far out take the
+// exponential form instead.
 inline void fill_tanh(float scale, float softcap, float *cap_v, float (&k)[5]) {
-    const double tanh_u[5] = {0.99999513443343968, -0.33317426517340881, 0.13186218927035279,
-                              -0.048261297051849339, 0.011464640653115934};
-    const double u_over_v = 0.56568542494923802, log2e = 1.4426950408889634;
+    const double tanh_u[5] = {0.99999943500438748, -0.33328250820635219, 0.13258976152428414,
+                              -0.050056102813472059, 0.012929458742386161};
+    const double u_over_v = 0.53033008588991064, log2e = 1.4426950408889634;
     *cap_v = softcap > 0.f ? static_cast<float>(scale / u_over_v / softcap) : 0.f;
     double power = softcap * log2e * u_over_v;
     for (int i = 0; i < 5; ++i, power *= u_over_v * u_over_v)

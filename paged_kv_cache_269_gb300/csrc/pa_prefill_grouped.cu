@@ -49,7 +49,7 @@
 //    and the maximum comes first.  With a distance bias the key tiles are taken
 //    from the row's own position backwards, so that scores fall along the way
 //    and the reference need not be raised at every tile.
-//  * tanh: an odd polynomial on the FMA pipe (degree 9, |u| <= 0.8, within
+//  * tanh: an odd polynomial on the FMA pipe (degree 9, |u| <= 0.75, within
 //    5e-7), chosen per warp and tile by the largest |u|; beyond it, 1 - 2 /
 //    (1 + e^(2u)), whose two special-function operations per score cost 3400
 //    cycles per 128 keys where the polynomial costs 1300.
@@ -118,7 +118,7 @@ constexpr int kCounters = 2 + 2 * kSplitTarget;   // queue head, CTAs done, a ti
 struct PrefillGroupedArgs {
     GroupedArgs g;
     float scale_log2, cap_log2, cap_in;
-    float cap_v;                       // v = cap_v (q . k) has v^2 < 2 iff |s / cap| < 0.8
+    float cap_v;                       // v = cap_v (q . k) has v^2 < 2 iff |s / cap| < 0.75
     float tanh_k[5];                   // there, x = v (k0 + k1 v^2 + ... + k4 v^8)
     int group, tpt;                    // heads per K/V head; tokens per tile
     int num_pairs, splits;
