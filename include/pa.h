@@ -524,7 +524,8 @@ int pa_decode_grouped(void *out, const void *q, const void *k_cache, const void 
                       uint32_t *counters, size_t counters_bytes, void *stream);
 
 /* Bytes of pa_decode_grouped's workspace ((size_t)-1 on invalid sizes) and
- * counters (0 on invalid sizes). */
+ * counters (0 on invalid sizes): a 32-bit word for each sequence, K/V head and
+ * chunk of its query heads, rounded up to 256 bytes. */
 size_t pa_decode_grouped_workspace_bytes(const pa_dims *dims, int32_t num_q_heads);
 size_t pa_decode_grouped_counters_bytes(const pa_dims *dims, int32_t num_q_heads);
 

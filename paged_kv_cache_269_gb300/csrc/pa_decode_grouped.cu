@@ -268,7 +268,7 @@ __device__ __forceinline__ bool take_ticket(const DecodeGroupedArgs &p, int s, i
                                             int others, int lane) {
     uint32_t last = 0;
     if (lane == 0) {
-        uint32_t *ticket = p.g.counters + 2 + static_cast<size_t>(s) * units + unit;
+        uint32_t *ticket = p.g.counters + static_cast<size_t>(s) * units + unit;   // a word a unit
         last = ticket_add(ticket, 1u) == static_cast<uint32_t>(others);
         if (last) atomicExch(ticket, 0u);
     }
@@ -936,10 +936,12 @@ Variant variant_of(int group) {
 size_t decode_grouped_workspace_bytes(int head_dim, int group) {
     return static_cast<size_t>(2 * kMaxCtas) * heads_per_chunk(head_dim, group) * (head_dim + 2) * 4;
 }
+// A ticket for every unit, and nothing else (take_ticket); never 0, which says
+// that the sizes are invalid.
 size_t decode_grouped_counters_bytes(int num_seqs, int num_kv_heads, int group, int head_dim) {
     const int per = heads_per_chunk(head_dim, group);
     const size_t tickets = static_cast<size_t>(num_seqs) * num_kv_heads * ((group + per - 1) / per);
-    return (tickets * 4 + 4 + 255) / 256 * 256;
+    return (tickets < 1 ? 1 : (tickets + 63) / 64) * 256;
 }
 
 cudaError_t launch_decode_grouped(const GroupedArgs &args, int dtype, int head_dim, int num_sms,

@@ -1,0 +1,67 @@
+"""GPU tests of the grouped calls at the edges of their buffers, and of what may
+not reach their outputs; references and bounds as in grouped_ref."""
+import pytest
+import torch
+
+import paged_kv_cache_269_gb300 as pa
+from grouped_ref import make_case
+from test_gpu_grouped import check, run_decode, to_dev
+
+pytestmark = pytest.mark.gpu
+F16, BF16 = torch.float16, torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    d = torch.device("cuda", 0)
+    torch.cuda.set_device(d)
+    pa.lib()
+    pa.device_errors()
+    return d
+
+
+# ------------------------------------------------------------------ buffers
+
+@pytest.mark.parametrize("S,H,group,D", [(63, 1, 4, 128), (127, 1, 4, 64), (21, 3, 2, 128), (64, 1, 4, 128),
+                                         (9, 7, 1, 64), (63, 1, 9, 256), (7, 3, 40, 64)])
+def test_decode_counters_of_the_stated_size(dev, S, H, group, D):
+    """Counters of exactly the stated size inside a larger tensor, at numbers of
+    tickets that fill it (or pass it by one): the last context, which several CTAs
+    share, is joined, and the words around the buffer stay as they were."""
+    ctx = [1 + 13 * s % 40 for s in range(S)]
+    ctx[-1] = 6000
+    c = make_case(101, ctx, [1] * S, H * group, H, D, 16, F16)
+    d = to_dev(c, dev)
+    n = pa.decode_grouped_counters_bytes(S, H * group, H, D, 16) // 4
+    guarded = torch.full((n + 128,), 0x5A5A5A5A, dtype=torch.int32, device=dev)
+    guarded[64:64 + n] = 0
+    ws = torch.empty(pa.decode_grouped_workspace_bytes(H * group, H, D, 16), dtype=torch.uint8, device=dev)
+    for _ in range(3):
+        out = run_decode(c, d, counters=guarded[64:64 + n], workspace=ws)
+        assert pa.device_errors() == 0
+        check(c, out, False)
+        assert not guarded[64:64 + n].any()
+        assert (guarded[:64] == 0x5A5A5A5A).all() and (guarded[64 + n:] == 0x5A5A5A5A).all()
+
+
+@pytest.mark.parametrize("S", [63, 127])
+def test_decode_counters_of_a_captured_call(dev, S):
+    """A captured call takes counters of the stated size from the graph's pool."""
+    ctx = [1 + 13 * s % 40 for s in range(S)]
+    ctx[-1] = 6000
+    c = make_case(102, ctx, [1] * S, 4, 1, 128, 16, BF16)
+    d = to_dev(c, dev)
+    out = torch.empty_like(d["q"])
+    run_decode(c, d, out)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run_decode(c, d, out)
+    for _ in range(3):
+        out.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        check(c, out, False)
+    assert pa.device_errors() == 0
