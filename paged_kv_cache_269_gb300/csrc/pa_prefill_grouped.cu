@@ -112,7 +112,7 @@ constexpr float kRaise = 8.f;          // where a maximum is taken, it is kept i
 constexpr float kBias = 4.f;
 template <bool kBf16> constexpr float kMostSum = kBf16 ? 1.1529215e18f : 32768.f;   // 2^60, 2^15
 constexpr float kFar = 1e30f;
-constexpr int kMaskRing = 16;
+constexpr int kMaskRing = 32;         // key tiles whose blocks are known; see Cfg
 // Work is split over keys while there are fewer items than SMs (152).
 constexpr int kSplitTarget = 152;
 constexpr int kCounters = 2 + 2 * kSplitTarget;   // queue head, CTAs done, a ticket per (item, tile)
@@ -175,6 +175,14 @@ struct Cfg {
     static constexpr int OFF_ITEM = OFF_MASK + kMaskRing * 4;       // Item[2]
     static constexpr int kSmemBytes = OFF_ITEM + 2 * static_cast<int>(sizeof(Item)) + 1024;
     static_assert(kSmemBytes <= 232448, "shared memory");
+    // A tile's entry in the mask ring is read by the softmax before its P and is
+    // rewritten without a wait, so the ring is longer than the K warp can get
+    // ahead of a softmax that stands at tile a: V is loaded up to a + kSlots - 1
+    // (P V of tile a holds its slot), the other query tile's S goes kBufs products
+    // past that and over the kBufs - 1 tiles for which the first one has S ahead,
+    // and K is loaded kSlots further.  With 16 entries a context's last key tile
+    // could stand in for another at head_dim 64.
+    static_assert(2 * kSlots + 2 * static_cast<int>(kBufs) - 2 < kMaskRing, "mask ring");
 };
 
 // kind::f16 instruction descriptor: fp32 accumulate, A and B fp16 or bf16, A

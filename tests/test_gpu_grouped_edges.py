@@ -4,8 +4,8 @@ import pytest
 import torch
 
 import paged_kv_cache_269_gb300 as pa
-from grouped_ref import make_case
-from test_gpu_grouped import check, run_decode, to_dev
+from grouped_ref import make_case, reference
+from test_gpu_grouped import check, run_decode, run_prefill, to_dev
 
 pytestmark = pytest.mark.gpu
 F16, BF16 = torch.float16, torch.bfloat16
@@ -65,3 +65,26 @@ def test_decode_counters_of_a_captured_call(dev, S):
         torch.cuda.synchronize()
         check(c, out, False)
     assert pa.device_errors() == 0
+
+
+# ------------------------------------------------------------------ prefill's roles
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("D,group,alibi", [(64, 4, False), (64, 4, True), (64, 1, False), (128, 4, False)])
+def test_prefill_tiles_of_unequal_pace(dev, dtype, D, group, alibi):
+    """Second query tiles whose softmax is slow at every key tile (an outlier past
+    the cap's polynomial), items whose second tile is empty behind them, and a last
+    key tile that ends inside a block: each tile masks with its own blocks."""
+    per = 128 // group
+    new = [per * (1 + 2 * (i % 4)) + i % 3 for i in range(60)]
+    ctx = [n + (997 - 13 * i) % 700 + 200 for i, n in enumerate(new)]
+    c = make_case(103, ctx, new, group, 1, D, 16, dtype, cap=10.0, alibi=alibi)
+    for s, n in enumerate(new):
+        for first in range(per, n, 2 * per):          # one token of every second tile
+            c.q[c.starts_list[s] + first] *= 40.0
+    d = to_dev(c, dev)
+    want, bound = (x.to(dev) for x in reference(c, True))
+    for _ in range(20):
+        got = run_prefill(c, d)
+        assert pa.device_errors() == 0
+        assert ((got.double() - want).abs() <= bound).all()

@@ -1,5 +1,9 @@
 """Edges of the rotary and grouped-query calls that need no GPU: sizes,
 refusals, and the state of the binding."""
+import os
+import random
+import re
+
 import pytest
 
 import paged_kv_cache_269_gb300 as pa
@@ -15,3 +19,61 @@ def test_decode_counters_hold_a_word_for_every_unit(D):
             n = pa.decode_grouped_counters_bytes(S, H * group, H, D, 16)
             assert n % 256 == 0 and n >= max(4 * units, 256)
             assert n < 4 * units + 512
+
+
+def _ahead(items, slots, bufs, descending, held_tile, held):
+    """How far past key tile `held` the K copies of the grouped prefill get while the
+    softmax of query tile `held_tile` stands there and every other role goes on as
+    far as its waits allow.  items: (key tiles, those tile 0 needs, those tile 1
+    needs or -1)."""
+    needs = []
+    for n, n0, n1 in items:
+        for j in range(n):
+            at = n - 1 - j if descending else j
+            needs.append((at < n0, at < n1))
+    total = len(needs)
+    own = [[i for i in range(total) if needs[i][t]] for t in (0, 1)]
+    if held not in own[held_tile]:
+        return 0
+    k = v = 0                                     # tiles of K and V loaded
+    s, pv = [0, 0], [0, 0]                        # tiles passed by the product threads
+    scores, weights, products = [0, 0], [0, 0], [0, 0]
+    while True:
+        before = (k, v, *s, *pv, *weights)
+        while k < total and (k < slots or min(s) > k - slots):
+            k += 1
+        while v < total and (v < slots or min(pv) > v - slots):
+            v += 1
+        for t in (0, 1):
+            while s[t] < k and not (needs[s[t]][t] and scores[t] - products[t] >= bufs):
+                scores[t] += needs[s[t]][t]
+                s[t] += 1
+            while weights[t] < scores[t] and not (t == held_tile and own[t][weights[t]] == held):
+                weights[t] += 1
+            while pv[t] < v and not (needs[pv[t]][t] and products[t] >= weights[t]):
+                products[t] += needs[pv[t]][t]
+                pv[t] += 1
+        if before == (k, v, *s, *pv, *weights):
+            return k - 1 - held
+
+
+def test_prefill_mask_ring_outlasts_its_slowest_reader():
+    """A key tile's entry is rewritten one ring later, without a wait: no order of
+    the roles may bring the copies that far ahead of a softmax yet to read it."""
+    path = os.path.join(os.path.dirname(pa.__file__), "csrc", "pa_prefill_grouped.cu")
+    src = open(path).read()
+    ring = int(re.search(r"kMaskRing = (\d+);", src).group(1))
+    slots = re.search(r"kSlots = D == 64 \? (\d+) : (\d+);", src).groups()
+    bufs = re.search(r"kBufs = D == 64 \? (\d+) : (\d+);", src).groups()
+    rng = random.Random(1)
+    for ns, nb in zip(map(int, slots), map(int, bufs)):
+        most = 0
+        for _ in range(6000):
+            items = []
+            for _ in range(rng.randint(2, 8)):
+                n = rng.choice([1, 1, 2, 2, 3, 4, 8, 16, 17])
+                items.append((n, n, -1) if rng.random() < 0.5 else (n, max(0, n - rng.randint(0, 3)), n))
+            tiles = sum(i[0] for i in items)
+            most = max(most, _ahead(items, ns, nb, rng.random() < 0.5, rng.randint(0, 1), rng.randrange(tiles)))
+        assert 0 < most <= 2 * ns + 2 * nb - 2    # the bound that the kernel asserts
+        assert most < ring
