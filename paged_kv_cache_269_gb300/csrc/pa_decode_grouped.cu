@@ -618,6 +618,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[ks][nt][e] = 0.f;
         }
+        // key k0 + i of a tile whose loaded boxes are `have`
+        auto visible = [&](int k0, int i, unsigned have) {
+            const int key = k0 + i;
+            return (key < g.pre || key >= g.lo) && key < g.ctx && ((have >> (i >> rb_shift)) & 1);
+        };
         while (queue[0] < seg_start + seg_len) {
             const int t = queue[0];
 #pragma unroll
@@ -657,8 +662,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  (k0 < g.lo && k0 + TK > g.pre);
             bool raise = false;
             if (a.softcap > 0.f) {
-                // by the polynomial if that holds for every score of the tile: a large
-                // cap would lose the low bits of small scores in 1 - 2 / (1 + e^(2u))
+                // Each score by the form that its own size asks for: the polynomial where it
+                // holds (small scores would lose their low bits in 1 - 2 / (1 + e^(2u))).
+                // So no score depends on another's, which may be of a key that is not
+                // visible or of a box that was not loaded; a tile without far ones skips
+                // the second form.
                 bool far = false;
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
@@ -677,15 +685,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             float &x = sc[mt][nt][e];
-                            if (far) {
-                                x = p.cap_log2 - 2.f * p.cap_log2 * fast_rcp(1.f + fast_exp2(x * p.cap_in));
-                            } else {
-                                const float v = x * p.cap_v, w = v * v;
-                                float y = p.tanh_k[4];
+                            const float s = x, v = x * p.cap_v, w = v * v;
+                            float y = p.tanh_k[4];
 #pragma unroll
-                                for (int i = 3; i >= 0; --i) y = fmaf(y, w, p.tanh_k[i]);
-                                x = v * y;
-                            }
+                            for (int i = 3; i >= 0; --i) y = fmaf(y, w, p.tanh_k[i]);
+                            x = v * y;
+                            if (far && !(w < 2.f))
+                                x = p.cap_log2 - 2.f * p.cap_log2 * fast_rcp(1.f + fast_exp2(s * p.cap_in));
                         }
             } else {
 #pragma unroll
@@ -704,11 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         float x = sc[mt][nt][e];
                         const int key = k0 + mt * 16 + row + (e >= 2 ? 8 : 0);
                         if (a.alibi_slopes) x -= slope[nt][e & 1] * static_cast<float>(g.ctx - 1 - key);
-                        if (partial) {
-                            const bool vis = (key < g.pre || key >= g.lo) && key < g.ctx &&
-                                             ((have >> ((key - k0) >> rb_shift)) & 1);
-                            x = vis ? x : -INFINITY;
-                        }
+                        if (partial) x = visible(k0, key - k0, have) ? x : -INFINITY;
                         sc[mt][nt][e] = x;
                         raise |= x > m[nt][e & 1] + kRaise;
                     }
@@ -770,9 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         keep0 = keep1 = 0;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const int key = k0 + mt * 16 + col + (e & 1) + (e >= 2 ? 8 : 0);
-                            const bool vis = (key < g.pre || key >= g.lo) && key < g.ctx &&
-                                             ((have >> ((key - k0) >> rb_shift)) & 1);
+                            const bool vis = visible(k0, mt * 16 + col + (e & 1) + (e >= 2 ? 8 : 0), have);
                             const uint32_t bits = vis ? ((e & 1) ? 0xFFFF0000u : 0xFFFFu) : 0u;
                             if (e < 2)
                                 keep0 |= bits;

@@ -52,9 +52,9 @@
 //    from the row's own position backwards, so that scores fall along the way
 //    and the reference need not be raised at every tile.
 //  * tanh: an odd polynomial on the FMA pipe (degree 9, |u| <= 0.75, within
-//    5e-7), chosen per warp and tile by the largest |u|; beyond it, 1 - 2 /
-//    (1 + e^(2u)), whose two special-function operations per score cost 3400
-//    cycles per 128 keys where a polynomial of degree 11 cost 1300.
+//    5e-7); a tile with visible scores past that is taken again with 1 - 2 /
+//    (1 + e^(2u)) for these, whose two special-function operations per score
+//    cost 3400 cycles per 128 keys where a polynomial of degree 11 cost 1300.
 //  * The weights are rounded to 16 bits (the element type) before P V, the sum
 //    is taken before the rounding, in fp32.  A weight is then off by half a
 //    step of the type, independently of its neighbours, so the output's error
@@ -747,15 +747,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                             b1 = fmaf(slope, static_cast<float>(e + 1), bias);
                         }
                         if constexpr (kCap) {
+                            // what is not visible has no say in the form of tanh
+                            float x0 = x[e], x1 = x[e + 1];
+                            if constexpr (decltype(masked)::value == 2) {
+                                x0 = (vis[e / 32] >> (e % 32)) & 1 ? x0 : 0.f;
+                                x1 = (vis[e / 32] >> (e % 32 + 1)) & 1 ? x1 : 0.f;
+                            }
                             if (e % 8 == 0) {
                                 // one pair in four by the special-function unit, which
                                 // has time left (8192 tokens: none 540 us, one in eight
                                 // 543, in four 503, in three 516, 3 in 8 521)
-                                y0 = cap_mufu(x[e], b0);
-                                y1 = cap_mufu(x[e + 1], b1);
+                                y0 = cap_mufu(x0, b0);
+                                y1 = cap_mufu(x1, b1);
                             } else {
                                 uint64_t v, y;
-                                cap_poly(x[e], x[e + 1], v, y, any);
+                                cap_poly(x0, x1, v, y, any);
                                 split_pair(fma_pair(v, y, make_pair(b0, b1)), y0, y1);
                             }
                         } else {
@@ -781,34 +787,48 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (fast) {
                     if (all_visible)
                         weights(std::integral_constant<int, 0>{});
-                    else if (have == full && a.window == 0 && pre_all <= k0)
+                    else if (!kCap && have == full && a.window == 0 && pre_all <= k0)
                         weights(std::integral_constant<int, 1>{});
                     else
                         weights(std::integral_constant<int, 2>{});
                     // the sum bounds every weight; v^2 < 2
                     // that the polynomial holds (no bit pattern reaches that of 2)
                     done_fast = warp_all(sum <= kMostSum<kBf16> && any < 0x40000000u);
-                    if (!done_fast) load_raw();
+                    if (!kCap && !done_fast) load_raw();
                 }
                 if (!done_fast) {
                     // scores to the log2 domain
                     if constexpr (kCap) {
-                        uint32_t any = 0;
+                        // in tensor memory, 16 at a time: each by the form that its own size
+                        // asks for, so that no score depends on another's, seen or not.
+                        // (Unrolled in registers over the tile, or 32 at a time, this took
+                        // the loop's other tiles 4 to 8 % longer: 8192 tokens 521 to 540 us
+                        // instead of 503.)
+#pragma unroll 1
+                        for (int q = 0; q < kBN / 16; ++q) {
+                            uint32_t u[16], far = 0;
+                            tmem_ld16_nowait(s_col + q * 16, u);
+                            tmem_ld_wait();
+                            float z[16];
 #pragma unroll
-                        for (int e = 0; e < kBN; ++e)
-                            any |= __float_as_uint((x[e] * p.cap_v) * (x[e] * p.cap_v));
-                        if (warp_all(any < 0x40000000u)) {
-#pragma unroll
-                            for (int e = 0; e < kBN; e += 2) {
+                            for (int e = 0; e < 16; e += 2) {
                                 uint64_t v, y;
-                                cap_poly(x[e], x[e + 1], v, y, any);
-                                split_pair(mul_pair(v, y), x[e], x[e + 1]);
+                                cap_poly(__uint_as_float(u[e]), __uint_as_float(u[e + 1]), v, y, far);
+                                split_pair(mul_pair(v, y), z[e], z[e + 1]);
                             }
-                        } else {
+                            if (!warp_all(far < 0x40000000u)) {
 #pragma unroll
-                            for (int e = 0; e < kBN; ++e)
-                                x[e] = cap_mufu(x[e], 0.f);
+                                for (int e = 0; e < 16; ++e) {
+                                    const float v = __uint_as_float(u[e]) * p.cap_v;
+                                    if (!(v * v < 2.f)) z[e] = cap_mufu(__uint_as_float(u[e]), 0.f);
+                                }
+                            }
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(z[e]);
+                            tmem_st16(s_col + q * 16, u);
                         }
+                        tmem_st_wait();
+                        load_raw();
                     } else {
 #pragma unroll
                         for (int e = 0; e < kBN; ++e) x[e] *= c;

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import paged_kv_cache_269_gb300 as pa
-from grouped_ref import make_case, reference
+from grouped_ref import make_case, reference, seen_mask
 from test_gpu_grouped import check, run_decode, run_prefill, to_dev
 
 pytestmark = pytest.mark.gpu
@@ -88,3 +88,56 @@ def test_prefill_tiles_of_unequal_pace(dev, dtype, D, group, alibi):
         got = run_prefill(c, d)
         assert pa.device_errors() == 0
         assert ((got.double() - want).abs() <= bound).all()
+
+
+# ------------------------------------------------------------------ what no query sees
+
+def _unseen_keys(c):
+    """[N, B] bool: slots of the pool that no query sees."""
+    seen = torch.zeros(c.k_cache.shape[0], c.B, dtype=torch.bool)
+    for s, ctx in enumerate(c.ctx):
+        if c.new[s]:
+            for j in seen_mask(c, s).any(0).nonzero().flatten().tolist():
+                seen[int(c.tables[s, j // c.B]), j % c.B] = True
+    return ~seen
+
+
+def _same_whatever_is_unseen(c, dev, run, weights16):
+    """One result, to the bit, whatever the unseen key rows hold and whatever a call
+    before has left in the shared memory of boxes that are not loaded."""
+    d = to_dev(c, dev)
+    unseen = _unseen_keys(c).to(dev)[:, None, :, None]
+    dirty = make_case(1, [128] * 320, [1] * 320, c.q_heads, c.kv_heads, c.D, c.B, c.dtype)
+    dd = to_dev(dirty, dev)
+    dd["v_cache"].zero_()
+    first = None
+    for value in (0.0, float("nan"), 6e4, -6e4, float("inf")):
+        k = torch.where(unseen, torch.full_like(d["k_cache"], value), d["k_cache"])
+        dd["k_cache"].fill_(value)
+        for _ in range(3):
+            run(dirty, dd)
+            got = run(c, dict(d, k_cache=k))
+            first = got if first is None else first
+            assert torch.equal(first, got), f"unseen keys of {value}"
+    assert pa.device_errors() == 0
+    check(c, first, weights16)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("D,B,group", [(64, 16, 2), (64, 8, 8), (64, 32, 9), (128, 16, 4), (128, 32, 8), (256, 8, 2)])
+def test_capped_decode_ignores_unseen_keys(dev, dtype, D, B, group):
+    ctx = [10, 45, 300, 17, 1, 130]
+    c = make_case(104, ctx, [1] * 6, 2 * group, 2, D, B, dtype, cap=50.0, window=37, prefix=[0, 3, 0, 17, 1, 40])
+    _same_whatever_is_unseen(c, dev, run_decode, False)
+    c = make_case(105, ctx, [1] * 6, 2 * group, 2, D, B, dtype, cap=20.0, alibi=True)
+    _same_whatever_is_unseen(c, dev, run_decode, False)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("D,B,alibi", [(64, 16, False), (64, 8, True), (128, 16, False), (128, 32, True)])
+def test_capped_prefill_ignores_unseen_keys(dev, dtype, D, B, alibi):
+    ctx, new = [10, 45, 300, 17, 200], [4, 45, 30, 1, 130]
+    c = make_case(106, ctx, new, 8, 2, D, B, dtype, cap=50.0, window=37, prefix=[0, 3, 0, 17, 40], alibi=alibi)
+    _same_whatever_is_unseen(c, dev, run_prefill, True)
+    c = make_case(107, ctx, new, 8, 2, D, B, dtype, cap=20.0, alibi=alibi)
+    _same_whatever_is_unseen(c, dev, run_prefill, True)
