@@ -360,16 +360,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         *abort_flag = 0;
         mbar_init_fence();
     }
-    // rows that no copy of Q fills (G that does not divide 128): zero, so that
-    // nothing left there slows their warp down
-    const int filled = p.tpt * p.group;
-    if (filled < kBM) {
-        for (int i = threadIdx.x; i < (kBM - filled) * 8 * C::kHalves * 4; i += kThreads) {
-            const int c = i % 8, rr = filled + i / 8 % (kBM - filled), hq = i / 8 / (kBM - filled);
-            *reinterpret_cast<uint4 *>(smem + C::OFF_Q + hq * C::kHalfQ + rr * 128 + c * 16) = make_uint4(0, 0, 0, 0);
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    }
     if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_addr(const_cast<uint32_t *>(tmem_slot))),
@@ -657,8 +647,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 continue;
             }
             // The row's position.  A row without a query stands where the warp's last
-            // query does, so that it costs the warp no mask, and is not written; in
-            // a warp without any, every row is at -1 and sees nothing.
+            // query does, so that it costs the warp no mask; in a warp without any,
+            // every row is at -1 and sees nothing.  Its Q is another sequence's, or what
+            // an earlier item's output has left there, so it is not written and has no
+            // say in what the warp does.
             const bool live = tok < min(p.tpt, it->q_len - it->tok0 - t * p.tpt);
             const int own = live ? it->first_pos + t * p.tpt + tok : -1;
             const int wmax = __reduce_max_sync(0xffffffffu, own);
@@ -669,8 +661,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             float slope = 0.f;
             if constexpr (kAlibi)
                 slope = pos >= 0 ? __ldg(a.alibi_slopes + it->hk * p.group + head) * 1.4426950408889634f : 0.f;
-            // (m = 0 where nothing is seen: no maximum is missing)
-            float m = pos >= 0 ? -INFINITY : 0.f, l = 0.f;
+            // (m = 0 in rows without a query: no maximum is missing)
+            float m = live ? -INFINITY : 0.f, l = 0.f;
             for (int j = 0; j < nk; ++j, ++n) {
                 const uint32_t buf = n % C::kBufs;
                 ok = warp_all(mbar_wait(&bar[C::S_FULL + t * 3 + buf], (n / C::kBufs) & 1, abort_flag, a.err));
@@ -793,7 +785,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         weights(std::integral_constant<int, 2>{});
                     // the sum bounds every weight; v^2 < 2
                     // that the polynomial holds (no bit pattern reaches that of 2)
-                    done_fast = warp_all(sum <= kMostSum<kBf16> && any < 0x40000000u);
+                    done_fast = warp_all((sum <= kMostSum<kBf16> && any < 0x40000000u) || !live);
                     if (!kCap && !done_fast) load_raw();
                 }
                 if (!done_fast) {
@@ -855,7 +847,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
                                             fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
                     const bool raise = top > m + kRaise;
-                    if (__any_sync(0xffffffffu, raise)) {
+                    if (__any_sync(0xffffffffu, raise && live)) {
                         const float m_new = raise ? top : m;
                         const float alpha = m == m_new ? 1.f : fast_exp2(m - m_new);
                         m = m_new;

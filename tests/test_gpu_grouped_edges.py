@@ -141,3 +141,38 @@ def test_capped_prefill_ignores_unseen_keys(dev, dtype, D, B, alibi):
     _same_whatever_is_unseen(c, dev, run_prefill, True)
     c = make_case(107, ctx, new, 8, 2, D, B, dtype, cap=20.0, alibi=alibi)
     _same_whatever_is_unseen(c, dev, run_prefill, True)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("D,group", [(128, 3), (64, 3), (128, 4), (64, 5), (128, 12)])
+@pytest.mark.parametrize("cap", [0.0, 20.0])
+def test_prefill_rows_of_others_do_not_round(dev, dtype, D, group, cap):
+    """A sequence's result is the same to the bit whatever the queries of its
+    neighbours in the pack and the rows behind the last sequence hold: rows of a tile
+    that are not the sequence's, and rows that no query fills when the heads do not
+    divide 128, decide nothing."""
+    S = 100
+    new = [1 + (37 * s) % 90 for s in range(S)]
+    ctx = [n + (53 * s) % 150 for s, n in enumerate(new)]
+    c = make_case(108, ctx, new, 2 * group, 2, D, 16, dtype, cap=cap)
+    d = to_dev(c, dev)
+    rows = c.starts_list[-1]
+    mine = torch.zeros(rows, dtype=torch.bool)
+    for s in range(0, S, 2):
+        mine[c.starts_list[s]:c.starts_list[s + 1]] = True
+    mine = mine.to(dev)
+    first = None
+    for value in (None, 0.0, float("nan"), 300.0, -300.0, float("inf")):
+        q = torch.cat([d["q"], torch.zeros(40, 2 * group, D, dtype=dtype, device=dev)])
+        if value is not None:
+            q[:rows][~mine] = value
+            q[rows:] = value
+        for _ in range(3):
+            got = torch.full_like(q, 7.0)
+            run_prefill(c, dict(d, q=q), got)
+            assert (got[rows:] == 7.0).all()
+            if first is None:
+                check(c, got[:rows], True)
+                first = got[:rows][mine]
+            assert torch.equal(first, got[:rows][mine]), f"other queries of {value}"
+    assert pa.device_errors() == 0
