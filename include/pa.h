@@ -473,9 +473,9 @@ int pa_rope_and_cache(void *q_out, const void *q, const void *k, const void *v, 
  * queries: to later ones past the window, and to earlier ones before them in
  * the sequence (a prompt's part that is read in both directions).
  *
- * tanh is taken in fp32, so a capped score is off by up to softcap * 2^-20:
- * nothing at caps of the scores' own size (20 to 100), but a softcap of 10^5
- * or more, set to say "no cap", costs a tenth of a score.  0 says that.
+ * tanh is taken in fp32: a capped score is off by at most 2^-20 of itself, and in
+ * pa_prefill_grouped, for softcap up to 128 (fp16) or 1024 (bf16), by at most
+ * 2^-20 of softcap; past that, prompts take about a third longer.
  */
 typedef struct pa_attn_opts {
     float softcap;               /* 0: none; otherwise finite and > 0                     */

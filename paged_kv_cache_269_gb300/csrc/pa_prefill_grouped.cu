@@ -112,6 +112,12 @@ constexpr float kRaise = 8.f;          // where a maximum is taken, it is kept i
 constexpr float kBias = 4.f;
 template <bool kBf16> constexpr float kMostSum = kBf16 ? 1.1529215e18f : 32768.f;   // 2^60, 2^15
 constexpr float kFar = 1e30f;
+// Up to this cap one score in four may be taken by 1 - 2 / (1 + e^(2u)) whatever
+// its size, which is off by up to 2^-20 of the cap: a quarter of what the weights'
+// rounding to the type moves.  Past it every score is taken by the form of its own
+// size, off by 2^-20 of itself, in the second form of the weights (one prompt of
+// 8192 tokens 504 us at a cap of 30, 686 past the limit).
+template <bool kBf16> constexpr float kShareCap = kBf16 ? 1024.f : 128.f;
 constexpr int kMaskRing = 32;         // key tiles whose blocks are known; see Cfg
 // Work is split over keys while there are fewer items than SMs (152).
 constexpr int kSplitTarget = 152;
@@ -122,6 +128,7 @@ struct PrefillGroupedArgs {
     float scale_log2, cap_log2, cap_in;
     float cap_v;                       // v = cap_v (q . k) has v^2 < 2 iff |s / cap| < 0.75
     float tanh_k[5];                   // there, x = v (k0 + k1 v^2 + ... + k4 v^8)
+    int cap_share;                     // the first form may take scores in either way
     int group, tpt;                    // heads per K/V head; tokens per tile
     int num_pairs, splits;
     int store_boxes;                   // a warp's 32 rows are whole tokens: tm_out applies
@@ -717,7 +724,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // First against the reference as it is (with the distance bias: if no
                 // visible key is ahead of the row).
                 bool done_fast = false;
-                const bool fast = (!kAlibi || pre_all <= k0 || k0 + kBN - 1 <= wmin) && warp_all(m != -INFINITY);
+                const bool fast = (!kAlibi || pre_all <= k0 || k0 + kBN - 1 <= wmin) && warp_all(m != -INFINITY) &&
+                                  (!kCap || p.cap_share);
                 uint32_t any = 0;
                 auto weights = [&](auto masked) {
                     uint32_t vis[kBN / 32];
@@ -1127,6 +1135,7 @@ cudaError_t launch_prefill_grouped(const GroupedArgs &args, int dtype, int head_
     p.cap_in = args.softcap > 0.f ? static_cast<float>(2.0 * args.scale / args.softcap * log2e) : 0.f;
     p.group = Hq / Hk;
     fill_tanh(args.scale, args.softcap, &p.cap_v, p.tanh_k);
+    p.cap_share = args.softcap <= (bf16 ? kShareCap<true> : kShareCap<false>);
     p.tpt = kBM / p.group;
     const Plan pl = make_plan(args.num_seqs, Hk, p.group, args.max_q);
     const long long items = pl.base * pl.splits;   // fits an int (the caller checks), with room past the end

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import paged_kv_cache_269_gb300 as pa
-from grouped_ref import make_case, reference, seen_mask
+from grouped_ref import TINY, U, make_case, reference, seen_mask
 from test_gpu_grouped import check, run_decode, run_prefill, to_dev
 
 pytestmark = pytest.mark.gpu
@@ -175,4 +175,52 @@ def test_prefill_rows_of_others_do_not_round(dev, dtype, D, group, cap):
                 check(c, got[:rows], True)
                 first = got[:rows][mine]
             assert torch.equal(first, got[:rows][mine]), f"other queries of {value}"
+    assert pa.device_errors() == 0
+
+
+# ------------------------------------------------------------------ caps
+
+def _capped_reference(c, weights16, share):
+    """As grouped_ref.reference for a capped call without biases, but each score is
+    off by 2^-20 of itself where it was 2^-20 of the cap (share: 2^-20 of the
+    cap, for one score in four).  The cap's slope is at most 1, so the dot
+    product's error passes through it undiminished at most."""
+    out, bound = torch.zeros(c.q.shape).double(), torch.zeros(c.q.shape).double()
+    G, u = c.q_heads // c.kv_heads, U[c.dtype]
+    for s, ctx in enumerate(c.ctx):
+        r = slice(c.starts_list[s], c.starts_list[s + 1])
+        seen = seen_mask(c, s)
+        blk, off = c.tables[s, torch.arange(ctx) // c.B].long(), torch.arange(ctx) % c.B
+        for hq in range(c.q_heads):
+            K, V = c.k_cache[blk, hq // G, off].double(), c.v_cache[blk, hq // G, off].double()
+            q = c.q[r, hq].double()
+            x = c.cap * torch.tanh(q @ K.T * c.scale / c.cap)
+            d = c.D * 2.0 ** -23 * abs(c.scale) * (q.abs() @ K.abs().T)
+            d = d + 2.0 ** -20 * (c.cap if share else x.abs()) + 2.0 ** -21 * x.abs()
+            x = x.masked_fill(~seen, float("-inf"))
+            w = torch.softmax(x, -1)
+            mag = w @ V.abs()
+            d = torch.where(x >= x.amax(-1, keepdim=True) - 28.0, d, torch.zeros_like(d))
+            n = seen.sum(-1, keepdim=True).double()
+            rel = 2.1 * d.amax(-1, keepdim=True) + (64 + n / 16) * 2.0 ** -23 + (u if weights16 else 2.0 ** -16)
+            out[r, hq] = w @ V
+            bound[r, hq] = (u * out[r, hq].abs() + rel * mag) * 1.001 + TINY[c.dtype]
+    return out, bound
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("cap", [3.0, 128.0, 129.0, 1e3, 1025.0, 1e5, 1e7, 1e25])
+def test_caps_of_any_size_keep_the_scores(dev, dtype, cap):
+    """A cap far above the scores changes nothing, one among them bends them, and
+    neither costs a score more than 2^-20 of itself (prefill: 2^-20 of a cap up to 128
+    in fp16, 1024 in bf16)."""
+    for D, group in ((128, 4), (64, 2)):
+        c = make_case(109, [90, 300], [1, 1], 2 * group, 2, D, 16, dtype, cap=cap, q_scale=3.0)
+        got = run_decode(c, to_dev(c, dev)).cpu().double()
+        want, bound = _capped_reference(c, False, False)
+        assert ((got - want).abs() <= bound).all()
+        c = make_case(110, [90, 300, 70], [90, 200, 3], 2 * group, 2, D, 16, dtype, cap=cap, q_scale=3.0)
+        got = run_prefill(c, to_dev(c, dev)).cpu().double()
+        want, bound = _capped_reference(c, True, cap <= (128.0 if dtype == F16 else 1024.0))
+        assert ((got - want).abs() <= bound).all()
     assert pa.device_errors() == 0
