@@ -478,7 +478,8 @@ int pa_rope_and_cache(void *q_out, const void *q, const void *k, const void *v, 
  * 2^-20 of softcap; past that, prompts take about a third longer.
  */
 typedef struct pa_attn_opts {
-    float softcap;               /* 0: none; otherwise finite and > 0                     */
+    float softcap;               /* 0: none; otherwise in [2^-100, 2^100], and so is
+                                    |scale| / softcap (scale 0 goes too)                  */
     int32_t window;              /* 0: none; otherwise >= 1                               */
     const float *alibi_slopes;   /* device, fp32 [num_q_heads], or NULL                   */
     const int32_t *prefix_lens;  /* device, int32 [S], or NULL; clamped to [0, ctx]       */
@@ -510,8 +511,8 @@ typedef struct pa_attn_opts {
  * [0, N) flags PA_DEVERR_TABLE and its keys are left out.
  * PA_ERR_SHAPE if num_q_heads is not a positive multiple of H, N * H * B or
  * S * num_q_heads exceeds INT32_MAX, max_blocks_per_seq * B exceeds 2^30, S
- * exceeds 2^28, window < 0, or softcap is negative or not finite.  out must not
- * overlap the inputs.
+ * exceeds 2^28, window < 0, scale is not finite or past 2^100, or softcap is out
+ * of its range.  out must not overlap the inputs.
  *
  * Each K and V row is read once for all query heads that share it (in chunks
  * of 16 heads; of 8 for D = 256).  Scores, softmax and sums are fp32; the

@@ -25,9 +25,19 @@ int check_grouped_dims(const pa_dims *dims, int32_t num_q_heads, bool need_seqs)
     return PA_OK;
 }
 
-int check_opts(const pa_attn_opts *o) {
+// The scale and the score options.  The kernels hold scale log2(e), softcap
+// log2(e) and scale / softcap in fp32, so these have to be numbers that fp32
+// holds with room on both sides (scale 0 is one: every score is 0).
+int check_scores(float scale, const pa_attn_opts *o) {
+    const double wide = 1.2676506002282294e30;   // 2^100
+    if (!isfinite(scale) || fabs(scale) > wide) return PA_ERR_SHAPE;
     if (!o) return PA_OK;
     if (!isfinite(o->softcap) || o->softcap < 0.f || o->window < 0) return PA_ERR_SHAPE;
+    if (o->softcap > 0.f) {
+        const double turn = fabs(static_cast<double>(scale)) / o->softcap;
+        if (o->softcap > wide || o->softcap < 1. / wide || turn > wide || (scale != 0.f && turn < 1. / wide))
+            return PA_ERR_SHAPE;
+    }
     return PA_OK;
 }
 
@@ -162,11 +172,10 @@ int pa_decode_grouped(void *out, const void *q, const void *k_cache, const void 
                       uint32_t *counters, size_t counters_bytes, void *stream) {
     int rc = check_grouped_dims(dims, num_q_heads, true);
     if (rc != PA_OK) return rc;
-    rc = check_opts(opts);
+    rc = check_scores(scale, opts);
     if (rc != PA_OK) return rc;
     rc = check_ranges(dims, num_q_heads, max_blocks_per_seq);
     if (rc != PA_OK) return rc;
-    if (!isfinite(scale)) return PA_ERR_SHAPE;
     if (dims->num_seqs == 0) return PA_OK;
     if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens) return PA_ERR_NULL;
     if (!aligned(out, 16) || !aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
@@ -216,11 +225,11 @@ int pa_prefill_grouped(void *out, const void *q, const void *k_cache, const void
     if (!prefill_grouped_supported(dims->dtype, dims->head_dim, dims->block_size,
                                    num_q_heads / dims->num_heads))
         return PA_ERR_UNSUPPORTED;
-    rc = check_opts(opts);
+    rc = check_scores(scale, opts);
     if (rc != PA_OK) return rc;
     rc = check_ranges(dims, num_q_heads, max_blocks_per_seq);
     if (rc != PA_OK) return rc;
-    if (!isfinite(scale) || total_query_tokens < 0 || max_query_len < 0) return PA_ERR_SHAPE;
+    if (total_query_tokens < 0 || max_query_len < 0) return PA_ERR_SHAPE;
     // work items (query tiles x sequences x K/V heads) are counted in 32 bits
     if (prefill_grouped_items(dims->num_seqs, dims->num_heads, num_q_heads / dims->num_heads, max_query_len) >
         0x7fffffffLL - 4096)

@@ -1,5 +1,6 @@
 """Edges of the rotary and grouped-query calls that need no GPU: sizes,
 refusals, and the state of the binding."""
+import ctypes
 import os
 import random
 import re
@@ -7,6 +8,7 @@ import re
 import pytest
 
 import paged_kv_cache_269_gb300 as pa
+from paged_kv_cache_269_gb300.grouped import AttnOpts
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])
@@ -77,3 +79,26 @@ def test_prefill_mask_ring_outlasts_its_slowest_reader():
             most = max(most, _ahead(items, ns, nb, rng.random() < 0.5, rng.randint(0, 1), rng.randrange(tiles)))
         assert 0 < most <= 2 * ns + 2 * nb - 2    # the bound that the kernel asserts
         assert most < ring
+
+
+FAKE = ctypes.c_void_p(0x100000)     # never dereferenced: the checks fail first
+
+
+def test_scales_and_caps_that_fp32_cannot_hold_are_refused():
+    lib = pa.lib()
+
+    def refused(scale, cap):
+        d, o = pa.Dims(2, 4, 128, 16, 32, 0), AttnOpts(cap, 0, None, None)
+        # no counters: a call that the numbers do not stop is stopped there (-5)
+        rc = {lib.pa_decode_grouped(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, scale, 8, ctypes.byref(d), 8, ctypes.byref(o),
+                                    FAKE, 1 << 30, None, 0, None),
+              lib.pa_prefill_grouped(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 4, 4, scale, 8, ctypes.byref(d), 8,
+                                     ctypes.byref(o), FAKE, 1 << 30, None, 0, None)}
+        assert rc in ({-2}, {-5})
+        return rc == {-2}
+
+    assert refused(3e38, 0.0) and refused(-3e38, 0.0) and refused(float("inf"), 0.0)
+    assert refused(0.1, 1e-39) and refused(0.1, 1e-31) and refused(0.1, 3e38)
+    assert refused(1e25, 1e-25) and refused(1e-20, 1e15)
+    assert not refused(1e30, 0.0) and not refused(0.0, 50.0) and not refused(-0.1, 50.0)
+    assert not refused(0.1, 1e-25) and not refused(0.1, 1e25) and not refused(1e-38, 0.0)
