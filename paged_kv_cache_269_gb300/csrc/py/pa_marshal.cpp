@@ -169,7 +169,9 @@ bool attention(Args &g, Attention *x) {
         return false;
     x->d.num_seqs = static_cast<int32_t>(x->S);
     x->scale = static_cast<float>(PyFloat_AsDouble(a[6]));
-    x->opts.softcap = static_cast<float>(number(a[7]));
+    const double cap = number(a[7]);
+    x->opts.softcap = static_cast<float>(cap);
+    if (x->opts.softcap == 0.f && cap != 0.0) return false;   // 0 would say "none"
     const long window = integer(a[9]);
     if (PyErr_Occurred() || window < 0 || window > 0x7fffffff) return false;
     x->opts.window = static_cast<int32_t>(window);

@@ -110,6 +110,27 @@ def _caches(k_cache, v_cache):
     return index, device, code, et, shape
 
 
+_I32_MAX = 0x7fffffff
+
+
+def _bound(value, name):
+    """An upper bound (a window, the longest query) for a 32-bit argument, which
+    would otherwise keep its low 32 bits: one past them bounds nothing."""
+    n = int(value)
+    if n != value:
+        raise ValueError(f"{name} must be a whole number, got {value}")
+    return max(-1, min(n, _I32_MAX))
+
+
+def _cap(softcap):
+    """The softcap as the fp32 number the library gets; one that would become 0
+    there, which means none, is refused."""
+    cap = ctypes.c_float(softcap or 0.0).value
+    if cap == 0.0 and softcap:
+        raise ValueError(f"softcap {softcap} is out of range")
+    return cap
+
+
 # What the library needs for given sizes (pure functions of them).
 @functools.lru_cache(maxsize=4096)
 def _decode_needs(S, Hq, H, D, B, code):
@@ -307,7 +328,10 @@ def _attention_args(what, out, q, k_cache, v_cache, block_tables, context_lens, 
     if H == 0 or Hq == 0 or Hq % H:
         raise ValueError(f"{what}: query heads must be a multiple of the cache's heads")
     opts = None
-    if softcap or window or alibi_slopes is not None or prefix_lens is not None:
+    cap, span = _cap(softcap), _bound(window or 0, "window")
+    if MB > _I32_MAX:
+        raise ValueError(f"{what}: block_tables are too wide")
+    if cap or span or alibi_slopes is not None or prefix_lens is not None:
         a_p = x_p = None
         if alibi_slopes is not None:
             a_p = _plain(alibi_slopes, "alibi_slopes", _F32, 1, index, dev)
@@ -317,7 +341,7 @@ def _attention_args(what, out, q, k_cache, v_cache, block_tables, context_lens, 
             x_p = _plain(prefix_lens, "prefix_lens", _I32, 1, index, dev)
             if prefix_lens.shape[0] != S:
                 raise ValueError(f"{what}: prefix_lens must have one entry per sequence")
-        opts = ctypes.byref(AttnOpts(float(softcap or 0.0), int(window or 0), a_p, x_p))
+        opts = ctypes.byref(AttnOpts(cap, span, a_p, x_p))
     head = (o_p, q_p, k_cache.data_ptr(), v_cache.data_ptr(), t_p, l_p)
     return index, dev, S, Hq, (H, D, B, code), MB, shape[0], head, _pa().Dims(S, H, D, B, N, code), opts
 
@@ -462,7 +486,7 @@ def prefill_grouped(out, q, k_cache, v_cache, block_tables, context_lens, query_
                                    workspace, counters, stream)
     if max_query_len is None:
         max_query_len = int((query_start[1:] - query_start[:-1]).max()) if S else 0
-    max_query_len = int(max_query_len)
+    max_query_len = _bound(max_query_len, "max_query_len")
     need_ws, need_ctr = _prefill_needs(S, Hq, *sizes, max_query_len)
     if need_ws == pa._SIZE_ERROR or need_ctr == 0:
         raise pa.PaError(-3, "prefill_grouped: unsupported head_dim, block_size or heads, or "

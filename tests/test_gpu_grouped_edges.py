@@ -224,3 +224,29 @@ def test_caps_of_any_size_keep_the_scores(dev, dtype, cap):
         want, bound = _capped_reference(c, True, cap <= (128.0 if dtype == F16 else 1024.0))
         assert ((got - want).abs() <= bound).all()
     assert pa.device_errors() == 0
+
+
+# ------------------------------------------------------------------ the binding's numbers
+
+def test_bounds_past_32_bits(dev):
+    """A window or a longest query that 32 bits do not hold limits nothing."""
+    c = make_case(111, [90, 300], [1, 1], 4, 2, 128, 16, F16)
+    d = to_dev(c, dev)
+    first = run_decode(c, d)
+    for window in (2 ** 31, 2 ** 32 + 5, 2 ** 63 - 1):
+        c.window = window
+        assert torch.equal(first, run_decode(c, d))
+    c.window, c.cap = 0, 1e-50
+    with pytest.raises(ValueError):
+        run_decode(c, d)
+    c = make_case(112, [90, 300], [90, 30], 4, 2, 128, 16, F16)
+    d = to_dev(c, dev)
+    first = run_prefill(c, d)
+    c.window = 2 ** 32 + 5
+    assert torch.equal(first, run_prefill(c, d))
+    c.window = 0
+    many = make_case(112, [1, 2] * 40, [1] * 80, 128, 64, 64, 16, F16)
+    for longest in (2 ** 32 + 5, 2 ** 33):     # more work items than there can be
+        with pytest.raises(pa.PaError):
+            run_prefill(many, to_dev(many, dev), max_query_len=longest)
+    assert pa.device_errors() == 0

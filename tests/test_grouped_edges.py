@@ -8,6 +8,7 @@ import re
 import pytest
 
 import paged_kv_cache_269_gb300 as pa
+from paged_kv_cache_269_gb300 import grouped
 from paged_kv_cache_269_gb300.grouped import AttnOpts
 
 
@@ -102,3 +103,22 @@ def test_scales_and_caps_that_fp32_cannot_hold_are_refused():
     assert refused(1e25, 1e-25) and refused(1e-20, 1e15)
     assert not refused(1e30, 0.0) and not refused(0.0, 50.0) and not refused(-0.1, 50.0)
     assert not refused(0.1, 1e-25) and not refused(0.1, 1e25) and not refused(1e-38, 0.0)
+
+
+def test_numbers_past_32_bits_are_not_cut():
+    """A bound that 32 bits do not hold bounds nothing; it does not become its low
+    32 bits.  A cap that fp32 would take for 0, which says none, is refused."""
+    top = 2 ** 31 - 1
+    for n in (0, 1, 1024, top):
+        assert grouped._bound(n, "window") == n
+    for n in (top + 1, 2 ** 32, 2 ** 32 + 5, 2 ** 63 - 1, 2 ** 80):
+        assert grouped._bound(n, "window") == top
+    for n in (-1, -2 ** 31 - 7, -2 ** 32):
+        assert grouped._bound(n, "window") == -1          # the library refuses it
+    assert grouped._bound(7.0, "window") == 7
+    with pytest.raises(ValueError):
+        grouped._bound(0.5, "window")
+    assert grouped._cap(None) == 0.0 and grouped._cap(0) == 0.0 and grouped._cap(30) == 30.0
+    assert grouped._cap(-2.0) == -2.0                      # the library refuses it
+    with pytest.raises(ValueError):
+        grouped._cap(1e-50)
