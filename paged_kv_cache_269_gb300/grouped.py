@@ -16,6 +16,9 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.util
+import threading
+import warnings
 
 torch = Tensor = _I32 = _F32 = _U8 = _raw_stream = _package = None
 _marshal = None        # the compiled marshalling module: one call per operator
@@ -23,33 +26,47 @@ _get_device = _capturing = None
 _addresses: dict = {}  # of the library's functions, for _marshal
 
 
+_init_lock = threading.Lock()
+
+
 def _init():
     """Imports what the calls need, at the first one (the package itself, with
-    its block manager, works without torch)."""
+    its block manager, works without torch).  _package is set last: a thread that
+    finds it finds the rest, and one that comes before waits."""
     global torch, Tensor, _I32, _F32, _U8, _raw_stream, _package, _marshal, _get_device, _capturing
-    import importlib.util
+    with _init_lock:
+        if _package is not None:
+            return
+        import torch as torch_
+        import paged_kv_cache_269_gb300 as package
+        torch, Tensor = torch_, torch_.Tensor
+        _I32, _F32, _U8 = torch.int32, torch.float32, torch.uint8
+        c = torch._C
+        if all(hasattr(c, n) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice",
+                                       "_cuda_isCurrentStreamCapturing")) and torch.cuda.is_available():
+            torch.cuda.init()
+            _raw_stream, _get_device = c._cuda_getCurrentRawStream, c._cuda_getDevice
+            _capturing = c._cuda_isCurrentStreamCapturing
+            l = package.lib()
+            for name in ("pa_rope_and_cache", "pa_decode_grouped", "pa_decode_grouped_workspace_bytes",
+                         "pa_decode_grouped_counters_bytes", "pa_prefill_grouped",
+                         "pa_prefill_grouped_workspace_bytes", "pa_prefill_grouped_counters_bytes"):
+                _addresses[name] = ctypes.cast(getattr(l, name), ctypes.c_void_p).value
+            try:
+                _marshal = _load_marshal(package._build.build_marshal())
+            except (RuntimeError, OSError, ImportError) as e:
+                # once: every call then takes the Python checks, slower by 9 us
+                warnings.warn(f"the grouped calls' marshalling module is missing, their arguments are checked "
+                              f"in Python: {e}", RuntimeWarning, stacklevel=4)
+        # (without CUDA the checks refuse every tensor)
+        _package = package
 
-    import torch as torch_
-    import paged_kv_cache_269_gb300 as package
-    torch, Tensor, _package = torch_, torch_.Tensor, package
-    _I32, _F32, _U8 = torch.int32, torch.float32, torch.uint8
-    c = torch._C
-    if not all(hasattr(c, n) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice",
-                                       "_cuda_isCurrentStreamCapturing")):
-        return             # a torch without CUDA: the checks refuse every tensor
-    if not torch.cuda.is_available():
-        return
-    torch.cuda.init()
-    _raw_stream, _get_device = c._cuda_getCurrentRawStream, c._cuda_getDevice
-    _capturing = c._cuda_isCurrentStreamCapturing
-    l = package.lib()
-    for name in ("pa_rope_and_cache", "pa_decode_grouped", "pa_decode_grouped_workspace_bytes",
-                 "pa_decode_grouped_counters_bytes", "pa_prefill_grouped",
-                 "pa_prefill_grouped_workspace_bytes", "pa_prefill_grouped_counters_bytes"):
-        _addresses[name] = ctypes.cast(getattr(l, name), ctypes.c_void_p).value
-    spec = importlib.util.spec_from_file_location("pa_marshal", package._build.build_marshal())
-    _marshal = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(_marshal)
+
+def _load_marshal(path):
+    spec = importlib.util.spec_from_file_location("pa_marshal", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
 
 
 class AttnOpts(ctypes.Structure):

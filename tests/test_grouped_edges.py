@@ -4,6 +4,8 @@ import ctypes
 import os
 import random
 import re
+import threading
+import warnings
 
 import pytest
 
@@ -122,3 +124,65 @@ def test_numbers_past_32_bits_are_not_cut():
     assert grouped._cap(-2.0) == -2.0                      # the library refuses it
     with pytest.raises(ValueError):
         grouped._cap(1e-50)
+
+
+@pytest.fixture
+def fresh_binding(monkeypatch):
+    """The binding as a process finds it before its first grouped call, on a machine
+    that says it has CUDA."""
+    torch = pytest.importorskip("torch")
+    for name in ("torch", "Tensor", "_I32", "_F32", "_U8", "_raw_stream", "_package", "_marshal", "_get_device",
+                 "_capturing"):
+        monkeypatch.setattr(grouped, name, None)
+    monkeypatch.setattr(grouped, "_buffers", {})
+    monkeypatch.setattr(torch.cuda, "is_available", lambda: True)
+    monkeypatch.setattr(torch.cuda, "init", lambda: None)
+    if not hasattr(torch._C, "_cuda_getCurrentRawStream"):
+        pytest.skip("a torch without CUDA")
+    return monkeypatch
+
+
+def test_a_marshalling_module_that_does_not_build_is_told_once(fresh_binding):
+    calls = []
+
+    def broken():
+        calls.append(1)
+        raise RuntimeError("no compiler")
+
+    fresh_binding.setattr(pa._build, "build_marshal", broken)
+    with pytest.warns(RuntimeWarning, match="no compiler"):
+        assert grouped._pa() is pa
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")
+        assert grouped._pa() is pa
+    assert calls == [1] and grouped._marshal is None and grouped._raw_stream is not None
+
+
+def test_a_second_thread_waits_for_the_first_call(fresh_binding):
+    building, go = threading.Event(), threading.Event()
+
+    def slow():
+        building.set()
+        assert go.wait(30)
+        return "path"
+
+    module = object()
+    fresh_binding.setattr(pa._build, "build_marshal", slow)
+    fresh_binding.setattr(grouped, "_load_marshal", lambda path: module)
+    found = []
+
+    def call():
+        package = grouped._pa()
+        found.append((package, grouped._raw_stream is not None, grouped._marshal))
+
+    threads = [threading.Thread(target=call) for _ in range(4)]
+    threads[0].start()
+    assert building.wait(30)
+    for t in threads[1:]:
+        t.start()
+    threads[1].join(0.2)
+    assert found == []
+    go.set()
+    for t in threads:
+        t.join(30)
+    assert found == [(pa, True, module)] * 4
