@@ -325,10 +325,18 @@ def _known_buffers(stream, counters, workspace):
 
 
 def reset_counters():
-    """Zero every cached counter buffer (needed after a device error)."""
-    with _pa()._buf_lock:
+    """Zero every cached counter buffer (needed after a device error), with no
+    call in flight on any of their streams."""
+    if _package is None:
+        return             # no call was made
+    with _package._buf_lock:
+        devices = {index for index, _ in _buffers}
+        for index in devices:
+            torch.cuda.synchronize(index)
         for got in _buffers.values():
             got[0].zero_()
+        for index in devices:
+            torch.cuda.synchronize(index)
 
 
 def _attention_args(what, out, q, k_cache, v_cache, block_tables, context_lens, softcap,

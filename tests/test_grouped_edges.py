@@ -186,3 +186,12 @@ def test_a_second_thread_waits_for_the_first_call(fresh_binding):
     for t in threads:
         t.join(30)
     assert found == [(pa, True, module)] * 4
+
+
+def test_resetting_workspaces_builds_nothing(fresh_binding):
+    def never():
+        raise AssertionError("built")
+
+    fresh_binding.setattr(pa._build, "build_marshal", never)
+    pa.reset_workspaces()
+    assert grouped._package is None
