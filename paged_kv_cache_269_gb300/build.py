@@ -88,7 +88,18 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
 
 
 MARSHAL_SRC = os.path.join(CSRC, "py", "pa_marshal.cpp")
-MARSHAL_PATH = os.path.join(LIB_DIR, "pa_marshal.so")
+
+
+def marshal_path() -> str:
+    """Where the marshalling module of this interpreter and torch lies.  It reads
+    their objects directly, so it is one file for each pair: times of files would
+    not tell an older torch from the one it was built against."""
+    import re
+    import sysconfig
+
+    import torch
+    tag = f"{sysconfig.get_config_var('SOABI')}-torch{torch.__version__}-abi{int(torch._C._GLIBCXX_USE_CXX11_ABI)}"
+    return os.path.join(LIB_DIR, f"pa_marshal.{re.sub('[^A-Za-z0-9_.+-]', '_', tag)}.so")
 
 
 def build_marshal(force: bool = False) -> str:
@@ -96,14 +107,14 @@ def build_marshal(force: bool = False) -> str:
     import sysconfig
 
     import torch
+    path = marshal_path()
     inputs = (MARSHAL_SRC, os.path.join(INCLUDE, "pa.h"), __file__, torch.__file__)
-    if not force and os.path.exists(MARSHAL_PATH) and all(
-            os.path.getmtime(p) <= os.path.getmtime(MARSHAL_PATH) for p in inputs):
-        return MARSHAL_PATH
+    if not force and os.path.exists(path) and all(os.path.getmtime(p) <= os.path.getmtime(path) for p in inputs):
+        return path
     os.makedirs(LIB_DIR, exist_ok=True)
     base = os.path.dirname(torch.__file__)
     inc = os.path.join(base, "include")
-    tmp = MARSHAL_PATH + f".tmp{os.getpid()}"
+    tmp = path + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", MARSHAL_SRC, "-o", tmp,
            "-I", INCLUDE, "-I", inc, "-I", os.path.join(inc, "torch", "csrc", "api", "include"),
            "-I", sysconfig.get_paths()["include"], "-L", os.path.join(base, "lib"), "-ltorch_python",
@@ -111,8 +122,8 @@ def build_marshal(force: bool = False) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {MARSHAL_SRC}:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, MARSHAL_PATH)
-    return MARSHAL_PATH
+    os.replace(tmp, path)
+    return path
 
 
 if __name__ == "__main__":

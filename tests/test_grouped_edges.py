@@ -4,6 +4,7 @@ import ctypes
 import os
 import random
 import re
+import sysconfig
 import threading
 import warnings
 
@@ -195,3 +196,14 @@ def test_resetting_workspaces_builds_nothing(fresh_binding):
     fresh_binding.setattr(pa._build, "build_marshal", never)
     pa.reset_workspaces()
     assert grouped._package is None
+
+
+def test_the_marshalling_module_belongs_to_one_torch_and_python(monkeypatch):
+    torch = pytest.importorskip("torch")
+    path = pa._build.marshal_path()
+    assert os.path.dirname(path) == pa._build.LIB_DIR and path.endswith(".so")
+    monkeypatch.setattr(torch, "__version__", "0.0+other")
+    other = pa._build.marshal_path()
+    assert other != path
+    monkeypatch.setattr(sysconfig, "get_config_var", lambda name: "cpython-00")
+    assert pa._build.marshal_path() not in (path, other)
