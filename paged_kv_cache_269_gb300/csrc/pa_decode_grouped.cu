@@ -75,7 +75,10 @@ constexpr int kW = 4;                  // warps per CTA
 constexpr int kThreads = kW * 32;
 constexpr int kChunks = 512;           // entries of the CTA's prefix over the sequences
 constexpr int kMaxCtas = 640;          // bounds the partial slots (2 per CTA)
-constexpr float kRaise = 8.f;
+// The reference is raised by scores more than this above it.  The sum is rounded
+// down: past 2^26 fp32's step is 8 and the bias below becomes 8 too, so a score one
+// step above the reference would have a weight of 2^16, past fp16.
+constexpr float kRaise = 7.9f;
 constexpr float kBias = 6.f;           // weights are 2^(x - m + 6)
 
 struct DecodeGroupedArgs {
@@ -712,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (a.alibi_slopes) x -= slope[nt][e & 1] * static_cast<float>(g.ctx - 1 - key);
                         if (partial) x = visible(k0, key - k0, have) ? x : -INFINITY;
                         sc[mt][nt][e] = x;
-                        raise |= x > m[nt][e & 1] + kRaise;
+                        raise |= x > __fadd_rd(m[nt][e & 1], kRaise);
                     }
             if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
@@ -726,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int d = 4; d < 32; d *= 2)
                             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-                        if (x > m[nt][e] + kRaise) {
+                        if (x > __fadd_rd(m[nt][e], kRaise)) {
                             const float r = m[nt][e] == -INFINITY ? 0.f : fast_exp2(m[nt][e] - x);
                             m[nt][e] = x;
                             l[nt][e] *= r;

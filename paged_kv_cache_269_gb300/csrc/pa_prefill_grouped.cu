@@ -105,7 +105,10 @@ constexpr int kPvWarp0 = 11;
 // MMA warps give registers up to the softmax warps: 2 x 168 + 2 x 88 = 4 x 128.
 constexpr int kRegsSoftmax = 168, kRegsOther = 88;
 constexpr uint32_t kTmemCols = 512;
-constexpr float kRaise = 8.f;          // where a maximum is taken, it is kept if it is this near
+// Where a maximum is taken, the reference is kept if it is this near.  The sum is
+// rounded down: past 2^26 fp32's step is 8 and the bias below may become 8, so a
+// score one step above the reference would have a weight of 2^16, past fp16.
+constexpr float kRaise = 7.9f;
 // Weights are 2^(x - m + bias).  fp16 holds at most 2^16: a row sum of up to
 // 2^15 proves every weight fits; bf16 has the exponent range of fp32, and its
 // reference hardly ever has to be raised.
@@ -854,7 +857,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int q = 0; q < 8; ++q) mx[q] = fmaxf(mx[q], x[e + q]);
                     const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
                                             fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
-                    const bool raise = top > m + kRaise;
+                    const bool raise = top > __fadd_rd(m, kRaise);
                     if (__any_sync(0xffffffffu, raise && live)) {
                         const float m_new = raise ? top : m;
                         const float alpha = m == m_new ? 1.f : fast_exp2(m - m_new);

@@ -250,3 +250,35 @@ def test_bounds_past_32_bits(dev):
         with pytest.raises(pa.PaError):
             run_prefill(many, to_dev(many, dev), max_query_len=longest)
     assert pa.device_errors() == 0
+
+
+# ------------------------------------------------------------------ large numbers
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("base", [2.0, 2.5])
+def test_scores_of_a_large_step(dev, dtype, D, base):
+    """Scores near 2^26, where fp32 counts in steps of 8: keys a step apart, the larger
+    ones last, give a finite softmax of them (the weights' ratio is 2^-8)."""
+    c = make_case(113, [200, 100], [1, 1], 8, 2, D, 16, dtype, scale=0.6931471805599453)
+    big = 4096.0 * 2 if dtype == F16 else 8192.0
+    for s, n in enumerate(c.ctx):
+        for j in range(n):
+            k = c.k_cache[int(c.tables[s, j // 16]), :, j % 16]
+            k[:] = 0.0
+            k[:, 0] = big * base / 2
+            k[:, 1] = 1.0 if j < 64 else 2.0
+    c.q[:] = 0.0
+    c.q[:, :, 0], c.q[:, :, 1] = big, 8.0            # scores of 2^26 base / 2 + 8 or 16, in log2 units
+    for run in (run_decode, run_prefill):
+        got = run(c, to_dev(c, dev)).cpu().double()
+        assert torch.isfinite(got).all()
+        for s, n in enumerate(c.ctx):
+            V = torch.stack([c.v_cache[int(c.tables[s, j // 16]), :, j % 16].double() for j in range(n)])   # [n, H, D]
+            w = torch.where(torch.arange(n) < 64, 2.0 ** -8, 1.0).double()
+            want = torch.einsum("n,nhd->hd", w / w.sum(), V).repeat_interleave(4, 0)
+            # a score that is off by a step moves the early keys' part of the output,
+            # at most 64 / n of the weights, between two means of the same values
+            share = 2.0 * 64 / n * V.abs().amax()
+            assert ((got[s] - want).abs() <= share + U[dtype] * V.abs().amax()).all()
+    assert pa.device_errors() == 0
