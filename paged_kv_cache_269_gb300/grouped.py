@@ -510,7 +510,8 @@ def prefill_grouped(out, q, k_cache, v_cache, block_tables, context_lens, query_
                                    scale, max_query_len, softcap, alibi_slopes, window, prefix_lens,
                                    workspace, counters, stream)
     if max_query_len is None:
-        max_query_len = int((query_start[1:] - query_start[:-1]).max()) if S else 0
+        with torch.cuda.stream(stream):      # the one that query_start is ready on
+            max_query_len = int((query_start[1:] - query_start[:-1]).max()) if S else 0
     max_query_len = _bound(max_query_len, "max_query_len")
     need_ws, need_ctr = _prefill_needs(S, Hq, *sizes, max_query_len)
     if need_ws == pa._SIZE_ERROR or need_ctr == 0:

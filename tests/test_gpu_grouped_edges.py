@@ -282,3 +282,79 @@ def test_scores_of_a_large_step(dev, dtype, D, base):
             share = 2.0 * 64 / n * V.abs().amax()
             assert ((got[s] - want).abs() <= share + U[dtype] * V.abs().amax()).all()
     assert pa.device_errors() == 0
+
+
+# ------------------------------------------------------------------ streams
+
+def test_calls_on_a_given_stream(dev):
+    """stream= orders the whole call, the search for the longest query among it, and
+    has buffers of its own, in a capture too."""
+    side = torch.cuda.Stream(dev)
+    c = make_case(114, [700, 90, 3000], [64, 90, 5], 8, 2, 128, 16, F16)
+    d = to_dev(c, dev)
+    want = run_prefill(c, d)
+    starts = d["starts"].clone()
+    busy = torch.randn(4096, 4096, device=dev)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        late = torch.zeros_like(starts)
+        out = torch.zeros_like(d["q"])
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            for _ in range(40):
+                busy @ busy
+            late.copy_(starts)
+        run_prefill(c, dict(d, starts=late), out, max_query_len=None, stream=side)
+        side.synchronize()
+        assert torch.equal(want, out)
+    e = make_case(115, [700, 3000, 9], [1] * 3, 8, 2, 128, 16, BF16)
+    de = to_dev(e, dev)
+    want = run_decode(e, de)
+    torch.cuda.synchronize()
+    out = torch.zeros_like(want)
+    run_decode(e, de, out, stream=side)
+    side.synchronize()
+    assert torch.equal(want, out)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        run_decode(e, de, out, stream=side)
+        run_decode(e, de, out, stream=side)
+    for _ in range(3):
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(want, out)
+    assert pa.device_errors() == 0
+
+
+# ------------------------------------------------------------------ batches
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("D,group,kw", [(128, 4, {}), (64, 3, dict(alibi=True)), (128, 8, dict(window=200, cap=30.0))])
+def test_prefill_a_chunk_beside_single_tokens(dev, dtype, D, group, kw):
+    """A prompt's chunk and the next tokens of running sequences in one call: most
+    work items of the call are empty."""
+    ctx = [1500] + [17 + 41 * s % 700 for s in range(63)]
+    c = make_case(116, ctx, [600] + [1] * 63, 2 * group, 2, D, 16, dtype, **kw)
+    got = run_prefill(c, to_dev(c, dev))
+    assert pa.device_errors() == 0
+    check(c, got, True)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_unseen_keys_and_values_stay_out(dev, dtype, D):
+    """NaN and infinities in keys and values behind a decode's window, and in keys
+    behind a prompt's, with the bound of grouped_ref."""
+    ctx = [300, 77, 40]
+    for run, new, weights16 in ((run_decode, [1, 1, 1], False), (run_prefill, [60, 5, 40], True)):
+        if run is run_prefill and D == 256:
+            continue
+        c = make_case(117, ctx, new, 8, 2, D, 16, dtype, window=33)
+        unseen = _unseen_keys(c)[:, None, :, None]
+        c.k_cache = torch.where(unseen, torch.full_like(c.k_cache, float("inf")), c.k_cache)
+        if run is run_decode:
+            c.v_cache = torch.where(unseen, torch.full_like(c.v_cache, float("nan")), c.v_cache)
+        got = run(c, to_dev(c, dev))
+        assert pa.device_errors() == 0
+        check(c, got, weights16)
