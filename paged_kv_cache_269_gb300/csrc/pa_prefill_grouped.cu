@@ -131,7 +131,6 @@ struct PrefillGroupedArgs {
     float scale_log2, cap_log2, cap_in;
     float cap_v;                       // v = cap_v (q . k) has v^2 < 2 iff |s / cap| < 0.75
     float tanh_k[5];                   // there, x = v (k0 + k1 v^2 + ... + k4 v^8)
-    int cap_share;                     // the first form may take scores in either way
     int group, tpt;                    // heads per K/V head; tokens per tile
     int num_pairs, splits;
     int store_boxes;                   // a warp's 32 rows are whole tokens: tm_out applies
@@ -728,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // visible key is ahead of the row).
                 bool done_fast = false;
                 const bool fast = (!kAlibi || pre_all <= k0 || k0 + kBN - 1 <= wmin) && warp_all(m != -INFINITY) &&
-                                  (!kCap || p.cap_share);
+                                  (!kCap || a.softcap <= kShareCap<kBf16>);
                 uint32_t any = 0;
                 auto weights = [&](auto masked) {
                     uint32_t vis[kBN / 32];
@@ -1138,7 +1137,6 @@ cudaError_t launch_prefill_grouped(const GroupedArgs &args, int dtype, int head_
     p.cap_in = args.softcap > 0.f ? static_cast<float>(2.0 * args.scale / args.softcap * log2e) : 0.f;
     p.group = Hq / Hk;
     fill_tanh(args.scale, args.softcap, &p.cap_v, p.tanh_k);
-    p.cap_share = args.softcap <= (bf16 ? kShareCap<true> : kShareCap<false>);
     p.tpt = kBM / p.group;
     const Plan pl = make_plan(args.num_seqs, Hk, p.group, args.max_q);
     const long long items = pl.base * pl.splits;   // fits an int (the caller checks), with room past the end
