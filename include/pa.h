@@ -551,6 +551,8 @@ size_t pa_decode_grouped_counters_bytes(const pa_dims *dims, int32_t num_q_heads
  *
  * Scores, softmax and sums are fp32; the weights are rounded to the element
  * type once before the P V product (pa_prefill carries a second 16-bit term).
+ * bf16 values past 2^50 may overflow the sums: a weight may stand as much as 2^60
+ * above the reference that it is taken against.
  * An output element is then off by at most u (|o| + sum_j p_j |v_j|) plus the
  * fp32 terms, u = 2^-11 for fp16 and 2^-8 for bf16; over a tensor the error is
  * about 1.4 times that of rounding the exact result.

@@ -7,9 +7,10 @@
 // over the keys with a running reference m_g that every weight and the sum
 // share, so the result does not depend on it.
 //
-// What bounds it: each K and V element is used G times (2 G flops per
-// element read), so the call is bound by HBM as long as the products are
-// cheaper than the loads.  On the FMA pipe they are not from G = 4 on, so both
+// What bounds it: each K and V element is read once for up to 16 query heads (8
+// at head_dim 256; wider groups are taken in chunks, and each chunk reads the
+// context again), 2 flops for each of them, so the call is bound by HBM as long
+// as the products are cheaper than the loads.  On the FMA pipe they are not from G = 4 on, so both
 // products run as mma.sync m16n8k16 with the 16 rows on the keys (then the
 // head dims) and the 8 columns on the query heads: a group of 8 heads fills
 // the shape, where tcgen05's 128-row tiles would be 1/16 used.
@@ -35,13 +36,13 @@
 //    bf16), so the output is as exact as fp32 weights make it.  With G <= 4
 //    the two halves share one product: columns 4-7 repeat the heads and carry
 //    P_lo.
-//  * The reference m is raised only when a score exceeds it by more than 8
+//  * The reference m is raised only when a score exceeds it by about 8
 //    (weights stay below 2^(8 + 6), inside fp16), so most tiles need no
 //    maximum across lanes and no rescaling.
 //  * Keys that are not visible get weight 0 and their V values are cleared in
 //    registers, so nothing they hold reaches the output.
 //
-// Shape: 4 warps a CTA and 2 CTAs an SM, as many as 189 registers a thread
+// Shape: 4 warps a CTA and 2 CTAs an SM, as many as 181 to 251 registers a thread
 // leave, with as many stages a warp as shared memory holds.  A third stage at
 // head_dim 128 (in exchange for a smaller merge area) cost 4 % (59.5 us against
 // 57.1 on the first batch below), at 256 nothing changed.  Work cut into small
@@ -49,13 +50,14 @@
 // partials to join are many.
 //
 // Measured: 64 sequences of 256 to 2048 tokens, 32 heads on 8 of 128, bf16:
-// 56 us, 5.4 TB/s; 256 sequences of 1000 to 4000 tokens 380 us, 6.8 TB/s,
+// 57 us, 5.3 TB/s; 256 sequences of 1000 to 4000 tokens 386 us, 6.8 TB/s,
 // the rate of a copy.  4 documents of 20001 to 32768 tokens, 64 heads on 8,
-// distance bias: 73 us, 5.7 TB/s (HBM busy, the tensor pipe 12 %).  96
-// sequences, window 1024, head_dim 256, capped: 136 us, 5.9 TB/s.  What is not
-// streaming is 5 to 7 us until all rings are full (lengths, table entry, first
-// tiles, one after another) and about 8 us at the end (merge, ticket, join); a
-// sequence of 1000 tokens is nothing else, and takes 8.5 us.
+// distance bias: 74 us, 5.6 TB/s (HBM busy, the tensor pipe 12 %).  96
+// sequences, window 1024, head_dim 256, capped: 134 us, 6.0 TB/s.  What is not
+// streaming is the start until all rings are full (lengths, table entry, first
+// tiles, one after another) and the end (merge, ticket, join), about 12 us of
+// such calls together; a sequence of 1000 tokens is nothing else, and takes
+// 8.6 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>

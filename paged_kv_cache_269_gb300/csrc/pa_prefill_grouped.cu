@@ -5,20 +5,22 @@
 // key j, x_j = log2(e) f(scale q . k_j) with f the optional tanh cap and
 // distance bias, and o = sum_j 2^(x_j - m) v_j / sum_j 2^(x_j - m) over the
 // visible keys, in one pass over tiles of keys with a reference m that is only
-// raised when a tile's maximum exceeds it by more than 8 (a common factor of
+// raised when a tile's maximum exceeds it by about 8 (a common factor of
 // weights and sum cancels, so m need not be the maximum).
 //
 // What bounds it: 4 D flops per (row, key) pair on the tensor cores; beside
 // them the softmax warps spend an ex2 a pair on the special-function unit, and
 // with the cap a polynomial of 7 products on the FMA pipe.
 //
-// Measured (32 heads on 4, one prompt of 8192 tokens, bf16): head_dim 128 333 us,
-// 1650 TFLOP/s, 0.86 of this GPU's largest library product, the products bound;
-// with distance biases 358 us; with the cap 503 us, 1093 TFLOP/s, the softmax
-// warps bound (FMA pipe, and two warps a scheduler to hide latencies); head_dim
-// 64 324 us, 847 TFLOP/s, the softmax again, with half the products a pair.  16
-// prompts of 333 to 1024 tokens, 32 heads on 8: 79 us, 840 TFLOP/s: the first
-// key tile of an item and its output cost as much as several tiles.
+// Measured (32 heads on 4, one prompt of 8192 tokens, bf16): head_dim 128 330 us,
+// 1660 TFLOP/s, 0.87 of this GPU's largest library product, the products bound;
+// with distance biases 362 us; with the cap 503 us, 1093 TFLOP/s, the latency of
+// the softmax warps' longer chains, two warps a scheduler (no pipe is busier than
+// 46 %: tensor 46, FMA 45, special functions 39; an instruction in 0.58 of the
+// cycles); head_dim 64 327 us, 841 TFLOP/s, the softmax again, with half the
+// products a pair.  16 prompts of 333 to 1024 tokens, 32 heads on 8: 79 us, 840
+// TFLOP/s (118 capped): the first key tile of an item and its output cost as much
+// as several tiles.
 //
 // How (persistent, one CTA per SM, 512 threads):
 //  * A tile is 128 rows of (token, head) pairs: 128 / G tokens x the G heads of

@@ -16,8 +16,9 @@
 // Launched with programmatic dependent launch, like reshape_and_cache: it
 // waits for the previous kernel on the stream before it touches memory.
 //
-// Measured, bf16, 32 + 8 + 8 heads of 128: 16384 tokens 63.5 us, 6.5 TB/s of
-// its 411 MB, 0.95 of this GPU's copy rate; 256 tokens 3.1 us and one token
+// Measured, bf16, 32 + 8 + 8 heads of 128: 16384 tokens 63.3 us, 6.5 TB/s of
+// its 411 MB, 0.96 of this GPU's copy rate; 256 tokens 3.8 us, a launch and two
+// round trips to HBM (positions and slots, then the rows and the table); one token
 // 1.8 us, which is what a launch costs.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
