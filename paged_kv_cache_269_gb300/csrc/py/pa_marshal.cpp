@@ -21,6 +21,7 @@ struct Args {
     PyObject *const *a;
     int device;
     bool ok = true;
+    void *pointer(int i) const { return THPVariable_Unpack(a[i]).data_ptr(); }
     const Tensor *tensor(int i) {
         if (!THPVariable_Check(a[i])) {
             ok = false;
@@ -129,13 +130,18 @@ PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
     void *stream = pointer(a[11]);
     auto fn = reinterpret_cast<decltype(&pa_rope_and_cache)>(pointer(a[12]));
     if (PyErr_Occurred() || turn < 0 || !fn) return take_over();
+    // every pointer before the interpreter is let go: asking for one may throw
+    void *const kp = g.pointer(4), *const vp = g.pointer(5);
+    void *const op = o->data_ptr();
+    const void *const qp = q->data_ptr(), *const k_new = k->data_ptr(), *const v_new = v->data_ptr();
+    const auto *positions = static_cast<const int32_t *>(pos->data_ptr());
+    const auto *table = static_cast<const float *>(cs->data_ptr());
+    const auto *slot = static_cast<const int32_t *>(slots->data_ptr());
+    const int32_t rotary = static_cast<int32_t>(cs->size(1)), most = static_cast<int32_t>(cs->size(0));
     int rc;
     Py_BEGIN_ALLOW_THREADS;
-    rc = fn(o->data_ptr(), q->data_ptr(), k->data_ptr(), v->data_ptr(),
-            THPVariable_Unpack(a[4]).data_ptr(), THPVariable_Unpack(a[5]).data_ptr(),
-            static_cast<const int32_t *>(pos->data_ptr()), static_cast<const float *>(cs->data_ptr()),
-            static_cast<const int32_t *>(slots->data_ptr()), static_cast<int32_t>(T), static_cast<int32_t>(Hq), qs,
-            ks, vs, os, static_cast<int32_t>(cs->size(1)), static_cast<int32_t>(cs->size(0)), turn, &d, stream);
+    rc = fn(op, qp, k_new, v_new, kp, vp, positions, table, slot, static_cast<int32_t>(T), static_cast<int32_t>(Hq), qs,
+            ks, vs, os, rotary, most, turn, &d, stream);
     Py_END_ALLOW_THREADS;
     return PyLong_FromLong(rc);
 }
@@ -149,6 +155,11 @@ struct Attention {
     int64_t S, Hq, MB;
     float scale;
     void *stream;
+    // their pointers: taken before the interpreter is let go, for asking may throw
+    void *out_p, *k_p, *v_p, *workspace_p;
+    const void *q_p;
+    const int32_t *tables_p, *lens_p;
+    uint32_t *counters_p;
 };
 // args: out, q, k_cache, v_cache, tables, lens, scale, softcap, slopes, window,
 // prefix, counters, workspace, device, stream
@@ -190,7 +201,16 @@ bool attention(Args &g, Attention *x) {
     x->counters = g.plain(11, at::kInt, 1);
     x->workspace = g.ok ? g.plain(12, at::kByte, 1) : nullptr;
     x->stream = pointer(a[14]);
-    return g.ok && !PyErr_Occurred();
+    if (!g.ok || PyErr_Occurred()) return false;
+    x->out_p = x->out->data_ptr();
+    x->q_p = x->q->data_ptr();
+    x->k_p = g.pointer(2);
+    x->v_p = g.pointer(3);
+    x->tables_p = static_cast<const int32_t *>(x->tables->data_ptr());
+    x->lens_p = static_cast<const int32_t *>(x->lens->data_ptr());
+    x->counters_p = static_cast<uint32_t *>(x->counters->data_ptr());
+    x->workspace_p = x->workspace->data_ptr();
+    return true;
 }
 
 // decode(<attention's 15>, fn, workspace_fn, counters_fn) -> status or None
@@ -207,10 +227,8 @@ PyObject *decode(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (need_ct == 0 || have_ct < need_ct || have_ws < ws(&x.d, Hq)) return take_over();
     int rc;
     Py_BEGIN_ALLOW_THREADS;
-    rc = fn(x.out->data_ptr(), x.q->data_ptr(), THPVariable_Unpack(a[2]).data_ptr(),
-            THPVariable_Unpack(a[3]).data_ptr(), static_cast<const int32_t *>(x.tables->data_ptr()),
-            static_cast<const int32_t *>(x.lens->data_ptr()), x.scale, static_cast<int32_t>(x.MB), &x.d, Hq, &x.opts,
-            x.workspace->data_ptr(), have_ws, static_cast<uint32_t *>(x.counters->data_ptr()), have_ct, x.stream);
+    rc = fn(x.out_p, x.q_p, x.k_p, x.v_p, x.tables_p, x.lens_p, x.scale, static_cast<int32_t>(x.MB), &x.d, Hq, &x.opts,
+            x.workspace_p, have_ws, x.counters_p, have_ct, x.stream);
     Py_END_ALLOW_THREADS;
     return PyLong_FromLong(rc);
 }
@@ -234,14 +252,12 @@ PyObject *prefill(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const int32_t Hq = static_cast<int32_t>(x.Hq);
     const size_t need_ct = ct(&x.d, Hq), have_ct = x.counters->numel() * 4, have_ws = x.workspace->numel();
     if (need_ct == 0 || have_ct < need_ct || have_ws < ws(&x.d, Hq, static_cast<int32_t>(most))) return take_over();
+    const auto *starts_p = static_cast<const int32_t *>(starts->data_ptr());
     int rc;
     Py_BEGIN_ALLOW_THREADS;
-    rc = fn(x.out->data_ptr(), x.q->data_ptr(), THPVariable_Unpack(a[2]).data_ptr(),
-            THPVariable_Unpack(a[3]).data_ptr(), static_cast<const int32_t *>(x.tables->data_ptr()),
-            static_cast<const int32_t *>(x.lens->data_ptr()), static_cast<const int32_t *>(starts->data_ptr()),
-            static_cast<int32_t>(total), static_cast<int32_t>(most), x.scale, static_cast<int32_t>(x.MB), &x.d, Hq,
-            &x.opts, x.workspace->data_ptr(), have_ws, static_cast<uint32_t *>(x.counters->data_ptr()), have_ct,
-            x.stream);
+    rc = fn(x.out_p, x.q_p, x.k_p, x.v_p, x.tables_p, x.lens_p, starts_p, static_cast<int32_t>(total),
+            static_cast<int32_t>(most), x.scale, static_cast<int32_t>(x.MB), &x.d, Hq, &x.opts, x.workspace_p, have_ws,
+            x.counters_p, have_ct, x.stream);
     Py_END_ALLOW_THREADS;
     return PyLong_FromLong(rc);
 }

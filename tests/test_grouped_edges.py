@@ -4,6 +4,8 @@ import ctypes
 import os
 import random
 import re
+import subprocess
+import sys
 import sysconfig
 import threading
 import warnings
@@ -207,3 +209,50 @@ def test_the_marshalling_module_belongs_to_one_torch_and_python(monkeypatch):
     assert other != path
     monkeypatch.setattr(sysconfig, "get_config_var", lambda name: "cpython-00")
     assert pa._build.marshal_path() not in (path, other)
+
+
+_WITHOUT_STORAGE = """
+import ctypes, sys
+import torch
+import paged_kv_cache_269_gb300 as pa
+from paged_kv_cache_269_gb300 import grouped
+
+class Held(torch.Tensor):            # says that it is a CUDA tensor, holds nothing
+    @staticmethod
+    def __new__(cls, dtype, *size):
+        return torch.Tensor._make_wrapper_subclass(cls, size, dtype=dtype, device="cuda:0")
+    @classmethod
+    def __torch_dispatch__(cls, func, types, args=(), kwargs=None):
+        raise NotImplementedError(func)
+
+module, lib = grouped._load_marshal(pa._build.build_marshal()), pa.lib()
+def at(name):
+    return ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
+half, whole = torch.float16, torch.int32
+shapes = [(half, 2, 4, 128), (half, 2, 4, 128), (half, 2, 2, 128), (half, 2, 2, 128), (half, 8, 2, 16, 128),
+          (half, 8, 2, 16, 128), (whole, 2, 4), (whole, 2), (whole, 3), (whole, 4096), (torch.uint8, 1 << 24),
+          (torch.float32, 9, 128)]
+found = []
+def calls(out, q, k, v, kc, vc, tables, lens, starts, counters, workspace, table):
+    common = (out, q, kc, vc, tables, lens, 0.1, 0.0, None, 0, None, counters, workspace, 0, 0)
+    found.append(module.decode(*common, at("pa_decode_grouped"), at("pa_decode_grouped_workspace_bytes"),
+                               at("pa_decode_grouped_counters_bytes")))
+    found.append(module.prefill(*common, starts, 1, at("pa_prefill_grouped"), at("pa_prefill_grouped_workspace_bytes"),
+                                at("pa_prefill_grouped_counters_bytes")))
+    found.append(module.rope(out, q, k, v, kc, vc, lens, table, lens, False, 0, 0, at("pa_rope_and_cache")))
+    raise StopIteration
+try:
+    torch.vmap(calls)(*[Held(s[0], 1, *s[1:]) for s in shapes])
+except StopIteration:
+    pass
+assert found == [None] * 3, found
+"""
+
+
+def test_marshalled_calls_hand_back_tensors_without_storage():
+    """A batched tensor of vmap has no address to give, and asking for one throws:
+    the call goes to the Python checks, the interpreter stays alive."""
+    pytest.importorskip("torch")
+    r = subprocess.run([sys.executable, "-c", _WITHOUT_STORAGE], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(pa.__file__)))
+    assert r.returncode == 0, r.stderr[-2000:]
