@@ -10,10 +10,10 @@
 // What bounds it: each K and V element is read once for up to 16 query heads (8
 // at head_dim 256; wider groups are taken in chunks, and each chunk reads the
 // context again), 2 flops for each of them, so the call is bound by HBM as long
-// as the products are cheaper than the loads.  On the FMA pipe they are not from G = 4 on, so both
-// products run as mma.sync m16n8k16 with the 16 rows on the keys (then the
-// head dims) and the 8 columns on the query heads: a group of 8 heads fills
-// the shape, where tcgen05's 128-row tiles would be 1/16 used.
+// as the products are cheaper than the loads.  On the FMA pipe they are not from
+// G = 4 on, so both products run as mma.sync m16n8k16 with the 16 rows on the
+// keys (then the head dims) and the 8 columns on the query heads: a group of 8
+// heads fills the shape, where tcgen05's 128-row tiles would be 1/16 used.
 //
 // How:
 //  * Work is cut evenly, not by sequence: all sequences' visible key tiles,
