@@ -572,6 +572,99 @@ size_t pa_prefill_grouped_workspace_bytes(const pa_dims *dims, int32_t num_q_hea
 size_t pa_prefill_grouped_counters_bytes(const pa_dims *dims, int32_t num_q_heads);
 
 /*
+ * The 8-bit cache.  Caches [N, H, B, D] of e4m3 numbers (a byte each: a sign, 4
+ * exponent bits, 3 mantissa bits, the largest 448, no infinity; the layout of the
+ * 16-bit caches in half the bytes), and two fp32 arrays of H scales, one for K
+ * and one for V: the value of element (blk, h, t, d) is its number times
+ * scales[h].  A number holds 4 significant bits over [2^-6, 448] and steps of
+ * 2^-9 below, so scales[h] = (largest |value| of head h) / 448 leaves values a
+ * step of at most 1/16 of themselves down to 2^-15 of the largest.  The scales
+ * are set before the first token is stored and kept as long as the cache: a
+ * stored number means nothing under another scale.  They must be positive and
+ * in [2^-60, 2^60]; the calls do not look (results are unspecified otherwise).
+ * dims->dtype is the type of q, k, v and of the outputs.
+ */
+
+/* What pa_norm_rope_and_cache does beside the rotation.  NULL, or one of all
+ * zeros: nothing, and a 16-bit cache. */
+typedef struct pa_append_opts {
+    const float *q_weight;   /* device, fp32 [D]: norm the heads of q; NULL: do not */
+    const float *k_weight;   /* device, fp32 [D]: norm the heads of k; NULL: do not */
+    float eps;               /* finite and >= 0                                     */
+    const float *k_scales;   /* device, fp32 [H]: the caches are e4m3; both or none */
+    const float *v_scales;
+} pa_append_opts;
+
+/*
+ * pa_norm_rope_and_cache -- pa_rope_and_cache with a norm of each head of q and k
+ * before the rotation, and into a cache of 16 or of 8 bits.
+ *
+ * For each head row x of q (with q_weight) and k (with k_weight):
+ *   x_i = x_i / sqrt(mean_j x_j^2 + eps) * weight_i        over all D dims,
+ * then the rotation, then one rounding: q, and k and v in a 16-bit cache, to the
+ * element type; in an 8-bit cache to e4m3 of x / scales[h], to nearest even,
+ * values past 448 at 448 (infinities too; NaN stays).  The arithmetic is fp32: a
+ * row whose sum of squares is past fp32 comes out 0.  v is not normed.
+ *
+ * The arguments are those of pa_rope_and_cache, with these additions:
+ *   num_q_heads  may be 0: q and q_out are not read and may be NULL
+ *   rotary_dim   may be 0: no rotation; cos_sin is not read and may be NULL
+ *   positions    may be NULL where rotary_dim is 0: no token is padding
+ *   k_cache, v_cache   e4m3 where opts has scales
+ *   opts         host, or NULL
+ * PA_ERR_SHAPE if eps is negative or not finite; PA_ERR_NULL if one of k_scales
+ * and v_scales is missing.
+ */
+int pa_norm_rope_and_cache(void *q_out, const void *q, const void *k, const void *v, void *k_cache,
+                           void *v_cache, const int32_t *positions, const float *cos_sin,
+                           const int32_t *slot_mapping, int32_t num_tokens, int32_t num_q_heads,
+                           int64_t q_stride, int64_t k_stride, int64_t v_stride, int64_t q_out_stride,
+                           int32_t rotary_dim, int32_t max_positions, int32_t interleaved,
+                           const pa_dims *dims, const pa_append_opts *opts, void *stream);
+
+/*
+ * pa_gather_cache_q8 -- tokens of an 8-bit cache read back as 16-bit rows.
+ *
+ *   k_out, v_out  device, [num_tokens, H, D] of dims->dtype (written)
+ *   k_cache, v_cache, k_scales, v_scales   device: the 8-bit cache
+ *   slots         device, int32 [num_tokens]: the slot of each row, in any order,
+ *                 the same one any number of times.  slot < 0 leaves the row as it
+ *                 is; slot >= N * B does too, and flags PA_DEVERR_SLOT
+ *
+ * out[i, h, :] = number * scales[h], in fp32 and rounded once to the type (fp16: an
+ * infinity past 65504).  The outputs must not overlap the inputs or each other.
+ */
+int pa_gather_cache_q8(void *k_out, void *v_out, const void *k_cache, const void *v_cache,
+                       const float *k_scales, const float *v_scales, const int32_t *slots,
+                       int32_t num_tokens, const pa_dims *dims, void *stream);
+
+/*
+ * pa_decode_grouped_q8, pa_prefill_grouped_q8 -- pa_decode_grouped and
+ * pa_prefill_grouped over an 8-bit cache; k_scales, v_scales: device, fp32 [H].
+ * The rest is theirs: the arguments, the options, the workspace and counters
+ * (sized by the same functions), what is refused and what is flagged.
+ *
+ * The numbers are widened exactly on the way to the products, scores are fp32 and
+ * get k_scales[h], outputs v_scales[h], in fp32.  In the decode both products run
+ * on fp16 operands whatever the type of q: a bf16 query row is first scaled by a
+ * power of two that brings its largest element to [2^10, 2^11), which moves no
+ * element down to 2^-27 of the largest and lower ones by at most 2^-35 of it.
+ */
+int pa_decode_grouped_q8(void *out, const void *q, const void *k_cache, const void *v_cache,
+                         const float *k_scales, const float *v_scales, const int32_t *block_tables,
+                         const int32_t *context_lens, float scale, int32_t max_blocks_per_seq,
+                         const pa_dims *dims, int32_t num_q_heads, const pa_attn_opts *opts,
+                         void *workspace, size_t workspace_bytes, uint32_t *counters,
+                         size_t counters_bytes, void *stream);
+int pa_prefill_grouped_q8(void *out, const void *q, const void *k_cache, const void *v_cache,
+                          const float *k_scales, const float *v_scales, const int32_t *block_tables,
+                          const int32_t *context_lens, const int32_t *query_start,
+                          int32_t total_query_tokens, int32_t max_query_len, float scale,
+                          int32_t max_blocks_per_seq, const pa_dims *dims, int32_t num_q_heads,
+                          const pa_attn_opts *opts, void *workspace, size_t workspace_bytes,
+                          uint32_t *counters, size_t counters_bytes, void *stream);
+
+/*
  * KV block manager (host only; no CUDA call).
  *
  * The bookkeeping half of the paged cache: blocks are handed out one at a

@@ -16,6 +16,8 @@ Functions (names follow the C ABI):
   rope_and_cache(q_out, q, k, v, k_cache, v_cache, positions, cos_sin, slot_mapping, ...)
   decode_grouped(out, q, k_cache, v_cache, block_tables, context_lens, scale, ...)
   prefill_grouped(out, q, k_cache, v_cache, block_tables, context_lens, query_start, scale, ...)
+  norm_rope_and_cache(q_out, q, k, v, k_cache, v_cache, positions, cos_sin, slot_mapping, ...)
+  reshape_and_cache_q8, gather_cache_q8, decode_grouped_q8, prefill_grouped_q8: an 8-bit cache
   decode_workspace_bytes(...), decode_counters_bytes(...), device_errors(), version(),
   selftest_wait_timeout()
 """
@@ -26,6 +28,7 @@ import threading
 
 from . import build as _build
 from . import grouped as _grouped
+from . import quantized as _quantized
 
 __all__ = ["PaError", "Dims", "KVManager", "lib", "reshape_and_cache", "copy_blocks", "decode",
            "decode_shared_prefix", "selftest_wait_timeout",
@@ -35,7 +38,8 @@ __all__ = ["PaError", "Dims", "KVManager", "lib", "reshape_and_cache", "copy_blo
            "DEVERR_SLOT", "DEVERR_TIMEOUT", "DEVERR_PREFIX", "DEVERR_POSITION",
            "rope_and_cache", "rope_table", "decode_grouped", "prefill_grouped",
            "decode_grouped_workspace_bytes", "decode_grouped_counters_bytes",
-           "prefill_grouped_workspace_bytes", "prefill_grouped_counters_bytes"]
+           "prefill_grouped_workspace_bytes", "prefill_grouped_counters_bytes",
+           "norm_rope_and_cache", "reshape_and_cache_q8", "gather_cache_q8", "decode_grouped_q8", "prefill_grouped_q8"]
 
 DEVERR_TABLE = 0x1
 DEVERR_CONTEXT = 0x2
@@ -61,7 +65,8 @@ EXPORTS = ("pa_reshape_and_cache", "pa_copy_blocks", "pa_decode", "pa_prefill", 
            "pa_kvm_prefix_groups",
            "pa_rope_and_cache", "pa_decode_grouped", "pa_decode_grouped_workspace_bytes",
            "pa_decode_grouped_counters_bytes", "pa_prefill_grouped",
-           "pa_prefill_grouped_workspace_bytes", "pa_prefill_grouped_counters_bytes")
+           "pa_prefill_grouped_workspace_bytes", "pa_prefill_grouped_counters_bytes",
+           "pa_norm_rope_and_cache", "pa_gather_cache_q8", "pa_decode_grouped_q8", "pa_prefill_grouped_q8")
 _SIZE_ERROR = (1 << 64) - 1
 
 
@@ -142,6 +147,7 @@ def _declare(l):
                  "pa_last_cuda_error", "pa_version"):
         getattr(l, name).restype = ctypes.c_int
     _grouped.declare(l, dp)
+    _quantized.declare(l, dp)
     return l
 
 
@@ -682,3 +688,5 @@ from .grouped import (decode_grouped, decode_grouped_counters_bytes,  # noqa: E4
                       decode_grouped_workspace_bytes, prefill_grouped,
                       prefill_grouped_counters_bytes, prefill_grouped_workspace_bytes,
                       rope_and_cache, rope_table)
+from .quantized import (decode_grouped_q8, gather_cache_q8, norm_rope_and_cache,  # noqa: E402
+                        prefill_grouped_q8, reshape_and_cache_q8)

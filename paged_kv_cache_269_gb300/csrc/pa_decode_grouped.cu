@@ -67,6 +67,7 @@
 #include <type_traits>
 
 #include "pa_device.cuh"
+#include "pa_fp8.cuh"
 #include "pa_internal.h"
 #include "pa_tensor.cuh"
 
@@ -91,6 +92,7 @@ struct DecodeGroupedArgs {
     int group, chunks;                 // heads per K/V head; chunks of heads per K/V head
     int chunk_shift;                   // sequences per prefix entry: 2^chunk_shift
     float *partials;                   // [2 * kMaxCtas][heads * (D + 2)]
+    int io_bf16;                       // 8-bit caches: q and out are bf16
 };
 
 template <bool kBf16>
@@ -159,6 +161,14 @@ __device__ __forceinline__ uint32_t pack_pair(float a, float b) {
         const __half2 h = __floats2half2_rn(a, b);
         return *reinterpret_cast<const uint32_t *>(&h);
     }
+}
+
+// Two output elements.  Over an 8-bit cache the products are fp16's whatever the
+// type outside is, so that one is looked up.
+template <bool kBf16, bool kQ8>
+__device__ __forceinline__ uint32_t pack_out(const DecodeGroupedArgs &p, float a, float b) {
+    if constexpr (kQ8) return p.io_bf16 ? pack_pair<true>(a, b) : pack_pair<false>(a, b);
+    return pack_pair<kBf16>(a, b);
 }
 
 // A sequence's visible keys as tiles of TK keys: tile i covers keys from
@@ -242,12 +252,13 @@ struct Cursor {
     }
 };
 
-template <int D, int NT>
+template <int D, int NT, bool kQ8>
 struct Cfg {
-    static constexpr int TK = D == 64 ? 32 : 16;       // keys per tile
+    static constexpr int kElem = kQ8 ? 1 : 2;          // bytes of a cache element
+    static constexpr int TK = kQ8 ? 4096 / D : (D == 64 ? 32 : 16);   // keys per tile
     static constexpr int MT = TK / 16;
     static constexpr int kHeads = 8 * NT;
-    static constexpr int kMat = TK * D * 2;            // bytes of a K (or V) tile
+    static constexpr int kMat = TK * D * kElem;            // bytes of a K (or V) tile
     static constexpr int kStage = 2 * kMat;
     // more bytes in flight do not help (a third stage for D = 128 made 256 long
     // sequences 7 % slower); for D = 64 there is room for one
@@ -282,7 +293,7 @@ __device__ __forceinline__ bool take_ticket(const DecodeGroupedArgs &p, int s, i
 
 // Joins the partials of a unit, which pieces i0 .. i1 left, and writes its
 // output rows.  tid of n threads.
-template <bool kBf16, int D, int kHeads>
+template <bool kBf16, bool kQ8, int D, int kHeads>
 __device__ __forceinline__ void join_unit(const DecodeGroupedArgs &p, int s, int unit, int i0, int i1,
                                           int tid, int n) {
     constexpr int kVec = D / 4;
@@ -321,20 +332,21 @@ __device__ __forceinline__ void join_unit(const DecodeGroupedArgs &p, int s, int
                 acc.x += f * v[c].x, acc.y += f * v[c].y, acc.z += f * v[c].z, acc.w += f * v[c].w;
             }
         }
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
-        uint2 r = make_uint2(pack_pair<kBf16>(acc.x * inv, acc.y * inv),
-                             pack_pair<kBf16>(acc.z * inv, acc.w * inv));
+        float inv = sum > 0.f ? 1.f / sum : 0.f;
+        if constexpr (kQ8) inv *= __ldg(a.v_scales + hk);
+        uint2 r = make_uint2(pack_out<kBf16, kQ8>(p, acc.x * inv, acc.y * inv),
+                             pack_out<kBf16, kQ8>(p, acc.z * inv, acc.w * inv));
         *reinterpret_cast<uint2 *>(
             a.out + (static_cast<size_t>(s) * a.num_q_heads + hk * p.group + h0 + h) * D + d4 * 4) = r;
     }
 }
 
-template <bool kBf16, int D, int NT, bool kDup>
+template <bool kBf16, bool kQ8, int D, int NT, bool kDup>
 __global__ void __launch_bounds__(kThreads, 1)
     decode_grouped_kernel(const __grid_constant__ CUtensorMap tm_k,
                           const __grid_constant__ CUtensorMap tm_v,
                           const __grid_constant__ DecodeGroupedArgs p) {
-    using C = Cfg<D, NT>;
+    using C = Cfg<D, NT, kQ8>;
     constexpr int TK = C::TK, kCost = C::kCost, MT = C::MT, KS = D / 16, kHeads = C::kHeads;
     const GroupedArgs &a = p.g;
     extern __shared__ uint8_t smem_raw[];
@@ -491,11 +503,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 
     // ---------------------------------------------------------- producer side
-    // A tile arrives as boxes of RB rows (8 for 8-token blocks, else 16): lane
-    // i < TK / RB owns box i, its table entry and its two copies.
+    // A tile arrives as boxes of RB rows (8 for 8-token blocks, else 16, or of an
+    // 8-bit cache a whole block where it fits the tile): lane i < TK / RB owns box
+    // i, its table entry and its two copies.
     const int B = a.block_size;
-    const int RB = B == 8 ? 8 : 16;
-    const int rb_shift = B == 8 ? 3 : 4;
+    const int RB = kQ8 ? min(B, TK) : (B == 8 ? 8 : 16);
+    const int rb_shift = RB == 8 ? 3 : (RB == 16 ? 4 : 5);
     const int boxes = TK / RB;
     Cursor<TK, kCost> prod = cons;
     int at = 0;                              // tile of the piece `prod` is at
@@ -527,12 +540,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const unsigned have = __ballot_sync(0xffffffffu, blk >= 0);
         if (lane == 0) {
             stage_mask[stage] = have;
-            mbar_arrive_expect_tx(&bar[stage], __popc(have) * 2u * RB * D * 2u);
+            mbar_arrive_expect_tx(&bar[stage], __popc(have) * 2u * RB * D * C::kElem);
         }
         __syncwarp();
         if (blk >= 0) {
             const int y = (blk * a.num_kv_heads + unit / p.chunks) * B + box_y;
-            uint8_t *dst = ring + stage * C::kStage + lane * (RB * D * 2);
+            uint8_t *dst = ring + stage * C::kStage + lane * (RB * D * C::kElem);
             tma_load_3d(dst, &tm_k, 0, y, 0, &bar[stage]);
             tma_load_3d(dst + C::kMat, &tm_v, 0, y, 0, &bar[stage]);
         }
@@ -570,9 +583,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t v_lane = vgrp * row_group + krow * 128;
     const int col = 2 * (lane & 3);          // the lane's two head columns
     const int row = lane >> 2;               // its key row (and row + 8)
+    // 8-bit caches: where a 16-byte chunk of a key's row lies; rows of 64 bytes are in
+    // the 64-byte swizzle, of 128 (256 as two halves, per box) in the 128-byte one.
+    // y: the key modulo 8.
+    [[maybe_unused]] auto q8_offset = [&](int key, int y, int chunk) -> uint32_t {
+        if constexpr (D == 64) return key * 64 + ((chunk ^ (y >> 1)) << 4);
+        if constexpr (D == 128) return key * 128 + ((chunk ^ y) << 4);
+        return (key / 8) * (B == 8 ? 2048 : 1024) + y * 128 + (chunk / 8) * half_step + (((chunk & 7) ^ y) << 4);
+    };
 
     uint32_t qf[KS][NT][2];
     float m[NT][2], l[NT][2], o[KS][NT][4], slope[NT][2];
+    float qs[NT][2];                         // 8-bit caches: what a column's scores are short of
     bool ok = true;
     int n_done = 0;                          // tiles taken
     int seg_start = 0;                       // CTA tile at which the segment starts
@@ -585,10 +607,51 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int nt = 0; nt < NT; ++nt) {
             const int hq = h0 + nt * 8 + (kDup ? (lane >> 2) % 4 : lane >> 2);
             const bool live = hq < p.group;
+            if constexpr (kQ8) {
+                // dims 16 ks + 4 (lane % 4) .. + 3: those that the lane's keys are widened to
+                uint2 raw[KS];
+                const uint2 *src2 = reinterpret_cast<const uint2 *>(src);
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                qf[ks][nt][0] = live ? __ldg(src + (hq * D + ks * 16) / 2 + (lane & 3)) : 0u;
-                qf[ks][nt][1] = live ? __ldg(src + (hq * D + ks * 16 + 8) / 2 + (lane & 3)) : 0u;
+                for (int ks = 0; ks < KS; ++ks)
+                    raw[ks] = live ? __ldg(src2 + (hq * D + ks * 16) / 4 + (lane & 3)) : make_uint2(0u, 0u);
+                float f = live ? __ldg(a.k_scales + hk) : 0.f;
+                if (p.io_bf16) {
+                    // to fp16, by a power of two that brings the row's largest element to
+                    // [2^10, 2^11): bf16's exponents do not fit, its 8 bits do
+                    float top = 0.f;
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                        for (int z = 0; z < 2; ++z) {
+                            const uint32_t u = z ? raw[ks].y : raw[ks].x;
+                            top = fmaxf(top, fmaxf(fabsf(__uint_as_float(u << 16)), fabsf(__uint_as_float(u & 0xFFFF0000u))));
+                        }
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    const int e = max(static_cast<int>(__float_as_uint(top) >> 23) - 137, -100);
+                    const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+                    f *= __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                        for (int z = 0; z < 2; ++z) {
+                            const uint32_t u = z ? raw[ks].y : raw[ks].x;
+                            qf[ks][nt][z] = pack_pair<false>(__uint_as_float(u << 16) * down,
+                                                             __uint_as_float(u & 0xFFFF0000u) * down);
+                        }
+                } else {
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks) qf[ks][nt][0] = raw[ks].x, qf[ks][nt][1] = raw[ks].y;
+                }
+                // the factors of the lane's two columns, from the lanes that hold these heads
+                qs[nt][0] = __shfl_sync(0xffffffffu, f, 4 * col);
+                qs[nt][1] = __shfl_sync(0xffffffffu, f, 4 * col + 4);
+            } else {
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) {
+                    qf[ks][nt][0] = live ? __ldg(src + (hq * D + ks * 16) / 2 + (lane & 3)) : 0u;
+                    qf[ks][nt][1] = live ? __ldg(src + (hq * D + ks * 16 + 8) / 2 + (lane & 3)) : 0u;
+                }
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -648,17 +711,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) sc[mt][nt][e] = 0.f;
+            if constexpr (kQ8) {
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                const uint32_t c16 = ks * 2 + kchunk;   // 16-byte chunk of the row
-                const uint32_t off = (ks / 4) * half_step + (((c16 & 7) ^ krow) << 4);
+                for (int ks = 0; ks < KS; ks += 2)      // two 16-byte chunks of the row
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    uint32_t kf[4];
-                    ldsm4(kf, kb + mt * (16 * D * 2) + k_lane + off);
+                    for (int mt = 0; mt < MT; ++mt) {
+                        uint32_t kf[4];                 // rows 0-7, 8-15 of chunk ks, then of chunk ks + 1
+                        ldsm4(kf, kb + q8_offset(mt * 16 + kgrp * 8 + krow, krow, ks + kchunk));
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        mma16816<kBf16>(sc[mt][nt], kf, qf[ks][nt][0], qf[ks][nt][1]);
+                        for (int z = 0; z < 2; ++z) {
+                            const uint32_t wide[4] = {e4m3x2_to_f16x2(kf[2 * z]), e4m3x2_to_f16x2(kf[2 * z + 1]),
+                                                      e4m3x2_to_f16x2_high(kf[2 * z]), e4m3x2_to_f16x2_high(kf[2 * z + 1])};
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma16816<kBf16>(sc[mt][nt], wide, qf[ks + z][nt][0], qf[ks + z][nt][1]);
+                        }
+                    }
+            } else {
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) {
+                    const uint32_t c16 = ks * 2 + kchunk;   // 16-byte chunk of the row
+                    const uint32_t off = (ks / 4) * half_step + (((c16 & 7) ^ krow) << 4);
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        uint32_t kf[4];
+                        ldsm4(kf, kb + mt * (16 * D * 2) + k_lane + off);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma16816<kBf16>(sc[mt][nt], kf, qf[ks][nt][0], qf[ks][nt][1]);
+                    }
                 }
             }
             // scores in the log2 domain
@@ -679,6 +760,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
+                            if constexpr (kQ8) sc[mt][nt][e] *= qs[nt][e & 1];
                             const float v = sc[mt][nt][e] * p.cap_v;
                             far |= !(v * v < 2.f);
                         }
@@ -704,7 +786,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) sc[mt][nt][e] *= p.scale_log2;
+                        for (int e = 0; e < 4; ++e) sc[mt][nt][e] *= kQ8 ? p.scale_log2 * qs[nt][e & 1] : p.scale_log2;
             }
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
@@ -785,20 +867,63 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 keep1 |= bits;
                         }
                     }
+                    if constexpr (kQ8) {
+                        // keys col, col + 1, col + 8, col + 9, 16 dims of each (8 at head_dim
+                        // 64): the bytes of two neighbouring keys side by side, widened, are
+                        // a lane's operands of the products
+                        constexpr int kWords = D == 64 ? 2 : 4;
 #pragma unroll
-                    for (int ks = 0; ks < KS; ++ks) {
-                        const uint32_t c16 = ks * 2 + vchunk;
-                        const uint32_t off = (ks / 4) * half_step + (((c16 & 7) ^ krow) << 4);
-                        uint32_t vf[4];
-                        ldsm4_trans(vf, vb + mt * (16 * D * 2) + v_lane + off);
-                        if constexpr (decltype(masked)::value) {
-                            vf[0] &= keep0, vf[1] &= keep0, vf[2] &= keep1, vf[3] &= keep1;
+                        for (int hf = 0; hf < (D + 127) / 128; ++hf) {
+                            uint32_t v[4][kWords];
+#pragma unroll
+                            for (int z = 0; z < 4; ++z) {
+                                const int key = mt * 16 + col + (z & 1) + (z & 2) * 4;
+                                const uint8_t *src = ring + st * C::kStage + C::kMat;
+                                if constexpr (D == 64) {
+                                    const uint2 t2 = *reinterpret_cast<const uint2 *>(
+                                        src + q8_offset(key, key & 7, row >> 1) + 8 * (row & 1));
+                                    v[z][0] = t2.x, v[z][1] = t2.y;
+                                } else {
+                                    const uint4 t4 = *reinterpret_cast<const uint4 *>(
+                                        src + q8_offset(key, key & 7, hf * 8 + row));
+                                    v[z][0] = t4.x, v[z][1] = t4.y, v[z][2] = t4.z, v[z][3] = t4.w;
+                                }
+                            }
+#pragma unroll
+                            for (int i = 0; i < 2 * kWords; ++i) {   // dims 2 i and 2 i + 1 of the lane's
+                                const uint32_t pick = i & 1 ? 0x7362 : 0x5140;
+                                const uint32_t p0 = __byte_perm(v[0][i / 2], v[1][i / 2], pick);
+                                const uint32_t p1 = __byte_perm(v[2][i / 2], v[3][i / 2], pick);
+                                uint32_t vf[4] = {e4m3x2_to_f16x2(p0), e4m3x2_to_f16x2_high(p0),
+                                                  e4m3x2_to_f16x2(p1), e4m3x2_to_f16x2_high(p1)};
+                                if constexpr (decltype(masked)::value) {
+                                    vf[0] &= keep0, vf[1] &= keep0, vf[2] &= keep1, vf[3] &= keep1;
+                                }
+                                const int ks = hf * 8 + i;
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt) {
+                                    mma16816<kBf16>(o[ks][nt], vf, ph_[mt][nt][0], ph_[mt][nt][1]);
+                                    if constexpr (!kDup)
+                                        mma16816<kBf16>(o[ks][nt], vf, pl_[mt][nt][0], pl_[mt][nt][1]);
+                                }
+                            }
                         }
+                    } else {
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            mma16816<kBf16>(o[ks][nt], vf, ph_[mt][nt][0], ph_[mt][nt][1]);
-                            if constexpr (!kDup)
-                                mma16816<kBf16>(o[ks][nt], vf, pl_[mt][nt][0], pl_[mt][nt][1]);
+                        for (int ks = 0; ks < KS; ++ks) {
+                            const uint32_t c16 = ks * 2 + vchunk;
+                            const uint32_t off = (ks / 4) * half_step + (((c16 & 7) ^ krow) << 4);
+                            uint32_t vf[4];
+                            ldsm4_trans(vf, vb + mt * (16 * D * 2) + v_lane + off);
+                            if constexpr (decltype(masked)::value) {
+                                vf[0] &= keep0, vf[1] &= keep0, vf[2] &= keep1, vf[3] &= keep1;
+                            }
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                mma16816<kBf16>(o[ks][nt], vf, ph_[mt][nt][0], ph_[mt][nt][1]);
+                                if constexpr (!kDup)
+                                    mma16816<kBf16>(o[ks][nt], vf, pl_[mt][nt][0], pl_[mt][nt][1]);
+                            }
                         }
                     }
                 }
@@ -840,11 +965,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int d = 4; d < 32; d *= 2) x += __shfl_xor_sync(0xffffffffu, x, d);
                 const int h = nt * 8 + col + e;
                 if (row == 0) ml[warp * kHeads + h] = make_float2(m[nt][e], x);
-                float *dst = obuf + (warp * kHeads + h) * C::kRow + row;
+                float *dst = obuf + (warp * kHeads + h) * C::kRow;
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) {
-                    dst[ks * 16] = o[ks][nt][e];
-                    dst[ks * 16 + 8] = o[ks][nt][e + 2];
+                    if constexpr (kQ8) {   // a lane's neighbouring dims
+                        *reinterpret_cast<float2 *>(dst + ks / 8 * 128 + row * (D == 64 ? 8 : 16) + ks % 8 * 2) =
+                            make_float2(o[ks][nt][e], o[ks][nt][e + 2]);
+                    } else {
+                        dst[ks * 16 + row] = o[ks][nt][e];
+                        dst[ks * 16 + row + 8] = o[ks][nt][e + 2];
+                    }
                 }
             }
         __syncthreads();
@@ -875,9 +1005,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 acc.x += f * v.x, acc.y += f * v.y, acc.z += f * v.z, acc.w += f * v.w;
             }
             if (whole) {
-                const float inv = sum > 0.f ? 1.f / sum : 0.f;
-                uint2 r = make_uint2(pack_pair<kBf16>(acc.x * inv, acc.y * inv),
-                                     pack_pair<kBf16>(acc.z * inv, acc.w * inv));
+                float inv = sum > 0.f ? 1.f / sum : 0.f;
+                if constexpr (kQ8) inv *= __ldg(a.v_scales + hk);
+                uint2 r = make_uint2(pack_out<kBf16, kQ8>(p, acc.x * inv, acc.y * inv),
+                                     pack_out<kBf16, kQ8>(p, acc.z * inv, acc.w * inv));
                 *reinterpret_cast<uint2 *>(
                     a.out + (static_cast<size_t>(s) * a.num_q_heads + hk * p.group + h0 + h) * D + d4 * 4) = r;
             } else {
@@ -898,7 +1029,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (warp == kW - 1) {
                     ok = ok && __all_sync(0xffffffffu, mbar_wait(part_bar, 0, abort_flag, a.err));
                     if (ok && take_ticket(p, s, units, unit, i1 - i0, lane)) {
-                        join_unit<kBf16, D, kHeads>(p, s, unit, i0, i1, lane, 32);
+                        join_unit<kBf16, kQ8, D, kHeads>(p, s, unit, i0, i1, lane, 32);
                     }
                 }
             } else {
@@ -908,7 +1039,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0) *last_flag = last;
                 }
                 __syncthreads();
-                if (*last_flag) join_unit<kBf16, D, kHeads>(p, s, unit, i0, i1, threadIdx.x, kThreads);
+                if (*last_flag) join_unit<kBf16, kQ8, D, kHeads>(p, s, unit, i0, i1, threadIdx.x, kThreads);
             }
         }
     }
@@ -919,40 +1050,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-int heads_per_chunk(int head_dim, int group) { return group > 8 && head_dim != 256 ? 16 : 8; }
+inline int heads_per_chunk(int head_dim, int group) { return group > 8 && head_dim != 256 ? 16 : 8; }
 
-using Kernel = void (*)(CUtensorMap, CUtensorMap, DecodeGroupedArgs);
-struct Variant {
-    Kernel kernel;
-    int smem, ctas_per_sm;
-};
-template <bool kBf16, int D>
-Variant variant_of(int group) {
-    if (D != 256 && group > 8)
-        return {decode_grouped_kernel<kBf16, D, D == 256 ? 1 : 2, false>, Cfg<D, D == 256 ? 1 : 2>::kBytes,
-                Cfg<D, D == 256 ? 1 : 2>::kCtasPerSm};
-    if (group > 4)
-        return {decode_grouped_kernel<kBf16, D, 1, false>, Cfg<D, 1>::kBytes, Cfg<D, 1>::kCtasPerSm};
-    return {decode_grouped_kernel<kBf16, D, 1, true>, Cfg<D, 1>::kBytes, Cfg<D, 1>::kCtasPerSm};
-}
-
-}  // namespace
-
-size_t decode_grouped_workspace_bytes(int head_dim, int group) {
-    return static_cast<size_t>(2 * kMaxCtas) * heads_per_chunk(head_dim, group) * (head_dim + 2) * 4;
-}
-// A ticket for every unit, and nothing else (take_ticket); never 0, which says
-// that the sizes are invalid.
-size_t decode_grouped_counters_bytes(int num_seqs, int num_kv_heads, int group, int head_dim) {
-    const int per = heads_per_chunk(head_dim, group);
-    const size_t tickets = static_cast<size_t>(num_seqs) * num_kv_heads * ((group + per - 1) / per);
-    return (tickets < 1 ? 1 : (tickets + 63) / 64) * 256;
-}
-
-cudaError_t launch_decode_grouped(const GroupedArgs &args, int dtype, int head_dim, int num_sms,
-                                  cudaStream_t stream) {
-    const bool bf16 = dtype == PA_DTYPE_BF16;
-    const int B = args.block_size, Hk = args.num_kv_heads;
+// What the kernels take beside the caller's arguments.
+inline DecodeGroupedArgs prepare_args(const GroupedArgs &args, int head_dim) {
     DecodeGroupedArgs p;
     p.g = args;
     const double log2e = 1.4426950408889634;
@@ -960,33 +1061,35 @@ cudaError_t launch_decode_grouped(const GroupedArgs &args, int dtype, int head_d
     p.cap_log2 = static_cast<float>(args.softcap * log2e);
     p.cap_in = args.softcap > 0.f ? static_cast<float>(2.0 * args.scale / args.softcap * log2e) : 0.f;
     fill_tanh(args.scale, args.softcap, &p.cap_v, p.tanh_k);
-    p.group = args.num_q_heads / Hk;
+    p.group = args.num_q_heads / args.num_kv_heads;
     const int per = heads_per_chunk(head_dim, p.group);
     p.chunks = (p.group + per - 1) / per;
     p.chunk_shift = 0;
     while (((static_cast<long long>(args.num_seqs) - 1) >> p.chunk_shift) >= kChunks) ++p.chunk_shift;
     p.partials = static_cast<float *>(args.workspace);
+    p.io_bf16 = 0;
+    return p;
+}
 
-    // [D / 64 halves] x [all cache rows] x 64 dims: one box is a block's rows
-    // (or 16 of them) of one head, each half in the 128-byte swizzle
-    CUtensorMap tm_k, tm_v;
-    const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(args.num_blocks) * Hk * B,
-                                static_cast<cuuint64_t>(head_dim / 64)};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_dim) * 2, 128};
-    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(B == 8 ? 8 : 16),
-                               static_cast<cuuint32_t>(head_dim / 64)};
-    if (!encode(&tm_k, bf16, args.k_cache, 3, dims, strides, box) ||
-        !encode(&tm_v, bf16, args.v_cache, 3, dims, strides, box))
-        return cudaErrorInvalidValue;
+using Kernel = void (*)(CUtensorMap, CUtensorMap, DecodeGroupedArgs);
+struct Variant {
+    Kernel kernel;
+    int smem, ctas_per_sm;
+};
+template <bool kBf16, bool kQ8, int D>
+Variant variant_of(int group) {
+    if (D != 256 && group > 8)
+        return {decode_grouped_kernel<kBf16, kQ8, D, D == 256 ? 1 : 2, false>, Cfg<D, D == 256 ? 1 : 2, kQ8>::kBytes,
+                Cfg<D, D == 256 ? 1 : 2, kQ8>::kCtasPerSm};
+    if (group > 4)
+        return {decode_grouped_kernel<kBf16, kQ8, D, 1, false>, Cfg<D, 1, kQ8>::kBytes, Cfg<D, 1, kQ8>::kCtasPerSm};
+    return {decode_grouped_kernel<kBf16, kQ8, D, 1, true>, Cfg<D, 1, kQ8>::kBytes, Cfg<D, 1, kQ8>::kCtasPerSm};
+}
 
-    Variant v;
-    if (bf16)
-        v = head_dim == 64 ? variant_of<true, 64>(p.group)
-                           : (head_dim == 128 ? variant_of<true, 128>(p.group) : variant_of<true, 256>(p.group));
-    else
-        v = head_dim == 64 ? variant_of<false, 64>(p.group)
-                           : (head_dim == 128 ? variant_of<false, 128>(p.group) : variant_of<false, 256>(p.group));
-    // the kernel's shared-memory limit, once per device and variant
+// Launches a variant; its shared-memory limit is set once per device (`which`: the
+// variant's number among those of one file, below 18).
+inline cudaError_t launch_variant(const Variant &v, int which, CUtensorMap &tm_k, CUtensorMap &tm_v, DecodeGroupedArgs &p,
+                           int num_sms, cudaStream_t stream) {
     int device = 0;
     cudaError_t e = cudaGetDevice(&device);
     if (e != cudaSuccess) return e;
@@ -994,7 +1097,6 @@ cudaError_t launch_decode_grouped(const GroupedArgs &args, int dtype, int head_d
     {
         static std::mutex mu;
         static bool ready[64][18] = {};
-        const int which = (bf16 ? 9 : 0) + (head_dim == 64 ? 0 : head_dim == 128 ? 3 : 6) + (p.group <= 4 ? 0 : p.group <= 8 ? 1 : 2);
         std::lock_guard<std::mutex> lock(mu);
         if (!ready[device][which]) {
             e = cudaFuncSetAttribute(reinterpret_cast<const void *>(v.kernel),
@@ -1017,5 +1119,51 @@ cudaError_t launch_decode_grouped(const GroupedArgs &args, int dtype, int head_d
     void *params[] = {&tm_k, &tm_v, &p};
     return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void *>(v.kernel), params);
 }
+
+}  // namespace
+
+#ifndef PA_Q8_LAUNCHES   // pa_decode_q8.cu takes the kernel alone
+
+size_t decode_grouped_workspace_bytes(int head_dim, int group) {
+    return static_cast<size_t>(2 * kMaxCtas) * heads_per_chunk(head_dim, group) * (head_dim + 2) * 4;
+}
+// A ticket for every unit, and nothing else (take_ticket); never 0, which says
+// that the sizes are invalid.
+size_t decode_grouped_counters_bytes(int num_seqs, int num_kv_heads, int group, int head_dim) {
+    const int per = heads_per_chunk(head_dim, group);
+    const size_t tickets = static_cast<size_t>(num_seqs) * num_kv_heads * ((group + per - 1) / per);
+    return (tickets < 1 ? 1 : (tickets + 63) / 64) * 256;
+}
+
+cudaError_t launch_decode_grouped(const GroupedArgs &args, int dtype, int head_dim, int num_sms,
+                                  cudaStream_t stream) {
+    const bool bf16 = dtype == PA_DTYPE_BF16;
+    const int B = args.block_size, Hk = args.num_kv_heads;
+    DecodeGroupedArgs p = prepare_args(args, head_dim);
+
+    // [D / 64 halves] x [all cache rows] x 64 dims: one box is a block's rows
+    // (or 16 of them) of one head, each half in the 128-byte swizzle
+    CUtensorMap tm_k, tm_v;
+    const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(args.num_blocks) * Hk * B,
+                                static_cast<cuuint64_t>(head_dim / 64)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_dim) * 2, 128};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(B == 8 ? 8 : 16),
+                               static_cast<cuuint32_t>(head_dim / 64)};
+    if (!encode(&tm_k, bf16, args.k_cache, 3, dims, strides, box) ||
+        !encode(&tm_v, bf16, args.v_cache, 3, dims, strides, box))
+        return cudaErrorInvalidValue;
+
+    Variant v;
+    if (bf16)
+        v = head_dim == 64 ? variant_of<true, false, 64>(p.group)
+                           : (head_dim == 128 ? variant_of<true, false, 128>(p.group) : variant_of<true, false, 256>(p.group));
+    else
+        v = head_dim == 64 ? variant_of<false, false, 64>(p.group)
+                           : (head_dim == 128 ? variant_of<false, false, 128>(p.group) : variant_of<false, false, 256>(p.group));
+    const int which = (bf16 ? 9 : 0) + (head_dim == 64 ? 0 : head_dim == 128 ? 3 : 6) + (p.group <= 4 ? 0 : p.group <= 8 ? 1 : 2);
+    return launch_variant(v, which, tm_k, tm_v, p, num_sms, stream);
+}
+
+#endif  // PA_Q8_LAUNCHES
 
 }  // namespace pa

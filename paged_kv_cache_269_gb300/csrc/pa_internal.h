@@ -139,6 +139,8 @@ struct GroupedArgs {
     const int32_t *query_start;    // [S + 1] (prefill)
     const float *alibi_slopes;     // [Hq] or nullptr
     const int32_t *prefix_lens;    // [S] or nullptr
+    const float *k_scales;         // [Hkv], or nullptr: the caches are of 16 bits
+    const float *v_scales;         // [Hkv]; with them the caches are e4m3 [N, Hkv, B, D]
     float scale;
     float softcap;                 // 0: none
     int32_t window;                // 0: none
@@ -183,6 +185,11 @@ cudaError_t launch_decode_grouped(const GroupedArgs &args, int dtype, int head_d
                                   cudaStream_t stream);
 cudaError_t launch_prefill_grouped(const GroupedArgs &args, int dtype, int head_dim, int num_sms,
                                    cudaStream_t stream);
+// Over an 8-bit cache (with scales); plans, workspaces and counters are the same.
+cudaError_t launch_decode_grouped_q8(const GroupedArgs &args, int dtype, int head_dim, int num_sms,
+                                     cudaStream_t stream);
+cudaError_t launch_prefill_grouped_q8(const GroupedArgs &args, int dtype, int head_dim, int num_sms,
+                                      cudaStream_t stream);
 
 // Arguments of one rope_and_cache launch (device pointers unless noted).
 struct RopeArgs {
@@ -200,5 +207,36 @@ struct RopeArgs {
 };
 cudaError_t launch_rope_and_cache(const RopeArgs &args, int dtype, bool interleaved, int num_sms,
                                   cudaStream_t stream);
+
+// Arguments of one norm_rope_and_cache launch (device pointers unless noted).
+struct AppendArgs {
+    uint16_t *q_out;
+    const uint16_t *q, *k, *v;
+    void *k_cache, *v_cache;       // [N, Hkv, B, D]: 16-bit, or e4m3 where there are scales
+    const int32_t *positions;      // [T], or nullptr: no token is padding
+    const float *cos_sin;          // [max_positions, rotary_dim]; not read for rotary_dim 0
+    const int32_t *slot_mapping;   // [T]
+    const float *q_weight, *k_weight;   // [D], or nullptr: no norm
+    const float *k_scales, *v_scales;   // [Hkv], or nullptr
+    long long q_stride, k_stride, v_stride, q_out_stride;   // elements between tokens
+    int32_t num_tokens, num_q_heads, num_kv_heads, head_dim, block_size;
+    int32_t rotary_dim, max_positions;
+    float eps, inv_dim;            // inv_dim: 1 / D
+    long long pool_slots;          // N * B
+    unsigned int *err;
+};
+cudaError_t launch_norm_rope(const AppendArgs &args, int dtype, bool interleaved, int num_sms, cudaStream_t stream);
+
+// Arguments of one gather_cache_q8 launch (device pointers unless noted).
+struct GatherArgs {
+    uint16_t *k_out, *v_out;       // [T, Hkv, D]
+    const uint8_t *k_cache, *v_cache;   // e4m3 [N, Hkv, B, D]
+    const float *k_scales, *v_scales;   // [Hkv]
+    const int32_t *slots;          // [T]
+    int32_t num_tokens, num_kv_heads, head_dim, block_size;
+    long long pool_slots;          // N * B
+    unsigned int *err;
+};
+cudaError_t launch_gather_q8(const GatherArgs &args, int dtype, cudaStream_t stream);
 
 }  // namespace pa

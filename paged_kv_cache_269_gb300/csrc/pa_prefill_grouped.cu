@@ -90,6 +90,7 @@
 #include <type_traits>
 
 #include "pa_device.cuh"
+#include "pa_fp8.cuh"
 #include "pa_internal.h"
 #include "pa_tensor.cuh"
 
@@ -98,11 +99,12 @@ namespace {
 
 constexpr int kBM = 128;               // rows per tile (MMA M)
 constexpr int kBN = 64;                // keys per tile
-constexpr int kThreads = 512;          // 2 x 4 softmax warps, 2 TMA warps, 4 MMA warps, 2 idle
+constexpr int kThreads = 512;          // 2 x 4 softmax warps, 2 TMA warps, 4 MMA warps, 2 that widen
 constexpr int kTmaWarp = 8;            // items, Q, K
 constexpr int kVWarp = 13;
 constexpr int kSWarp0 = 9;
 constexpr int kPvWarp0 = 11;
+constexpr int kWidenWarp0 = 14;        // 8-bit caches: K, then V; idle otherwise
 // Register split: launched at 128 per thread; the warpgroups of the TMA and
 // MMA warps give registers up to the softmax warps: 2 x 168 + 2 x 88 = 4 x 128.
 constexpr int kRegsSoftmax = 168, kRegsOther = 88;
@@ -154,7 +156,7 @@ struct Item {
     int s;
 };
 
-template <int D>
+template <int D, bool kQ8>
 struct Cfg {
     static constexpr int kHalves = D / 64;
     static constexpr int kHalfQ = kBM * 128;
@@ -178,13 +180,16 @@ struct Cfg {
     static constexpr int PARTS = 29, TICKET = 31;                // [tile]
     static constexpr int K_FULL = 33, V_FULL = K_FULL + kSlots;
     static constexpr int K_EMPTY = V_FULL + kSlots, V_EMPTY = K_EMPTY + kSlots;
-    static constexpr int kNumBars = V_EMPTY + kSlots;
+    // 8-bit caches: a tile's bytes are there (K, then V), to be widened
+    static constexpr int K_BYTES = V_EMPTY + kSlots, V_BYTES = K_BYTES + (kQ8 ? kSlots : 0);
+    static constexpr int kNumBars = V_BYTES + (kQ8 ? kSlots : 0);
     static constexpr int OFF_TMEM = OFF_BAR + kNumBars * 8;
     static constexpr int OFF_FLAG = OFF_TMEM + 4;
     static constexpr int OFF_LAST = OFF_FLAG + 4;                   // int[2]
     static constexpr int OFF_MASK = OFF_LAST + 8;                   // uint32[kMaskRing]
     static constexpr int OFF_ITEM = OFF_MASK + kMaskRing * 4;       // Item[2]
-    static constexpr int kSmemBytes = OFF_ITEM + 2 * static_cast<int>(sizeof(Item)) + 1024;
+    static constexpr int OFF_INFO = OFF_ITEM + 2 * static_cast<int>(sizeof(Item));   // uint32[kSlots]: V's rows
+    static constexpr int kSmemBytes = OFF_INFO + (kQ8 ? kSlots * 4 : 0) + 1024;
     static_assert(kSmemBytes <= 232448, "shared memory");
     // A tile's entry in the mask ring is read by the softmax before its P and is
     // rewritten without a wait, so the ring is longer than the K warp can get
@@ -334,18 +339,72 @@ struct KeyBlocks {
     __device__ __forceinline__ int group(int blk) const { return (blk * heads + hk) << (b_shift - 3); }
 };
 
+// A tile of kBN keys of an 8-bit cache, widened where it lies: its bytes are in the
+// upper half of the slot, key after key, and become the slot's 16-bit operand
+// layout.  Groups of 8 keys in order, each read before the one ahead of it is
+// written: a group's output ends where the bytes of the next one start, or before.
+// valid(key): keys to keep, the others become 0.
+//
+// A lane's chunk of 16 numbers: lanes 8 q .. 8 q + 7 take keys 2 q and 2 q + 1, half a
+// row of each and not the same half, so that neither the loads nor the stores (every
+// other 16-byte chunk of a line, even ones of one key and odd ones of the next) meet
+// in a bank.
+template <bool kBf16, int D, typename Valid>
+__device__ __forceinline__ void widen_tile(uint8_t *slot, int lane, Valid &&valid) {
+    constexpr int kGroup = D * 16, kIn = D * 8, kPer = D / 64;   // bytes out and in a group; chunks a lane
+    const uint8_t *in = slot + kBN * D;
+    const int y = D == 64 ? lane / 4 : lane / 8 * 2 + (lane >> 2 & 1);   // key within the group
+    auto chunk_of = [&](int u) { return (lane & 3) + (D == 64 ? 0 : 4 * ((lane >> 2 & 1) ^ u)); };
+    uint4 next[kPer];
+    auto fetch = [&](int g) {
+#pragma unroll
+        for (int u = 0; u < kPer; ++u)
+            next[u] = *reinterpret_cast<const uint4 *>(in + g * kIn + y * D + chunk_of(u) * 16);
+    };
+    fetch(0);
+#pragma unroll
+    for (int g = 0; g < kBN / 8; ++g) {
+        uint4 now[kPer];
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) now[u] = valid(g * 8 + y) ? next[u] : make_uint4(0, 0, 0, 0);
+        if (g + 1 < kBN / 8) fetch(g + 1);
+        __syncwarp();
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) {
+            const uint32_t w[4] = {now[u].x, now[u].y, now[u].z, now[u].w};
+            uint32_t o[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                o[2 * i] = e4m3x2_to_f16x2(w[i]);
+                o[2 * i + 1] = e4m3x2_to_f16x2_high(w[i]);
+            }
+            if constexpr (kBf16) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&o[i]));
+                    o[i] = pack_pair<true>(f.x, f.y);
+                }
+            }
+            const int c = chunk_of(u), c16 = 2 * (c & 3);
+            uint8_t *line = slot + g * kGroup + (c >> 2) * 1024 + y * 128;
+            *reinterpret_cast<uint4 *>(line + ((c16 ^ y) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4 *>(line + (((c16 + 1) ^ y) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+        }
+    }
+}
+
 // kSplit: the call has key splits.  A call without them runs a kernel that leaves
 // out the code that writes and joins partials, which the softmax warps' loop pays
 // for although it does not run (one prompt of 8192 tokens: 348 us with it, 333
 // without).
-template <bool kBf16, int D, bool kCap, bool kAlibi, bool kSplit>
+template <bool kBf16, bool kQ8, int D, bool kCap, bool kAlibi, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_grouped_kernel(const __grid_constant__ CUtensorMap tm_q,
                            const __grid_constant__ CUtensorMap tm_k,
                            const __grid_constant__ CUtensorMap tm_v,
                            const __grid_constant__ CUtensorMap tm_out,
                            const __grid_constant__ PrefillGroupedArgs p) {
-    using C = Cfg<D>;
+    using C = Cfg<D, kQ8>;
     const GroupedArgs &a = p.g;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -356,6 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int *last_flag = reinterpret_cast<volatile int *>(smem + C::OFF_LAST);
     volatile uint32_t *mask_ring = reinterpret_cast<volatile uint32_t *>(smem + C::OFF_MASK);
     Item *items = reinterpret_cast<Item *>(smem + C::OFF_ITEM);
+    [[maybe_unused]] volatile uint32_t *v_rows = reinterpret_cast<volatile uint32_t *>(smem + C::OFF_INFO);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int B = a.block_size, b_shift = B == 8 ? 3 : (B == 16 ? 4 : 5);
 
@@ -364,8 +424,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t count = 1;
             if ((i >= C::P_FULL && i < C::P_FULL + 6) || i == C::PARTS || i == C::PARTS + 1)
                 count = 4;                                    // softmax warps
-            if (i == C::ITEM_EMPTY || i == C::ITEM_EMPTY + 1) count = 13;     // 4 MMA threads, 8 softmax warps, V
-            if (i >= C::K_EMPTY) count = 2;               // both tiles' threads
+            if (i == C::ITEM_EMPTY || i == C::ITEM_EMPTY + 1) count = kQ8 ? 15 : 13;     // 4 MMA threads, 8 softmax warps, V, 2 that widen
+            if (i >= C::K_EMPTY && i < C::V_EMPTY + C::kSlots) count = 2;               // both tiles' threads
             mbar_init(&bar[i], count);
         }
         *abort_flag = 0;
@@ -446,12 +506,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!ok) break;
                     if (lane == 0) {
                         mask_ring[g % kMaskRing] = have;
-                        mbar_arrive_expect_tx(&bar[C::K_FULL + st], __popc(have) * static_cast<uint32_t>(B * D * 2));
+                        mbar_arrive_expect_tx(&bar[kQ8 ? C::K_BYTES + st : C::K_FULL + st],
+                                              __popc(have) * static_cast<uint32_t>(kQ8 ? B * D : B * D * 2));
                     }
                     __syncwarp();
-                    if (blk >= 0)
-                        tma_load_4d(smem + C::OFF_K + st * C::kTileKV + lane * (B / 8) * C::kGroup, &tm_k, 0, 0, 0,
-                                    blocks.group(blk), &bar[C::K_FULL + st]);
+                    if (blk >= 0) {
+                        if constexpr (kQ8)
+                            bulk_copy_g2s(smem + C::OFF_K + st * C::kTileKV + kBN * D + lane * (B * D),
+                                          reinterpret_cast<const uint8_t *>(a.k_cache) +
+                                              static_cast<size_t>(blocks.group(blk)) * (8 * D),
+                                          B * D, &bar[C::K_BYTES + st]);
+                        else
+                            tma_load_4d(smem + C::OFF_K + st * C::kTileKV + lane * (B / 8) * C::kGroup, &tm_k, 0, 0, 0,
+                                        blocks.group(blk), &bar[C::K_FULL + st]);
+                    }
                     ++g;
                     blk = next;
                 }
@@ -463,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int i = max(0, k - 1); i <= k; ++i)   // item k's Q may be on its way
                         if (i < q_loads) mbar_wait_drain(&bar[C::Q_FULL + (i & 1)], (i >> 1) & 1);
                     for (uint32_t i = g > C::kSlots ? g - C::kSlots : 0; i < g; ++i)
-                        mbar_wait_drain(&bar[C::K_FULL + i % C::kSlots], (i / C::kSlots) & 1);
+                        mbar_wait_drain(&bar[(kQ8 ? C::K_BYTES : C::K_FULL) + i % C::kSlots], (i / C::kSlots) & 1);
                 }
                 __threadfence();
                 if (atomicAdd(a.counters + 1, 1u) == gridDim.x - 1) {
@@ -494,6 +562,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = warp_all(mbar_wait(&bar[C::V_EMPTY + st], ((g / C::kSlots) & 1) ^ 1, abort_flag, a.err));
                     if (!ok) break;
                     uint8_t *vt = smem + C::OFF_V + st * C::kTileKV;
+                    if constexpr (kQ8) {   // what is not seen is cleared as the rest is widened
+                        if (lane == 0) {
+                            const int tail = max(0, min(kBN, it.ctx - blocks.first_key(it, j)));
+                            v_rows[st] = have | static_cast<uint32_t>(tail) << 16;
+                            mbar_arrive_expect_tx(&bar[C::V_BYTES + st], __popc(have) * static_cast<uint32_t>(B * D));
+                        }
+                        __syncwarp();
+                        if (blk >= 0)
+                            bulk_copy_g2s(vt + kBN * D + lane * (B * D),
+                                          reinterpret_cast<const uint8_t *>(a.v_cache) +
+                                              static_cast<size_t>(blocks.group(blk)) * (8 * D),
+                                          B * D, &bar[C::V_BYTES + st]);
+                        ++g;
+                        blk = next;
+                        continue;
+                    }
                     auto clear_row = [&](int r) {
                         for (int c = lane; c < C::kHalves * 8; c += 32)
                             *reinterpret_cast<uint4 *>(vt + (r / 8) * C::kGroup + (c / 8) * 1024 + (r % 8) * 128 +
@@ -532,7 +616,48 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!ok && lane == 0)   // let every copy already issued land
                 for (uint32_t i = g > C::kSlots ? g - C::kSlots : 0; i < g; ++i)
-                    mbar_wait_drain(&bar[C::V_FULL + i % C::kSlots], (i / C::kSlots) & 1);
+                    mbar_wait_drain(&bar[(kQ8 ? C::V_BYTES : C::V_FULL) + i % C::kSlots], (i / C::kSlots) & 1);
+            __syncwarp();
+        } else if (kQ8 && warp >= kWidenWarp0) {
+            // -------------------------------------------------------- 8 bits to 16
+            if constexpr (kQ8) {
+                const bool is_k = warp == kWidenWarp0;
+                uint64_t *bytes = &bar[is_k ? C::K_BYTES : C::V_BYTES], *full = &bar[is_k ? C::K_FULL : C::V_FULL];
+                uint8_t *slots = smem + (is_k ? C::OFF_K : C::OFF_V);
+                uint32_t g = 0;                    // tiles widened, over all items
+                bool ok = true;
+                for (int k = 0; ok; ++k) {
+                    const int slot = k % 2;
+                    ok = warp_all(mbar_wait(&bar[C::ITEM_FULL + slot], (k / 2) & 1, abort_flag, a.err));
+                    if (!ok) break;
+                    const bool done = static_cast<const volatile Item *>(items + slot)->done;
+                    const int nkt = static_cast<const volatile Item *>(items + slot)->nkt;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar[C::ITEM_EMPTY + slot]);
+                    if (done) break;
+                    for (int j = 0; j < nkt; ++j, ++g) {
+                        const uint32_t st = g % C::kSlots;
+                        ok = warp_all(mbar_wait(bytes + st, (g / C::kSlots) & 1, abort_flag, a.err));
+                        if (!ok) break;
+                        uint8_t *tile = slots + st * C::kTileKV;
+                        if (is_k) {
+                            widen_tile<kBf16, D>(tile, lane, [](int) { return true; });
+                        } else {
+                            const uint32_t rows = v_rows[st];
+                            const int tail = static_cast<int>(rows >> 16);
+                            if (tail == kBN && (rows & 0xffffu) == (1u << (kBN >> b_shift)) - 1)
+                                widen_tile<kBf16, D>(tile, lane, [](int) { return true; });
+                            else
+                                widen_tile<kBf16, D>(tile, lane, [&](int r) {
+                                    return r < tail && ((rows >> (r >> b_shift)) & 1);
+                                });
+                        }
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(full + st);
+                    }
+                }
+            }
             __syncwarp();
         } else if (warp >= kSWarp0 && warp < kPvWarp0 + 2) {
             // -------------------------------------------------------- products
@@ -613,7 +738,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp % 4) * 32) << 16);
         const uint32_t s_cols = lane_base + t * C::kBufs * 64;
         const uint32_t o_col = lane_base + C::TM_O + t * D;
-        const float c = p.scale_log2;
+        float c = p.scale_log2;            // 8-bit caches: times the head's scale, for each item
         const unsigned full = (1u << (kBN >> b_shift)) - 1;
         // the polynomial's coefficients as pairs, kept in registers (volatile: not
         // built again at each use, which took as many moves as products)
@@ -623,6 +748,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 5; ++i) tanh2[i] = keep_pair(p.tanh_k[i]);
             cap_v2 = keep_pair(p.cap_v);
         }
+        float cap_v = p.cap_v, cap_in = p.cap_in;   // as c
         // The item before: its slot and its Q buffer, which holds the staged rows,
         // are handed back once the copies out of it have read them.
         int pending = -1;
@@ -669,6 +795,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int wmin = __reduce_min_sync(0xffffffffu, pos);
             const int pre_all = it->pre, na = it->na, skip = it->skip, j0 = it->j0;
             const int last = j0 + max(nk, 0) - 1;
+            if constexpr (kQ8) {
+                const float f = __ldg(a.k_scales + it->hk);
+                c = p.scale_log2 * f;
+                if constexpr (kCap) {
+                    cap_v = p.cap_v * f;
+                    cap_in = p.cap_in * f;
+                    cap_v2 = keep_pair(cap_v);
+                }
+            }
             float slope = 0.f;
             if constexpr (kAlibi)
                 slope = pos >= 0 ? __ldg(a.alibi_slopes + it->hk * p.group + head) * 1.4426950408889634f : 0.f;
@@ -709,7 +844,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 };
                 // cap tanh(s / cap) + bias by 1 - 2 / (1 + e^(2 s / cap)), in log2 units
                 auto cap_mufu = [&](float s, float b) {
-                    return fmaf(-2.f * p.cap_log2, fast_rcp(1.f + fast_exp2(s * p.cap_in)), p.cap_log2 + b);
+                    return fmaf(-2.f * p.cap_log2, fast_rcp(1.f + fast_exp2(s * (kQ8 ? cap_in : p.cap_in))), p.cap_log2 + b);
                 };
                 // One bit per key: keys before pr, and from lw up to h (none for a row
                 // without a query), in blocks that are there.
@@ -823,7 +958,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (!warp_all(far < 0x40000000u)) {
 #pragma unroll
                                 for (int e = 0; e < 16; ++e) {
-                                    const float v = __uint_as_float(u[e]) * p.cap_v;
+                                    const float v = __uint_as_float(u[e]) * (kQ8 ? cap_v : p.cap_v);
                                     if (!(v * v < 2.f)) z[e] = cap_mufu(__uint_as_float(u[e]), 0.f);
                                 }
                             }
@@ -908,7 +1043,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const int splits = kSplit ? it->splits : 1;
             if (!kSplit || splits == 1) {
-                const float inv = l > 0.f ? 1.f / l : 0.f;
+                float inv = l > 0.f ? 1.f / l : 0.f;
+                if constexpr (kQ8) inv *= __ldg(a.v_scales + it->hk);
                 const bool whole = p.store_boxes && warp_all(live);
 #pragma unroll
                 for (int hf = 0; hf < C::kHalves; ++hf) {
@@ -1029,7 +1165,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int z = 0; z < kZ; ++z)
                             if (z0 + z < splits && mz[z] != -INFINITY) total += fast_exp2(mz[z] - top) * lz[z];
                     }
-                    const float inv = total > 0.f ? 1.f / total : 0.f;
+                    float inv = total > 0.f ? 1.f / total : 0.f;
+                    if constexpr (kQ8) inv *= __ldg(a.v_scales + it->hk);
 #pragma unroll 1
                     for (int d0 = warp % 4 * (D / 4); d0 < (warp % 4 + 1) * (D / 4); d0 += 16) {
                         float acc[16];
@@ -1084,7 +1221,7 @@ struct Plan {
     long long pairs, base;    // base: items without splits
     int splits;
 };
-Plan make_plan(int num_seqs, int num_kv_heads, int group, int max_q) {
+inline Plan make_plan(int num_seqs, int num_kv_heads, int group, int max_q) {
     Plan pl;
     const int tpt = kBM / group;
     pl.pairs = (static_cast<long long>(max_q) + 2 * tpt - 1) / (2 * tpt);
@@ -1094,41 +1231,22 @@ Plan make_plan(int num_seqs, int num_kv_heads, int group, int max_q) {
 }
 
 using Kernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, PrefillGroupedArgs);
-template <bool kBf16, int D, bool kSplit>
+template <bool kBf16, bool kQ8, int D, bool kSplit>
 Kernel pick(bool cap, bool alibi) {
-    return cap ? (alibi ? prefill_grouped_kernel<kBf16, D, true, true, kSplit>
-                        : prefill_grouped_kernel<kBf16, D, true, false, kSplit>)
-               : (alibi ? prefill_grouped_kernel<kBf16, D, false, true, kSplit>
-                        : prefill_grouped_kernel<kBf16, D, false, false, kSplit>);
+    return cap ? (alibi ? prefill_grouped_kernel<kBf16, kQ8, D, true, true, kSplit>
+                        : prefill_grouped_kernel<kBf16, kQ8, D, true, false, kSplit>)
+               : (alibi ? prefill_grouped_kernel<kBf16, kQ8, D, false, true, kSplit>
+                        : prefill_grouped_kernel<kBf16, kQ8, D, false, false, kSplit>);
 }
-template <bool kSplit>
+template <bool kQ8, bool kSplit>
 Kernel pick(bool bf16, int D, bool cap, bool alibi) {
-    return bf16 ? (D == 64 ? pick<true, 64, kSplit>(cap, alibi) : pick<true, 128, kSplit>(cap, alibi))
-                : (D == 64 ? pick<false, 64, kSplit>(cap, alibi) : pick<false, 128, kSplit>(cap, alibi));
+    return bf16 ? (D == 64 ? pick<true, kQ8, 64, kSplit>(cap, alibi) : pick<true, kQ8, 128, kSplit>(cap, alibi))
+                : (D == 64 ? pick<false, kQ8, 64, kSplit>(cap, alibi) : pick<false, kQ8, 128, kSplit>(cap, alibi));
 }
 
-}  // namespace
-
-bool prefill_grouped_supported(int dtype, int head_dim, int block_size, int group) {
-    return decode_variant_supported(dtype, head_dim, block_size) && head_dim != 256 && group <= kBM;
-}
-
-size_t prefill_grouped_workspace_bytes(int num_seqs, int num_kv_heads, int group, int head_dim,
-                                       int max_query_len) {
-    const Plan pl = make_plan(num_seqs, num_kv_heads, group, max_query_len);
-    if (pl.splits <= 1) return 0;
-    return static_cast<size_t>(pl.base) * pl.splits * 2 * (head_dim + 2) * kBM * sizeof(float);
-}
-
-long long prefill_grouped_items(int num_seqs, int num_kv_heads, int group, int max_query_len) {
-    const Plan pl = make_plan(num_seqs, num_kv_heads, group, max_query_len);
-    return pl.base * pl.splits;
-}
-
-size_t prefill_grouped_counters_bytes() { return (kCounters * 4 + 255) / 256 * 256; }
-
-cudaError_t launch_prefill_grouped(const GroupedArgs &args, int dtype, int head_dim, int num_sms,
-                                   cudaStream_t stream) {
+// The launch over a cache of 16 bits, or with kQ8 of 8.
+template <bool kQ8>
+cudaError_t launch_prefill_kind(const GroupedArgs &args, int dtype, int head_dim, int num_sms, cudaStream_t stream) {
     const bool bf16 = dtype == PA_DTYPE_BF16;
     const int Hk = args.num_kv_heads, Hq = args.num_q_heads, B = args.block_size, D = head_dim;
     PrefillGroupedArgs p;
@@ -1161,14 +1279,18 @@ cudaError_t launch_prefill_grouped(const GroupedArgs &args, int dtype, int head_
     const cuuint64_t kv_strides[3] = {static_cast<cuuint64_t>(D) * 2, 128, static_cast<cuuint64_t>(D) * 16};
     const cuuint32_t kv_box[4] = {64, 8, static_cast<cuuint32_t>(D / 64), static_cast<cuuint32_t>(B / 8)};
     if (!encode(&tm_q, bf16, args.q, 3, q_dims, q_strides, q_box) ||
-        !encode(&tm_out, bf16, args.out, 3, q_dims, q_strides, out_box) ||
-        !encode(&tm_k, bf16, args.k_cache, 4, kv_dims, kv_strides, kv_box) ||
+        !encode(&tm_out, bf16, args.out, 3, q_dims, q_strides, out_box))
+        return cudaErrorInvalidValue;
+    // (bytes of an 8-bit cache are fetched by untiled copies)
+    if constexpr (kQ8)
+        tm_k = tm_v = tm_q;
+    else if (!encode(&tm_k, bf16, args.k_cache, 4, kv_dims, kv_strides, kv_box) ||
         !encode(&tm_v, bf16, args.v_cache, 4, kv_dims, kv_strides, kv_box))
         return cudaErrorInvalidValue;
     const bool cap = args.softcap > 0.f, alibi = args.alibi_slopes != nullptr;
     const bool split = pl.splits > 1;
-    const Kernel kernel = split ? pick<true>(bf16, D, cap, alibi) : pick<false>(bf16, D, cap, alibi);
-    const int smem = D == 64 ? Cfg<64>::kSmemBytes : Cfg<128>::kSmemBytes;
+    const Kernel kernel = split ? pick<kQ8, true>(bf16, D, cap, alibi) : pick<kQ8, false>(bf16, D, cap, alibi);
+    const int smem = D == 64 ? Cfg<64, kQ8>::kSmemBytes : Cfg<128, kQ8>::kSmemBytes;
     // the kernel's shared-memory limit, once per device and variant
     int device = 0;
     cudaError_t e = cudaGetDevice(&device);
@@ -1199,5 +1321,34 @@ cudaError_t launch_prefill_grouped(const GroupedArgs &args, int dtype, int head_
     void *params[] = {&tm_q, &tm_k, &tm_v, &tm_out, &p};
     return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void *>(kernel), params);
 }
+
+}  // namespace
+
+#ifndef PA_Q8_LAUNCHES   // pa_prefill_q8.cu takes the kernel alone
+
+bool prefill_grouped_supported(int dtype, int head_dim, int block_size, int group) {
+    return decode_variant_supported(dtype, head_dim, block_size) && head_dim != 256 && group <= kBM;
+}
+
+size_t prefill_grouped_workspace_bytes(int num_seqs, int num_kv_heads, int group, int head_dim,
+                                       int max_query_len) {
+    const Plan pl = make_plan(num_seqs, num_kv_heads, group, max_query_len);
+    if (pl.splits <= 1) return 0;
+    return static_cast<size_t>(pl.base) * pl.splits * 2 * (head_dim + 2) * kBM * sizeof(float);
+}
+
+long long prefill_grouped_items(int num_seqs, int num_kv_heads, int group, int max_query_len) {
+    const Plan pl = make_plan(num_seqs, num_kv_heads, group, max_query_len);
+    return pl.base * pl.splits;
+}
+
+size_t prefill_grouped_counters_bytes() { return (kCounters * 4 + 255) / 256 * 256; }
+
+cudaError_t launch_prefill_grouped(const GroupedArgs &args, int dtype, int head_dim, int num_sms,
+                                   cudaStream_t stream) {
+    return launch_prefill_kind<false>(args, dtype, head_dim, num_sms, stream);
+}
+
+#endif  // PA_Q8_LAUNCHES
 
 }  // namespace pa

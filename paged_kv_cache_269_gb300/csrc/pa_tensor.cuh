@@ -248,4 +248,15 @@ inline bool encode(CUtensorMap *tm, bool bf16, const void *base, int rank, const
            CUDA_SUCCESS;
 }
 
+// A map of bytes, rows of `line` (64 or 128) in the swizzle of that many bytes.
+inline bool encode_bytes(CUtensorMap *tm, const void *base, int rank, const cuuint64_t *dims,
+                         const cuuint64_t *strides, const cuuint32_t *box, int line) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint32_t elem[5] = {1, 1, 1, 1, 1};
+    return fn(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void *>(base), dims, strides, box, elem,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, line == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace pa

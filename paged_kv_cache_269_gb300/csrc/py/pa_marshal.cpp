@@ -1,5 +1,6 @@
-// pa_marshal.cpp -- the calls of rope_and_cache, decode_grouped and
-// prefill_grouped from Python without the interpreter in between.
+// pa_marshal.cpp -- the calls of rope_and_cache, decode_grouped, prefill_grouped
+// and their forms over an 8-bit cache from Python without the interpreter in
+// between.
 //
 // A decode step's append and attention take a few microseconds on the GPU;
 // checking nine tensors in Python takes eight on the host.  These functions
@@ -39,14 +40,16 @@ struct Args {
     }
 };
 
-// The caches: [N, H, B, D] twice, of one 16-bit type.
-bool caches(Args &g, int i, pa_dims *d, at::ScalarType *type) {
+// The caches: [N, H, B, D] twice, of one 16-bit type, or with `like` of e4m3 beside
+// a tensor of a 16-bit type.
+bool caches(Args &g, int i, pa_dims *d, at::ScalarType *type, const Tensor *like = nullptr) {
     const Tensor *k = g.tensor(i);
     if (!k) return false;
-    *type = k->scalar_type();
+    *type = like ? like->scalar_type() : k->scalar_type();
     if (*type != at::kHalf && *type != at::kBFloat16) return false;
-    k = g.plain(i, *type, 4);
-    const Tensor *v = g.ok ? g.plain(i + 1, *type, 4) : nullptr;
+    const at::ScalarType stored = like ? at::kFloat8_e4m3fn : *type;
+    k = g.plain(i, stored, 4);
+    const Tensor *v = g.ok ? g.plain(i + 1, stored, 4) : nullptr;
     if (!v || k->sizes() != v->sizes()) return false;
     for (int j = 0; j < 4; ++j)
         if (k->size(j) <= 0 || k->size(j) > 0x7fffffff) return false;
@@ -57,6 +60,23 @@ bool caches(Args &g, int i, pa_dims *d, at::ScalarType *type) {
     d->head_dim = static_cast<int32_t>(k->size(3));
     d->dtype = *type == at::kBFloat16 ? PA_DTYPE_BF16 : PA_DTYPE_F16;
     return true;
+}
+
+// The scales of an 8-bit cache: fp32 [H] twice; null pointers where g.ok is false.
+struct Scales {
+    const float *k = nullptr, *v = nullptr;
+};
+Scales scales(Args &g, int i, int64_t H) {
+    Scales s;
+    const Tensor *k = g.plain(i, at::kFloat, 1);
+    const Tensor *v = g.ok ? g.plain(i + 1, at::kFloat, 1) : nullptr;
+    if (!v || k->size(0) != H || v->size(0) != H) {
+        g.ok = false;
+        return s;
+    }
+    s.k = static_cast<const float *>(k->data_ptr());
+    s.v = static_cast<const float *>(v->data_ptr());
+    return s;
 }
 
 // A [T, heads, D] tensor with adjacent heads; its elements between rows.
@@ -99,49 +119,133 @@ PyObject *take_over() {
     Py_RETURN_NONE;
 }
 
-// rope(q_out, q, k, v, k_cache, v_cache, positions, cos_sin, slot_mapping,
-//      interleaved, device, stream, fn) -> status or None
-PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    if (n != 13) return take_over();
-    Args g{a, static_cast<int>(integer(a[10]))};
+// What both appends share: q_out, q, k, v, k_cache, v_cache, positions, cos_sin,
+// slot_mapping, interleaved, device, stream.
+struct Append {
     pa_dims d;
-    at::ScalarType type;
-    if (!caches(g, 4, &d, &type)) return take_over();
-    const Tensor *q = g.tensor(1);
-    if (!q || q->dim() != 3) return take_over();
-    const int64_t T = q->size(0), Hq = q->size(1), H = d.num_heads, D = d.head_dim;
     int64_t qs, os, ks, vs;
-    q = rows(g, 1, type, T, Hq, D, &qs);
-    const Tensor *o = g.ok ? rows(g, 0, type, T, Hq, D, &os) : nullptr;
-    const Tensor *k = g.ok ? rows(g, 2, type, T, H, D, &ks) : nullptr;
-    const Tensor *v = g.ok ? rows(g, 3, type, T, H, D, &vs) : nullptr;
+    int32_t T, Hq, rotary, most;
+    int turn;
+    // taken before the interpreter is let go: asking for one may throw
+    void *out, *k_cache, *v_cache, *stream;
+    const void *q, *k, *v;
+    const int32_t *positions, *slots;
+    const float *table;
+};
+// q8: the caches are e4m3.
+bool append(Args &g, bool q8, Append *x) {
+    at::ScalarType type;
+    const Tensor *q = g.tensor(1);
+    if (!q || q->dim() != 3 || !caches(g, 4, &x->d, &type, q8 ? q : nullptr)) return false;
+    const int64_t T = q->size(0), Hq = q->size(1), H = x->d.num_heads, D = x->d.head_dim;
+    q = rows(g, 1, type, T, Hq, D, &x->qs);
+    const Tensor *o = g.ok ? rows(g, 0, type, T, Hq, D, &x->os) : nullptr;
+    const Tensor *k = g.ok ? rows(g, 2, type, T, H, D, &x->ks) : nullptr;
+    const Tensor *v = g.ok ? rows(g, 3, type, T, H, D, &x->vs) : nullptr;
     const Tensor *pos = g.ok ? g.plain(6, at::kInt, 1) : nullptr;
     const Tensor *cs = g.ok ? g.plain(7, at::kFloat, 2) : nullptr;
     const Tensor *slots = g.ok ? g.plain(8, at::kInt, 1) : nullptr;
     if (!g.ok || T <= 0 || T > 0x7fffffff || Hq <= 0 || Hq > 0x7fffffff || pos->size(0) != T ||
-        slots->size(0) != T || cs->size(0) > 0x7fffffff || cs->size(1) > 0x7fffffff ||
-        (T > 1 && os < Hq * D))
-        return take_over();
-    const bool in_place = o->data_ptr() == q->data_ptr() && (os == qs || T == 1);
-    if ((!in_place && overlap(o, os, Hq * D, q, qs, Hq * D, T)) || overlap(o, os, Hq * D, k, ks, H * D, T) ||
-        overlap(o, os, Hq * D, v, vs, H * D, T))
-        return take_over();
-    const int turn = PyObject_IsTrue(a[9]);
-    void *stream = pointer(a[11]);
+        slots->size(0) != T || cs->size(0) > 0x7fffffff || cs->size(1) > 0x7fffffff || cs->size(1) <= 0 ||
+        (T > 1 && x->os < Hq * D))
+        return false;
+    const bool in_place = o->data_ptr() == q->data_ptr() && (x->os == x->qs || T == 1);
+    if ((!in_place && overlap(o, x->os, Hq * D, q, x->qs, Hq * D, T)) ||
+        overlap(o, x->os, Hq * D, k, x->ks, H * D, T) || overlap(o, x->os, Hq * D, v, x->vs, H * D, T))
+        return false;
+    x->turn = PyObject_IsTrue(g.a[9]);
+    x->stream = pointer(g.a[11]);
+    if (PyErr_Occurred() || x->turn < 0) return false;
+    x->T = static_cast<int32_t>(T);
+    x->Hq = static_cast<int32_t>(Hq);
+    x->rotary = static_cast<int32_t>(cs->size(1));
+    x->most = static_cast<int32_t>(cs->size(0));
+    x->out = o->data_ptr();
+    x->k_cache = g.pointer(4);
+    x->v_cache = g.pointer(5);
+    x->q = q->data_ptr();
+    x->k = k->data_ptr();
+    x->v = v->data_ptr();
+    x->positions = static_cast<const int32_t *>(pos->data_ptr());
+    x->slots = static_cast<const int32_t *>(slots->data_ptr());
+    x->table = static_cast<const float *>(cs->data_ptr());
+    return true;
+}
+
+// rope(<append's 12>, fn) -> status or None
+PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    if (n != 13) return take_over();
+    Args g{a, static_cast<int>(integer(a[10]))};
+    Append x;
+    if (!append(g, false, &x)) return take_over();
     auto fn = reinterpret_cast<decltype(&pa_rope_and_cache)>(pointer(a[12]));
-    if (PyErr_Occurred() || turn < 0 || !fn) return take_over();
-    // every pointer before the interpreter is let go: asking for one may throw
-    void *const kp = g.pointer(4), *const vp = g.pointer(5);
-    void *const op = o->data_ptr();
-    const void *const qp = q->data_ptr(), *const k_new = k->data_ptr(), *const v_new = v->data_ptr();
-    const auto *positions = static_cast<const int32_t *>(pos->data_ptr());
-    const auto *table = static_cast<const float *>(cs->data_ptr());
-    const auto *slot = static_cast<const int32_t *>(slots->data_ptr());
-    const int32_t rotary = static_cast<int32_t>(cs->size(1)), most = static_cast<int32_t>(cs->size(0));
+    if (PyErr_Occurred() || !fn) return take_over();
     int rc;
     Py_BEGIN_ALLOW_THREADS;
-    rc = fn(op, qp, k_new, v_new, kp, vp, positions, table, slot, static_cast<int32_t>(T), static_cast<int32_t>(Hq), qs,
-            ks, vs, os, rotary, most, turn, &d, stream);
+    rc = fn(x.out, x.q, x.k, x.v, x.k_cache, x.v_cache, x.positions, x.table, x.slots, x.T, x.Hq, x.qs, x.ks, x.vs, x.os,
+            x.rotary, x.most, x.turn, &x.d, x.stream);
+    Py_END_ALLOW_THREADS;
+    return PyLong_FromLong(rc);
+}
+
+// norm_rope(<append's 12>, q_weight, k_weight, eps, k_scales, v_scales, fn) -> status or None
+PyObject *norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    if (n != 18) return take_over();
+    Args g{a, static_cast<int>(integer(a[10]))};
+    const bool q8 = a[15] != Py_None || a[16] != Py_None;
+    Append x;
+    if (!append(g, q8, &x)) return take_over();
+    pa_append_opts o{};
+    const float **weights[2] = {&o.q_weight, &o.k_weight};
+    for (int i = 0; i < 2; ++i) {
+        if (a[12 + i] == Py_None) continue;
+        const Tensor *t = g.plain(12 + i, at::kFloat, 1);
+        if (!t || t->size(0) != x.d.head_dim) return take_over();
+        *weights[i] = static_cast<const float *>(t->data_ptr());
+    }
+    o.eps = static_cast<float>(PyFloat_AsDouble(a[14]));
+    if (q8) {
+        const Scales s = scales(g, 15, x.d.num_heads);
+        o.k_scales = s.k;
+        o.v_scales = s.v;
+    }
+    auto fn = reinterpret_cast<decltype(&pa_norm_rope_and_cache)>(pointer(a[17]));
+    if (!g.ok || PyErr_Occurred() || !fn) return take_over();
+    int rc;
+    Py_BEGIN_ALLOW_THREADS;
+    rc = fn(x.out, x.q, x.k, x.v, x.k_cache, x.v_cache, x.positions, x.table, x.slots, x.T, x.Hq, x.qs, x.ks, x.vs, x.os,
+            x.rotary, x.most, x.turn, &x.d, &o, x.stream);
+    Py_END_ALLOW_THREADS;
+    return PyLong_FromLong(rc);
+}
+
+// gather_q8(k_out, v_out, k_cache, v_cache, k_scales, v_scales, slots, device, stream, fn) -> status or None
+PyObject *gather_q8(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    if (n != 10) return take_over();
+    Args g{a, static_cast<int>(integer(a[7]))};
+    pa_dims d;
+    at::ScalarType type;
+    const Tensor *ko = g.tensor(0);
+    if (!ko || !caches(g, 2, &d, &type, ko)) return take_over();
+    ko = g.plain(0, type, 3);
+    const Tensor *vo = g.ok ? g.plain(1, type, 3) : nullptr;
+    const Tensor *slots = g.ok ? g.plain(6, at::kInt, 1) : nullptr;
+    if (!slots) return take_over();
+    const int64_t T = slots->size(0), bytes = T * d.num_heads * d.head_dim * 2;
+    if (T <= 0 || T > 0x7fffffff || ko->sizes() != vo->sizes() || ko->size(0) != T || ko->size(1) != d.num_heads ||
+        ko->size(2) != d.head_dim)
+        return take_over();
+    const Scales s = scales(g, 4, d.num_heads);
+    void *const kp = ko->data_ptr(), *const vp = vo->data_ptr();
+    const int64_t apart = reinterpret_cast<int64_t>(kp) - reinterpret_cast<int64_t>(vp);
+    void *stream = pointer(a[8]);
+    auto fn = reinterpret_cast<decltype(&pa_gather_cache_q8)>(pointer(a[9]));
+    if (!g.ok || PyErr_Occurred() || !fn || (apart < bytes && -apart < bytes)) return take_over();
+    const void *const kc = g.pointer(2), *const vc = g.pointer(3);
+    const auto *at = static_cast<const int32_t *>(slots->data_ptr());
+    int rc;
+    Py_BEGIN_ALLOW_THREADS;
+    rc = fn(kp, vp, kc, vc, s.k, s.v, at, static_cast<int32_t>(T), &d, stream);
     Py_END_ALLOW_THREADS;
     return PyLong_FromLong(rc);
 }
@@ -150,6 +254,7 @@ PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
 struct Attention {
     pa_dims d;
     at::ScalarType type;
+    Scales scales;
     pa_attn_opts opts;
     const Tensor *out, *q, *tables, *lens, *counters, *workspace;
     int64_t S, Hq, MB;
@@ -162,10 +267,16 @@ struct Attention {
     uint32_t *counters_p;
 };
 // args: out, q, k_cache, v_cache, tables, lens, scale, softcap, slopes, window,
-// prefix, counters, workspace, device, stream
-bool attention(Args &g, Attention *x) {
+// prefix, counters, workspace, device, stream, and over an 8-bit cache (q8)
+// k_scales, v_scales
+bool attention(Args &g, Attention *x, bool q8) {
     PyObject *const *a = g.a;
-    if (!caches(g, 2, &x->d, &x->type)) return false;
+    const Tensor *like = q8 ? g.tensor(1) : nullptr;
+    if ((q8 && !like) || !caches(g, 2, &x->d, &x->type, like)) return false;
+    if (q8) {
+        x->scales = scales(g, 15, x->d.num_heads);
+        if (!g.ok) return false;
+    }
     x->q = g.plain(1, x->type, 3);
     x->out = g.ok ? g.plain(0, x->type, 3) : nullptr;
     x->tables = g.ok ? g.plain(4, at::kInt, 2) : nullptr;
@@ -213,51 +324,67 @@ bool attention(Args &g, Attention *x) {
     return true;
 }
 
-// decode(<attention's 15>, fn, workspace_fn, counters_fn) -> status or None
+// decode(<attention's 15, or 17>, fn, workspace_fn, counters_fn) -> status or None
+template <bool kQ8>
 PyObject *decode(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    if (n != 18) return take_over();
+    constexpr int at = kQ8 ? 17 : 15;
+    if (n != at + 3) return take_over();
     Args g{a, static_cast<int>(integer(a[13]))};
     Attention x;
-    if (!attention(g, &x) || x.q->size(0) != x.S) return take_over();
-    auto fn = reinterpret_cast<decltype(&pa_decode_grouped)>(pointer(a[15]));
-    auto ws = reinterpret_cast<decltype(&pa_decode_grouped_workspace_bytes)>(pointer(a[16]));
-    auto ct = reinterpret_cast<decltype(&pa_decode_grouped_counters_bytes)>(pointer(a[17]));
-    const int32_t Hq = static_cast<int32_t>(x.Hq);
+    if (!attention(g, &x, kQ8) || x.q->size(0) != x.S) return take_over();
+    void *const fn = pointer(a[at]);
+    auto ws = reinterpret_cast<decltype(&pa_decode_grouped_workspace_bytes)>(pointer(a[at + 1]));
+    auto ct = reinterpret_cast<decltype(&pa_decode_grouped_counters_bytes)>(pointer(a[at + 2]));
+    const int32_t Hq = static_cast<int32_t>(x.Hq), MB = static_cast<int32_t>(x.MB);
     const size_t need_ct = ct(&x.d, Hq), have_ct = x.counters->numel() * 4, have_ws = x.workspace->numel();
     if (need_ct == 0 || have_ct < need_ct || have_ws < ws(&x.d, Hq)) return take_over();
     int rc;
     Py_BEGIN_ALLOW_THREADS;
-    rc = fn(x.out_p, x.q_p, x.k_p, x.v_p, x.tables_p, x.lens_p, x.scale, static_cast<int32_t>(x.MB), &x.d, Hq, &x.opts,
+    if constexpr (kQ8)
+        rc = reinterpret_cast<decltype(&pa_decode_grouped_q8)>(fn)(
+            x.out_p, x.q_p, x.k_p, x.v_p, x.scales.k, x.scales.v, x.tables_p, x.lens_p, x.scale, MB, &x.d, Hq, &x.opts,
             x.workspace_p, have_ws, x.counters_p, have_ct, x.stream);
+    else
+        rc = reinterpret_cast<decltype(&pa_decode_grouped)>(fn)(
+            x.out_p, x.q_p, x.k_p, x.v_p, x.tables_p, x.lens_p, x.scale, MB, &x.d, Hq, &x.opts, x.workspace_p, have_ws,
+            x.counters_p, have_ct, x.stream);
     Py_END_ALLOW_THREADS;
     return PyLong_FromLong(rc);
 }
 
-// prefill(<attention's 15>, query_start, max_query_len, fn, workspace_fn,
+// prefill(<attention's 15, or 17>, query_start, max_query_len, fn, workspace_fn,
 //         counters_fn) -> status or None
+template <bool kQ8>
 PyObject *prefill(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    if (n != 20) return take_over();
+    constexpr int at = kQ8 ? 17 : 15;
+    if (n != at + 5) return take_over();
     Args g{a, static_cast<int>(integer(a[13]))};
     Attention x;
-    if (!attention(g, &x)) return take_over();
-    const Tensor *starts = g.plain(15, at::kInt, 1);
-    const long most = PyLong_AsLong(a[16]);
+    if (!attention(g, &x, kQ8)) return take_over();
+    const Tensor *starts = g.plain(at, at::kInt, 1);
+    const long most = PyLong_AsLong(a[at + 1]);
     const int64_t total = x.q->size(0);
     if (!starts || PyErr_Occurred() || most <= 0 || most > 0x7fffffff || starts->size(0) != x.S + 1 || total <= 0 ||
         total > 0x7fffffff)
         return take_over();
-    auto fn = reinterpret_cast<decltype(&pa_prefill_grouped)>(pointer(a[17]));
-    auto ws = reinterpret_cast<decltype(&pa_prefill_grouped_workspace_bytes)>(pointer(a[18]));
-    auto ct = reinterpret_cast<decltype(&pa_prefill_grouped_counters_bytes)>(pointer(a[19]));
-    const int32_t Hq = static_cast<int32_t>(x.Hq);
+    void *const fn = pointer(a[at + 2]);
+    auto ws = reinterpret_cast<decltype(&pa_prefill_grouped_workspace_bytes)>(pointer(a[at + 3]));
+    auto ct = reinterpret_cast<decltype(&pa_prefill_grouped_counters_bytes)>(pointer(a[at + 4]));
+    const int32_t Hq = static_cast<int32_t>(x.Hq), MB = static_cast<int32_t>(x.MB);
+    const int32_t rows = static_cast<int32_t>(total), longest = static_cast<int32_t>(most);
     const size_t need_ct = ct(&x.d, Hq), have_ct = x.counters->numel() * 4, have_ws = x.workspace->numel();
-    if (need_ct == 0 || have_ct < need_ct || have_ws < ws(&x.d, Hq, static_cast<int32_t>(most))) return take_over();
+    if (need_ct == 0 || have_ct < need_ct || have_ws < ws(&x.d, Hq, longest)) return take_over();
     const auto *starts_p = static_cast<const int32_t *>(starts->data_ptr());
     int rc;
     Py_BEGIN_ALLOW_THREADS;
-    rc = fn(x.out_p, x.q_p, x.k_p, x.v_p, x.tables_p, x.lens_p, starts_p, static_cast<int32_t>(total),
-            static_cast<int32_t>(most), x.scale, static_cast<int32_t>(x.MB), &x.d, Hq, &x.opts, x.workspace_p, have_ws,
-            x.counters_p, have_ct, x.stream);
+    if constexpr (kQ8)
+        rc = reinterpret_cast<decltype(&pa_prefill_grouped_q8)>(fn)(
+            x.out_p, x.q_p, x.k_p, x.v_p, x.scales.k, x.scales.v, x.tables_p, x.lens_p, starts_p, rows, longest, x.scale,
+            MB, &x.d, Hq, &x.opts, x.workspace_p, have_ws, x.counters_p, have_ct, x.stream);
+    else
+        rc = reinterpret_cast<decltype(&pa_prefill_grouped)>(fn)(
+            x.out_p, x.q_p, x.k_p, x.v_p, x.tables_p, x.lens_p, starts_p, rows, longest, x.scale, MB, &x.d, Hq, &x.opts,
+            x.workspace_p, have_ws, x.counters_p, have_ct, x.stream);
     Py_END_ALLOW_THREADS;
     return PyLong_FromLong(rc);
 }
@@ -277,7 +404,13 @@ constexpr PyMethodDef method(const char *name) {
     return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(&guarded<f>)), METH_FASTCALL, nullptr};
 }
 
-PyMethodDef methods[] = {method<rope>("rope"), method<decode>("decode"), method<prefill>("prefill"),
+PyMethodDef methods[] = {method<rope>("rope"),
+                         method<decode<false>>("decode"),
+                         method<prefill<false>>("prefill"),
+                         method<norm_rope>("norm_rope"),
+                         method<gather_q8>("gather_q8"),
+                         method<decode<true>>("decode_q8"),
+                         method<prefill<true>>("prefill_q8"),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "pa_marshal", nullptr, -1, methods};
 

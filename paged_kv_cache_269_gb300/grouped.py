@@ -50,7 +50,9 @@ def _init():
             l = package.lib()
             for name in ("pa_rope_and_cache", "pa_decode_grouped", "pa_decode_grouped_workspace_bytes",
                          "pa_decode_grouped_counters_bytes", "pa_prefill_grouped",
-                         "pa_prefill_grouped_workspace_bytes", "pa_prefill_grouped_counters_bytes"):
+                         "pa_prefill_grouped_workspace_bytes", "pa_prefill_grouped_counters_bytes",
+                         "pa_norm_rope_and_cache", "pa_gather_cache_q8", "pa_decode_grouped_q8",
+                         "pa_prefill_grouped_q8"):
                 _addresses[name] = ctypes.cast(getattr(l, name), ctypes.c_void_p).value
             try:
                 _marshal = _load_marshal(package._build.build_marshal())
@@ -340,8 +342,9 @@ def reset_counters():
 
 
 def _attention_args(what, out, q, k_cache, v_cache, block_tables, context_lens, softcap,
-                    alibi_slopes, window, prefix_lens):
-    index, dev, code, et, (N, H, B, D) = _caches(k_cache, v_cache)
+                    alibi_slopes, window, prefix_lens, caches=None):
+    """caches: what _caches returns, of caches that are checked already."""
+    index, dev, code, et, (N, H, B, D) = caches or _caches(k_cache, v_cache)
     q_p = _plain(q, "q", et, 3, index, dev)
     o_p = _plain(out, "out", et, 3, index, dev)
     t_p = _plain(block_tables, "block_tables", _I32, 2, index, dev)
