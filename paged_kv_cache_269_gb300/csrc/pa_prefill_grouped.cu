@@ -182,7 +182,9 @@ struct Cfg {
     static constexpr int K_EMPTY = V_FULL + kSlots, V_EMPTY = K_EMPTY + kSlots;
     // 8-bit caches: a tile's bytes are there (K, then V), to be widened
     static constexpr int K_BYTES = V_EMPTY + kSlots, V_BYTES = K_BYTES + (kQ8 ? kSlots : 0);
-    static constexpr int kNumBars = V_BYTES + (kQ8 ? kSlots : 0);
+    // a bf16 Q is there as fp16: [item parity][tile]
+    static constexpr int Q_READY = V_BYTES + (kQ8 ? kSlots : 0);
+    static constexpr int kNumBars = Q_READY + (kQ8 ? 4 : 0);
     static constexpr int OFF_TMEM = OFF_BAR + kNumBars * 8;
     static constexpr int OFF_FLAG = OFF_TMEM + 4;
     static constexpr int OFF_LAST = OFF_FLAG + 4;                   // int[2]
@@ -349,7 +351,7 @@ struct KeyBlocks {
 // row of each and not the same half, so that neither the loads nor the stores (every
 // other 16-byte chunk of a line, even ones of one key and odd ones of the next) meet
 // in a bank.
-template <bool kBf16, int D, typename Valid>
+template <int D, typename Valid>
 __device__ __forceinline__ void widen_tile(uint8_t *slot, int lane, Valid &&valid) {
     constexpr int kGroup = D * 16, kIn = D * 8, kPer = D / 64;   // bytes out and in a group; chunks a lane
     const uint8_t *in = slot + kBN * D;
@@ -378,13 +380,6 @@ __device__ __forceinline__ void widen_tile(uint8_t *slot, int lane, Valid &&vali
                 o[2 * i] = e4m3x2_to_f16x2(w[i]);
                 o[2 * i + 1] = e4m3x2_to_f16x2_high(w[i]);
             }
-            if constexpr (kBf16) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&o[i]));
-                    o[i] = pack_pair<true>(f.x, f.y);
-                }
-            }
             const int c = chunk_of(u), c16 = 2 * (c & 3);
             uint8_t *line = slot + g * kGroup + (c >> 2) * 1024 + y * 128;
             *reinterpret_cast<uint4 *>(line + ((c16 ^ y) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
@@ -405,6 +400,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                            const __grid_constant__ CUtensorMap tm_out,
                            const __grid_constant__ PrefillGroupedArgs p) {
     using C = Cfg<D, kQ8>;
+    // over an 8-bit cache the products are fp16's whatever the type outside is
+    constexpr bool kMmaBf16 = kBf16 && !kQ8, kScaleQ = kBf16 && kQ8;
     const GroupedArgs &a = p.g;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -422,7 +419,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kNumBars; ++i) {
             uint32_t count = 1;
-            if ((i >= C::P_FULL && i < C::P_FULL + 6) || i == C::PARTS || i == C::PARTS + 1)
+            if ((i >= C::P_FULL && i < C::P_FULL + 6) || i == C::PARTS || i == C::PARTS + 1 ||
+                (kQ8 && i >= C::Q_READY))
                 count = 4;                                    // softmax warps
             if (i == C::ITEM_EMPTY || i == C::ITEM_EMPTY + 1) count = kQ8 ? 15 : 13;     // 4 MMA threads, 8 softmax warps, V, 2 that widen
             if (i >= C::K_EMPTY && i < C::V_EMPTY + C::kSlots) count = 2;               // both tiles' threads
@@ -641,14 +639,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!ok) break;
                         uint8_t *tile = slots + st * C::kTileKV;
                         if (is_k) {
-                            widen_tile<kBf16, D>(tile, lane, [](int) { return true; });
+                            widen_tile<D>(tile, lane, [](int) { return true; });
                         } else {
                             const uint32_t rows = v_rows[st];
                             const int tail = static_cast<int>(rows >> 16);
                             if (tail == kBN && (rows & 0xffffu) == (1u << (kBN >> b_shift)) - 1)
-                                widen_tile<kBf16, D>(tile, lane, [](int) { return true; });
+                                widen_tile<D>(tile, lane, [](int) { return true; });
                             else
-                                widen_tile<kBf16, D>(tile, lane, [&](int r) {
+                                widen_tile<D>(tile, lane, [&](int r) {
                                     return r < tail && ((rows >> (r >> b_shift)) & 1);
                                 });
                         }
@@ -664,8 +662,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (elect_one()) {
                 const bool is_s = warp < kPvWarp0;
                 const int t = warp - (is_s ? kSWarp0 : kPvWarp0);
-                constexpr uint32_t idesc_s = instr_desc(kBf16, false, kBN);
-                constexpr uint32_t idesc_pv = instr_desc(kBf16, true, D);
+                constexpr uint32_t idesc_s = instr_desc(kMmaBf16, false, kBN);
+                constexpr uint32_t idesc_pv = instr_desc(kMmaBf16, true, D);
                 const uint32_t kv_addr = smem_addr(smem + (is_s ? C::OFF_K : C::OFF_V));
                 uint64_t *kv_full = &bar[is_s ? C::K_FULL : C::V_FULL], *kv_empty = &bar[is_s ? C::K_EMPTY : C::V_EMPTY];
                 const uint32_t tm_s = tmem + t * C::kBufs * 64, tm_o = tmem + C::TM_O + t * D;
@@ -682,7 +680,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive(&bar[C::ITEM_EMPTY + slot]);
                     if (done) break;
                     if (is_s) {
-                        ok = mbar_wait(&bar[C::Q_FULL + slot], (k / 2) & 1, abort_flag, a.err);
+                        ok = mbar_wait(&bar[kScaleQ ? C::Q_READY + slot * 2 + t : C::Q_FULL + slot], (k / 2) & 1,
+                                       abort_flag, a.err);
                         if (!ok) break;
                     }
                     const uint32_t q_addr = smem_addr(smem + C::OFF_Q) + (slot * 2 + t) * C::kTileQ;
@@ -759,9 +758,55 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             pending = -1;
         };
+        // Item k's Q, where it has to be made fp16: each row by a power of two that brings
+        // its largest element to [2^10, 2^11), since bf16's exponents do not fit and its 8
+        // bits do.  A thread takes its own row, while the item before waits for its last
+        // product.  Returns what the row's scores are short of.
+        float q_factor = 1.f;
+        auto ready_q = [&](int k) {
+            const int slot = k % 2;
+            if (!warp_all(mbar_wait(&bar[C::ITEM_FULL + slot], (k / 2) & 1, abort_flag, a.err))) return false;
+            const volatile Item *it = items + slot;
+            if (it->done) return true;
+            if ((t == 0 ? it->nk0 : it->nk1) >= 0) {
+                if (!warp_all(mbar_wait(&bar[C::Q_FULL + slot], (k / 2) & 1, abort_flag, a.err))) return false;
+                uint8_t *row = smem + C::OFF_Q + (slot * 2 + t) * C::kTileQ + r * 128;
+                auto chunk = [&](int i) {
+                    return reinterpret_cast<uint4 *>(row + i / 8 * C::kHalfQ + (((i & 7) ^ (r & 7)) << 4));
+                };
+                __nv_bfloat162 most = __floats2bfloat162_rn(0.f, 0.f);
+#pragma unroll 4
+                for (int i = 0; i < D / 8; ++i) {
+                    const uint4 v = *chunk(i);
+                    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int z = 0; z < 4; ++z)
+                        most = __hmax2(most, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&u[z])));
+                }
+                const float top = fmaxf(__low2float(most), __high2float(most));
+                const int e = max(static_cast<int>(__float_as_uint(top) >> 23) - 137, -100);
+                const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+                q_factor = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+#pragma unroll 4
+                for (int i = 0; i < D / 8; ++i) {
+                    const uint4 v = *chunk(i);
+                    uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int z = 0; z < 4; ++z)
+                        u[z] = pack_pair<false>(__uint_as_float(u[z] << 16) * down,
+                                                __uint_as_float(u[z] & 0xFFFF0000u) * down);
+                    *chunk(i) = make_uint4(u[0], u[1], u[2], u[3]);
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[C::Q_READY + slot * 2 + t]);
+            return true;
+        };
         uint32_t n = 0;            // S tiles consumed
         uint32_t tiles = 0;        // key tiles of all items (mask ring)
         bool ok = true;
+        if constexpr (kScaleQ) ok = ready_q(0);
         for (int k = 0; ok; ++k) {
             const int slot = k % 2;
             ok = warp_all(mbar_wait(&bar[C::ITEM_FULL + slot], (k / 2) & 1, abort_flag, a.err));
@@ -781,6 +826,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (nk < 0) {
                 release();
                 pending = slot;
+                if constexpr (kScaleQ) ok = ready_q(k + 1);
                 continue;
             }
             // The row's position.  A row without a query stands where the warp's last
@@ -796,7 +842,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int pre_all = it->pre, na = it->na, skip = it->skip, j0 = it->j0;
             const int last = j0 + max(nk, 0) - 1;
             if constexpr (kQ8) {
-                const float f = __ldg(a.k_scales + it->hk);
+                const float f = __ldg(a.k_scales + it->hk) * (kScaleQ ? q_factor : 1.f);
                 c = p.scale_log2 * f;
                 if constexpr (kCap) {
                     cap_v = p.cap_v * f;
@@ -864,7 +910,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // visible key is ahead of the row).
                 bool done_fast = false;
                 const bool fast = (!kAlibi || pre_all <= k0 || k0 + kBN - 1 <= wmin) && warp_all(m != -INFINITY) &&
-                                  (!kCap || a.softcap <= kShareCap<kBf16>);
+                                  (!kCap || a.softcap <= kShareCap<kMmaBf16>);
                 uint32_t any = 0;
                 auto weights = [&](auto masked) {
                     uint32_t vis[kBN / 32];
@@ -919,7 +965,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         y0 = fast_exp2(y0);
                         y1 = fast_exp2(y1);
                         add2(sums[e & 2], sums[(e & 2) + 1], sums[e & 2], sums[(e & 2) + 1], y0, y1);
-                        w[e / 2] = pack_pair<kBf16>(y0, y1);
+                        w[e / 2] = pack_pair<kMmaBf16>(y0, y1);
                     }
                     sum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
                 };
@@ -932,7 +978,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         weights(std::integral_constant<int, 2>{});
                     // the sum bounds every weight; v^2 < 2
                     // that the polynomial holds (no bit pattern reaches that of 2)
-                    done_fast = warp_all((sum <= kMostSum<kBf16> && any < 0x40000000u) || !live);
+                    done_fast = warp_all((sum <= kMostSum<kMmaBf16> && any < 0x40000000u) || !live);
                     if (!kCap && !done_fast) load_raw();
                 }
                 if (!done_fast) {
@@ -1022,7 +1068,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int e = 0; e < kBN; e += 2) {
                         const float y0 = fast_exp2(x[e] + bias), y1 = fast_exp2(x[e + 1] + bias);
                         add2(sums[0], sums[1], sums[0], sums[1], y0, y1);
-                        w[e / 2] = pack_pair<kBf16>(y0, y1);
+                        w[e / 2] = pack_pair<kMmaBf16>(y0, y1);
                     }
                     sum = sums[0] + sums[1];
                 }
@@ -1035,6 +1081,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (j == 0) release();
             }
             if (!ok) break;
+            if constexpr (kScaleQ) {
+                release();         // (an item without key tiles)
+                ok = ready_q(k + 1);
+                if (!ok) break;
+            }
             if (nk > 0) {
                 ok = warp_all(mbar_wait(&bar[C::PV_DONE + t * 3 + (n - 1) % C::kBufs], ((n - 1) / C::kBufs) & 1, abort_flag,
                                         a.err));
