@@ -41,6 +41,8 @@ int check_scores(float scale, const pa_attn_opts *o) {
     return PA_OK;
 }
 
+int block_shift(const pa_dims *dims) { return dims->block_size == 8 ? 3 : (dims->block_size == 16 ? 4 : 5); }
+
 // Products that the kernels hold in 32 bits (positions and counts of
 // sequences with room for a tile past the end).
 int check_ranges(const pa_dims *dims, int32_t num_q_heads, int32_t max_blocks_per_seq) {
@@ -364,12 +366,11 @@ int pa_norm_rope_and_cache(void *q_out, const void *q, const void *k, const void
     a.num_q_heads = num_q_heads;
     a.num_kv_heads = dims->num_heads;
     a.head_dim = D;
-    a.block_size = dims->block_size;
+    a.block_shift = block_shift(dims);
     a.rotary_dim = rotary_dim;
     // without a rotation no position is too far
     a.max_positions = rotary_dim > 0 ? max_positions : 0x7fffffff;
     a.eps = o.eps;
-    a.inv_dim = 1.f / D;
     a.pool_slots = slots;
     return finish(launch_norm_rope(a, dims->dtype, interleaved != 0, sms, static_cast<cudaStream_t>(stream)));
 }
@@ -400,8 +401,9 @@ int pa_gather_cache_q8(void *k_out, void *v_out, const void *k_cache, const void
     a.num_tokens = num_tokens;
     a.num_kv_heads = dims->num_heads;
     a.head_dim = dims->head_dim;
-    a.block_size = dims->block_size;
+    a.block_shift = block_shift(dims);
     a.pool_slots = pool;
+    a.wide_stores = aligned(k_out, 32) && aligned(v_out, 32);
     return finish(launch_gather_q8(a, dims->dtype, static_cast<cudaStream_t>(stream)));
 }
 

@@ -129,12 +129,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     return r;
 }
 
-__device__ __forceinline__ float fast_rcp(float x) {   // 1 ulp; 1 / inf = 0
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // Two weights as packed 16-bit values, and the packed remainders.
 template <bool kBf16>
 __device__ __forceinline__ void split_pair(float a, float b, uint32_t &hi, uint32_t &lo) {
@@ -278,6 +272,12 @@ struct Cfg {
     static constexpr int kCtasPerSm = 2 * (kBytes + 1024) <= 233472 ? 2 : 1;
 };
 
+// The K/V head of a unit (a division by a number that is 1 up to 8 or 16 query heads a
+// K/V head would be 25 instructions of every tile).
+__device__ __forceinline__ int head_of(const DecodeGroupedArgs &p, int unit) {
+    return p.chunks == 1 ? unit : unit / p.chunks;
+}
+
 // Takes the ticket of a partial that the CTA left (one warp; the partial's
 // writes happen before the call at CTA scope): whether it was the unit's last.
 __device__ __forceinline__ bool take_ticket(const DecodeGroupedArgs &p, int s, int units, int unit,
@@ -298,7 +298,7 @@ __device__ __forceinline__ void join_unit(const DecodeGroupedArgs &p, int s, int
                                           int tid, int n) {
     constexpr int kVec = D / 4;
     const GroupedArgs &a = p.g;
-    const int hk = unit / p.chunks, h0 = (unit % p.chunks) * kHeads;
+    const int hk = head_of(p, unit), h0 = (unit - hk * p.chunks) * kHeads;
     const int heads = min(kHeads, p.group - h0);
     // slot of piece i: 2 i + 1 for the one the unit starts in, else 2 i
     auto part = [&](int i) {
@@ -508,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // i, its table entry and its two copies.
     const int B = a.block_size;
     const int RB = kQ8 ? min(B, TK) : (B == 8 ? 8 : 16);
-    const int rb_shift = RB == 8 ? 3 : (RB == 16 ? 4 : 5);
+    const int rb_shift = RB == 8 ? 3 : (RB == 16 ? 4 : 5), b_shift = B == 8 ? 3 : (B == 16 ? 4 : 5);
     const int boxes = TK / RB;
     Cursor<TK, kCost> prod = cons;
     int at = 0;                              // tile of the piece `prod` is at
@@ -528,9 +528,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int i = prod.idx;
             const int k = TK * (i < prod.g.na ? i : i + prod.g.skip) + lane * RB;
             if (k < prod.g.ctx && (k < prod.g.pre || k + RB > prod.g.lo)) {
-                const int e = __ldg(a.block_tables + static_cast<size_t>(prod.s) * a.max_blocks_per_seq + k / B);
+                const int e = __ldg(a.block_tables + static_cast<size_t>(prod.s) * a.max_blocks_per_seq + (k >> b_shift));
                 box_blk = static_cast<unsigned>(e) < static_cast<unsigned>(a.num_blocks) ? e : -2;
-                box_row = k % B;
+                box_row = k & (B - 1);
             }
         }
     };
@@ -544,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         if (blk >= 0) {
-            const int y = (blk * a.num_kv_heads + unit / p.chunks) * B + box_y;
+            const int y = (blk * a.num_kv_heads + head_of(p, unit)) * B + box_y;
             uint8_t *dst = ring + stage * C::kStage + lane * (RB * D * C::kElem);
             tma_load_3d(dst, &tm_k, 0, y, 0, &bar[stage]);
             tma_load_3d(dst + C::kMat, &tm_v, 0, y, 0, &bar[stage]);
@@ -600,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int seg_start = 0;                       // CTA tile at which the segment starts
 
     auto load_q = [&]() {
-        const int hk = cons.unit / p.chunks, h0 = (cons.unit % p.chunks) * kHeads;
+        const int hk = head_of(p, cons.unit), h0 = (cons.unit - hk * p.chunks) * kHeads;
         const uint32_t *src = reinterpret_cast<const uint32_t *>(
             a.q + (static_cast<size_t>(cons.s) * a.num_q_heads + hk * p.group) * D);
 #pragma unroll
@@ -943,7 +943,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
         // ------------------------------------------------ end of the segment
         const int s = cons.s, unit = cons.unit;
-        const int hk = unit / p.chunks, h0 = (unit % p.chunks) * kHeads;
+        const int hk = head_of(p, unit), h0 = (unit - hk * p.chunks) * kHeads;
         const int heads = min(kHeads, p.group - h0);
         // the unit's place on the line, and whether this piece covers it whole
         const bool from_start = idx0 == 0, to_end = idx0 + seg_len >= g.nt;

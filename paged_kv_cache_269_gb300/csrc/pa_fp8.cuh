@@ -8,6 +8,8 @@
 #include <cuda_fp16.h>
 #include <stdint.h>
 
+#include "pa_tensor.cuh"
+
 namespace pa {
 
 // The two e4m3 numbers in the low half of `v` as a packed pair of fp16.
@@ -29,13 +31,26 @@ __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float a, float b) {
     return r;
 }
 
-// x / scale to nearest (x * inv with one correction by the remainder), where it
-// can be held; inv = 1 / scale.  Values past the type's range are left as they
-// come: they saturate, infinities among them, and their remainder says nothing.  (The
-// correction adds +0 to a quotient of -0, whose sign is put back.)
-__device__ __forceinline__ float divide_by_scale(float x, float scale, float inv) {
-    const float q = x * inv;
-    return fabsf(q) < 449.f ? copysignf(fmaf(fmaf(-q, scale, x), inv, q), q) : q;
+// 1 / x to one step; 1 / inf = 0.
+__device__ __forceinline__ float fast_rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// The e4m3 numbers of a pair's x / scale, x saturated at the type's range (NaN stays
+// NaN): x * inv with one correction by the remainder, which leaves the quotient fp32's
+// nearest.  minus: -scale twice; inv: 1 / scale, to a step, twice.  (The correction adds
+// +0 to a quotient of -0, whose sign is put back.)
+__device__ __forceinline__ uint32_t quantise_pair(uint64_t x, uint64_t minus, uint64_t inv) {
+    uint64_t q = mul_pair(x, inv);
+    float a, b, a1, b1;
+    split_pair(q, a, b);
+    split_pair(fma_pair(fma_pair(q, minus, x), inv, q), a1, b1);
+    // past the range the remainder says nothing (it may be of an infinity)
+    a1 = fabsf(a) < 449.f ? copysignf(a1, a) : a;
+    b1 = fabsf(b) < 449.f ? copysignf(b1, b) : b;
+    return f32x2_to_e4m3x2(a1, b1);
 }
 
 }  // namespace pa

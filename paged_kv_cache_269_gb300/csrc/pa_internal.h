@@ -219,9 +219,10 @@ struct AppendArgs {
     const float *q_weight, *k_weight;   // [D], or nullptr: no norm
     const float *k_scales, *v_scales;   // [Hkv], or nullptr
     long long q_stride, k_stride, v_stride, q_out_stride;   // elements between tokens
-    int32_t num_tokens, num_q_heads, num_kv_heads, head_dim, block_size;
+    int32_t num_tokens, num_q_heads, num_kv_heads, head_dim;
+    int32_t block_shift;           // blocks of 2^block_shift tokens
     int32_t rotary_dim, max_positions;
-    float eps, inv_dim;            // inv_dim: 1 / D
+    float eps;
     long long pool_slots;          // N * B
     unsigned int *err;
 };
@@ -233,7 +234,9 @@ struct GatherArgs {
     const uint8_t *k_cache, *v_cache;   // e4m3 [N, Hkv, B, D]
     const float *k_scales, *v_scales;   // [Hkv]
     const int32_t *slots;          // [T]
-    int32_t num_tokens, num_kv_heads, head_dim, block_size;
+    int32_t num_tokens, num_kv_heads, head_dim;
+    int32_t block_shift;           // blocks of 2^block_shift tokens
+    int32_t wide_stores;           // the outputs are 32-byte aligned
     long long pool_slots;          // N * B
     unsigned int *err;
 };

@@ -221,11 +221,6 @@ __device__ __forceinline__ uint32_t pack_pair(float a, float b) {
         return *reinterpret_cast<const uint32_t *>(&h);
     }
 }
-__device__ __forceinline__ float fast_rcp(float x) {   // 1 ulp; 1 / inf = 0
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 // The low n bits set (none for n <= 0, all from n = 32 on).
 __device__ __forceinline__ uint32_t bits_below(int n) {
     return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u);
