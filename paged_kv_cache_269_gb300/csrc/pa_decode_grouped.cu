@@ -246,30 +246,36 @@ struct Cursor {
     }
 };
 
-template <int D, int NT, bool kQ8>
+template <int D, int NT, bool kDup, bool kQ8>
 struct Cfg {
     static constexpr int kElem = kQ8 ? 1 : 2;          // bytes of a cache element
     static constexpr int TK = kQ8 ? 4096 / D : (D == 64 ? 32 : 16);   // keys per tile
     static constexpr int MT = TK / 16;
     static constexpr int kHeads = 8 * NT;
+    static constexpr int kOut = kDup ? 4 : kHeads;     // heads of a merge: repeated columns are added first
     static constexpr int kMat = TK * D * kElem;            // bytes of a K (or V) tile
     static constexpr int kStage = 2 * kMat;
-    // more bytes in flight do not help (a third stage for D = 128 made 256 long
-    // sequences 7 % slower); for D = 64 there is room for one
-    static constexpr int kStages = D == 64 && NT == 1 ? 3 : 2;
+    // of 16 bits, more bytes in flight do not help (a third stage for D = 128 made 256
+    // long sequences 7 % slower); for D = 64 there is room for one.  Of 8 bits it is the
+    // latency of a tile's work that bounds a warp, so the room is better used by a third
+    // CTA where registers allow it (kCtasPerSm)
+    static constexpr int kStages = !kQ8 && D == 64 && NT == 1 ? 3 : 2;
     // what a unit's end (merging the warps, a partial's ticket; 1.5 us) costs in
     // tiles' time: 64 sequences 61.3 us uncounted, 57.1 at 4; 16 heads 69.5 at 4,
     // 66.0 at 8
     static constexpr int kCost = 4 * NT;
     static constexpr int kRow = D + 4;                 // floats of a merge row (no bank conflicts)
     static constexpr int OFF_O = kW * kStages * kStage;
-    static constexpr int OFF_ML = OFF_O + kW * kHeads * kRow * 4;
-    static constexpr int OFF_PREFIX = OFF_ML + kW * kHeads * 8;
-    static constexpr int OFF_BAR = OFF_PREFIX + (kChunks + 1 + kW) * 8;
+    static constexpr int OFF_ML = OFF_O + kW * kOut * kRow * 4;
+    // (the prefix is read before the first merge)
+    static constexpr int OFF_PREFIX = kQ8 ? OFF_O : OFF_ML + kW * kOut * 8;
+    static constexpr int kPrefixEnd = OFF_PREFIX + (kChunks + 1 + kW) * 8, kMergeEnd = OFF_ML + kW * kOut * 8;
+    static constexpr int OFF_BAR = kPrefixEnd > kMergeEnd ? kPrefixEnd : kMergeEnd;
     static constexpr int OFF_MASK = OFF_BAR + (kW * kStages + 1) * 8;   // rings, partial written
     static constexpr int OFF_FLAG = OFF_MASK + kW * kStages * 4;
     static constexpr int kBytes = OFF_FLAG + 16 + 1024;  // + alignment slack
-    static constexpr int kCtasPerSm = 2 * (kBytes + 1024) <= 233472 ? 2 : 1;
+    static constexpr int kFit = 233472 / (kBytes + 1024);
+    static constexpr int kCtasPerSm = kQ8 && NT == 1 && D <= 128 && kFit >= 3 ? 3 : (kFit >= 2 ? 2 : 1);
 };
 
 // The K/V head of a unit (a division by a number that is 1 up to 8 or 16 query heads a
@@ -342,12 +348,12 @@ __device__ __forceinline__ void join_unit(const DecodeGroupedArgs &p, int s, int
 }
 
 template <bool kBf16, bool kQ8, int D, int NT, bool kDup>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, Cfg<D, NT, kDup, kQ8>::kCtasPerSm == 3 ? 3 : 1)
     decode_grouped_kernel(const __grid_constant__ CUtensorMap tm_k,
                           const __grid_constant__ CUtensorMap tm_v,
                           const __grid_constant__ DecodeGroupedArgs p) {
-    using C = Cfg<D, NT, kQ8>;
-    constexpr int TK = C::TK, kCost = C::kCost, MT = C::MT, KS = D / 16, kHeads = C::kHeads;
+    using C = Cfg<D, NT, kDup, kQ8>;
+    constexpr int TK = C::TK, kCost = C::kCost, MT = C::MT, KS = D / 16, kHeads = C::kHeads, kOut = C::kOut;
     const GroupedArgs &a = p.g;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -964,8 +970,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int d = 4; d < 32; d *= 2) x += __shfl_xor_sync(0xffffffffu, x, d);
                 const int h = nt * 8 + col + e;
-                if (row == 0) ml[warp * kHeads + h] = make_float2(m[nt][e], x);
-                float *dst = obuf + (warp * kHeads + h) * C::kRow;
+                if constexpr (kDup) {   // columns 4-7 hold what P_lo gave
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks) {
+                        o[ks][nt][e] += __shfl_xor_sync(0xffffffffu, o[ks][nt][e], 2);
+                        o[ks][nt][e + 2] += __shfl_xor_sync(0xffffffffu, o[ks][nt][e + 2], 2);
+                    }
+                    if (col >= 4) continue;
+                }
+                if (row == 0) ml[warp * kOut + h] = make_float2(m[nt][e], x);
+                float *dst = obuf + (warp * kOut + h) * C::kRow;
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) {
                     if constexpr (kQ8) {   // a lane's neighbouring dims
@@ -987,7 +1001,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float mw[kW], top = -INFINITY;
 #pragma unroll
             for (int w = 0; w < kW; ++w) {
-                mw[w] = ml[w * kHeads + h].x;
+                mw[w] = ml[w * kOut + h].x;
                 top = fmaxf(top, mw[w]);
             }
             float sum = 0.f;
@@ -995,13 +1009,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int w = 0; w < kW; ++w) {
                 const float f = mw[w] == -INFINITY ? 0.f : fast_exp2(mw[w] - top);
-                sum += f * ml[w * kHeads + h].y;
-                float4 v = *reinterpret_cast<const float4 *>(obuf + (w * kHeads + h) * C::kRow + d4 * 4);
-                if constexpr (kDup) {
-                    const float4 r = *reinterpret_cast<const float4 *>(
-                        obuf + (w * kHeads + h + 4) * C::kRow + d4 * 4);
-                    v.x += r.x, v.y += r.y, v.z += r.z, v.w += r.w;
-                }
+                sum += f * ml[w * kOut + h].y;
+                const float4 v = *reinterpret_cast<const float4 *>(obuf + (w * kOut + h) * C::kRow + d4 * 4);
                 acc.x += f * v.x, acc.y += f * v.y, acc.z += f * v.z, acc.w += f * v.w;
             }
             if (whole) {
@@ -1079,11 +1088,12 @@ struct Variant {
 template <bool kBf16, bool kQ8, int D>
 Variant variant_of(int group) {
     if (D != 256 && group > 8)
-        return {decode_grouped_kernel<kBf16, kQ8, D, D == 256 ? 1 : 2, false>, Cfg<D, D == 256 ? 1 : 2, kQ8>::kBytes,
-                Cfg<D, D == 256 ? 1 : 2, kQ8>::kCtasPerSm};
+        return {decode_grouped_kernel<kBf16, kQ8, D, D == 256 ? 1 : 2, false>, Cfg<D, D == 256 ? 1 : 2, false, kQ8>::kBytes,
+                Cfg<D, D == 256 ? 1 : 2, false, kQ8>::kCtasPerSm};
     if (group > 4)
-        return {decode_grouped_kernel<kBf16, kQ8, D, 1, false>, Cfg<D, 1, kQ8>::kBytes, Cfg<D, 1, kQ8>::kCtasPerSm};
-    return {decode_grouped_kernel<kBf16, kQ8, D, 1, true>, Cfg<D, 1, kQ8>::kBytes, Cfg<D, 1, kQ8>::kCtasPerSm};
+        return {decode_grouped_kernel<kBf16, kQ8, D, 1, false>, Cfg<D, 1, false, kQ8>::kBytes,
+                Cfg<D, 1, false, kQ8>::kCtasPerSm};
+    return {decode_grouped_kernel<kBf16, kQ8, D, 1, true>, Cfg<D, 1, true, kQ8>::kBytes, Cfg<D, 1, true, kQ8>::kCtasPerSm};
 }
 
 // Launches a variant; its shared-memory limit is set once per device (`which`: the
