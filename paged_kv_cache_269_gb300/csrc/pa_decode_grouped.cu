@@ -794,19 +794,36 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, kDup, kQ8>::kCtasPerSm ==
 #pragma unroll
                         for (int e = 0; e < 4; ++e) sc[mt][nt][e] *= kQ8 ? p.scale_log2 * qs[nt][e & 1] : p.scale_log2;
             }
+            // (bias and mask as steps of their own: as conditions of one, every tile paid for
+            // both)
+            if (a.alibi_slopes) {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int key = k0 + mt * 16 + row + (e >= 2 ? 8 : 0);
+                            sc[mt][nt][e] -= slope[nt][e & 1] * static_cast<float>(g.ctx - 1 - key);
+                        }
+            }
+            if (partial) {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int i = mt * 16 + row + (e >= 2 ? 8 : 0);
+                            if (!visible(k0, i, have)) sc[mt][nt][e] = -INFINITY;
+                        }
+            }
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float x = sc[mt][nt][e];
-                        const int key = k0 + mt * 16 + row + (e >= 2 ? 8 : 0);
-                        if (a.alibi_slopes) x -= slope[nt][e & 1] * static_cast<float>(g.ctx - 1 - key);
-                        if (partial) x = visible(k0, key - k0, have) ? x : -INFINITY;
-                        sc[mt][nt][e] = x;
-                        raise |= x > __fadd_rd(m[nt][e & 1], kRaise);
-                    }
+                    for (int e = 0; e < 4; ++e) raise |= sc[mt][nt][e] > __fadd_rd(m[nt][e & 1], kRaise);
             if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
