@@ -252,7 +252,10 @@ struct Cfg {
     static constexpr int TK = kQ8 ? 4096 / D : (D == 64 ? 32 : 16);   // keys per tile
     static constexpr int MT = TK / 16;
     static constexpr int kHeads = 8 * NT;
-    static constexpr int kOut = kDup ? 4 : kHeads;     // heads of a merge: repeated columns are added first
+    // Heads that a merge takes at a time: repeated columns are added first, and where
+    // it makes room for a third CTA the even columns go before the odd ones.
+    static constexpr int kPasses = kQ8 && D == 128 && NT == 1 && !kDup ? 2 : 1;
+    static constexpr int kOut = kDup || kPasses == 2 ? 4 : kHeads;
     static constexpr int kMat = TK * D * kElem;            // bytes of a K (or V) tile
     static constexpr int kStage = 2 * kMat;
     // of 16 bits, more bytes in flight do not help (a third stage for D = 128 made 256
@@ -978,69 +981,75 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, kDup, kQ8>::kCtasPerSm ==
             cons.advance(a, units, 0, lane);
             load_q();
         }
-        __syncthreads();   // everyone has read the previous merge
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float x = l[nt][e];
-#pragma unroll
-                for (int d = 4; d < 32; d *= 2) x += __shfl_xor_sync(0xffffffffu, x, d);
-                const int h = nt * 8 + col + e;
-                if constexpr (kDup) {   // columns 4-7 hold what P_lo gave
-#pragma unroll
-                    for (int ks = 0; ks < KS; ++ks) {
-                        o[ks][nt][e] += __shfl_xor_sync(0xffffffffu, o[ks][nt][e], 2);
-                        o[ks][nt][e + 2] += __shfl_xor_sync(0xffffffffu, o[ks][nt][e + 2], 2);
-                    }
-                    if (col >= 4) continue;
-                }
-                if (row == 0) ml[warp * kOut + h] = make_float2(m[nt][e], x);
-                float *dst = obuf + (warp * kOut + h) * C::kRow;
-#pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    if constexpr (kQ8) {   // a lane's neighbouring dims
-                        *reinterpret_cast<float2 *>(dst + ks / 8 * 128 + row * (D == 64 ? 8 : 16) + ks % 8 * 2) =
-                            make_float2(o[ks][nt][e], o[ks][nt][e + 2]);
-                    } else {
-                        dst[ks * 16 + row] = o[ks][nt][e];
-                        dst[ks * 16 + row + 8] = o[ks][nt][e + 2];
-                    }
-                }
-            }
-        __syncthreads();
         constexpr int kVec = D / 4;            // float4s per head
         const bool whole = from_start && to_end;
         float *slot = p.partials + static_cast<size_t>(2 * blockIdx.x + (from_start ? 1 : 0)) *
                                        (kHeads * (D + 2));
-        for (int i = threadIdx.x; i < heads * kVec; i += kThreads) {
-            const int h = i / kVec, d4 = i % kVec;
-            float mw[kW], top = -INFINITY;
 #pragma unroll
-            for (int w = 0; w < kW; ++w) {
-                mw[w] = ml[w * kOut + h].x;
-                top = fmaxf(top, mw[w]);
-            }
-            float sum = 0.f;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int pass = 0; pass < C::kPasses; ++pass) {
+            __syncthreads();   // everyone has read the previous merge
 #pragma unroll
-            for (int w = 0; w < kW; ++w) {
-                const float f = mw[w] == -INFINITY ? 0.f : fast_exp2(mw[w] - top);
-                sum += f * ml[w * kOut + h].y;
-                const float4 v = *reinterpret_cast<const float4 *>(obuf + (w * kOut + h) * C::kRow + d4 * 4);
-                acc.x += f * v.x, acc.y += f * v.y, acc.z += f * v.z, acc.w += f * v.w;
-            }
-            if (whole) {
-                float inv = sum > 0.f ? 1.f / sum : 0.f;
-                if constexpr (kQ8) inv *= __ldg(a.v_scales + hk);
-                uint2 r = make_uint2(pack_out<kBf16, kQ8>(p, acc.x * inv, acc.y * inv),
-                                     pack_out<kBf16, kQ8>(p, acc.z * inv, acc.w * inv));
-                *reinterpret_cast<uint2 *>(
-                    a.out + (static_cast<size_t>(s) * a.num_q_heads + hk * p.group + h0 + h) * D + d4 * 4) = r;
-            } else {
-                *reinterpret_cast<float4 *>(slot + h * D + d4 * 4) = acc;
-                if (d4 == 0)
-                    *reinterpret_cast<float2 *>(slot + kHeads * D + 2 * h) = make_float2(top, sum);
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if (C::kPasses == 2 && e != pass) continue;
+                    float x = l[nt][e];
+#pragma unroll
+                    for (int d = 4; d < 32; d *= 2) x += __shfl_xor_sync(0xffffffffu, x, d);
+                    const int h = C::kPasses == 2 ? col / 2 : nt * 8 + col + e;   // among the pass's
+                    if constexpr (kDup) {   // columns 4-7 hold what P_lo gave
+#pragma unroll
+                        for (int ks = 0; ks < KS; ++ks) {
+                            o[ks][nt][e] += __shfl_xor_sync(0xffffffffu, o[ks][nt][e], 2);
+                            o[ks][nt][e + 2] += __shfl_xor_sync(0xffffffffu, o[ks][nt][e + 2], 2);
+                        }
+                        if (col >= 4) continue;
+                    }
+                    if (row == 0) ml[warp * kOut + h] = make_float2(m[nt][e], x);
+                    float *dst = obuf + (warp * kOut + h) * C::kRow;
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks) {
+                        if constexpr (kQ8) {   // a lane's neighbouring dims
+                            *reinterpret_cast<float2 *>(dst + ks / 8 * 128 + row * (D == 64 ? 8 : 16) + ks % 8 * 2) =
+                                make_float2(o[ks][nt][e], o[ks][nt][e + 2]);
+                        } else {
+                            dst[ks * 16 + row] = o[ks][nt][e];
+                            dst[ks * 16 + row + 8] = o[ks][nt][e + 2];
+                        }
+                    }
+                }
+            __syncthreads();
+            for (int i = threadIdx.x; i < (C::kPasses == 2 ? kOut : heads) * kVec; i += kThreads) {
+                const int hb = i / kVec, d4 = i % kVec;
+                const int h = C::kPasses == 2 ? 2 * hb + pass : hb;
+                if (C::kPasses == 2 && h >= heads) continue;
+                float mw[kW], top = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < kW; ++w) {
+                    mw[w] = ml[w * kOut + hb].x;
+                    top = fmaxf(top, mw[w]);
+                }
+                float sum = 0.f;
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < kW; ++w) {
+                    const float f = mw[w] == -INFINITY ? 0.f : fast_exp2(mw[w] - top);
+                    sum += f * ml[w * kOut + hb].y;
+                    const float4 v = *reinterpret_cast<const float4 *>(obuf + (w * kOut + hb) * C::kRow + d4 * 4);
+                    acc.x += f * v.x, acc.y += f * v.y, acc.z += f * v.z, acc.w += f * v.w;
+                }
+                if (whole) {
+                    float inv = sum > 0.f ? 1.f / sum : 0.f;
+                    if constexpr (kQ8) inv *= __ldg(a.v_scales + hk);
+                    uint2 r = make_uint2(pack_out<kBf16, kQ8>(p, acc.x * inv, acc.y * inv),
+                                         pack_out<kBf16, kQ8>(p, acc.z * inv, acc.w * inv));
+                    *reinterpret_cast<uint2 *>(
+                        a.out + (static_cast<size_t>(s) * a.num_q_heads + hk * p.group + h0 + h) * D + d4 * 4) = r;
+                } else {
+                    *reinterpret_cast<float4 *>(slot + h * D + d4 * 4) = acc;
+                    if (d4 == 0)
+                        *reinterpret_cast<float2 *>(slot + kHeads * D + 2 * h) = make_float2(top, sum);
+                }
             }
         }
         if (!whole) {
