@@ -237,19 +237,11 @@ __device__ __forceinline__ uint32_t present(unsigned have, int q, int block_size
 }
 __device__ __forceinline__ bool warp_all(bool v) { return __all_sync(0xffffffffu, v); }
 
-// Work item w: (pair level, split, sequence, K/V head), latest pairs first.
-// False for an empty item, or for a sequence whose lengths are inconsistent
-// (reported once).
-__device__ __forceinline__ bool item_geometry(const PrefillGroupedArgs &p, int w, bool report,
-                                              Item &it) {
+// The item of a pair of tiles, a sequence and a K/V head.  False for an empty item, or
+// for a sequence whose lengths are inconsistent (reported once).
+__device__ __forceinline__ bool item_geometry(const PrefillGroupedArgs &p, int s, int hk, int pair, int split,
+                                              bool report, Item &it) {
     const GroupedArgs &a = p.g;
-    const int sh = a.num_seqs * a.num_kv_heads;
-    const int level = w / (sh * p.splits);
-    int rem = w - level * (sh * p.splits);
-    const int split = rem / sh;
-    rem -= split * sh;
-    const int s = rem / a.num_kv_heads, hk = rem - s * a.num_kv_heads;
-    const int pair = p.num_pairs - 1 - level;
     const int q_first = __ldg(a.query_start + s), q_end = __ldg(a.query_start + s + 1);
     const int ctx = __ldg(a.context_lens + s);
     const int pre_raw = a.prefix_lens ? __ldg(a.prefix_lens + s) : 0;
@@ -304,9 +296,68 @@ __device__ __forceinline__ bool item_geometry(const PrefillGroupedArgs &p, int w
     it.nk1 = tok0 + p.tpt < q_len ? it.nkt : -1;   // -1: tile 1 has no rows
     it.split = split;
     it.splits = parts;
-    it.slot = pair * sh + rem;
+    it.slot = (pair * a.num_seqs + s) * a.num_kv_heads + hk;
     return true;
 }
+// Work item w: (pair level, split, sequence, K/V head), latest pairs first.
+__device__ __forceinline__ bool item_geometry(const PrefillGroupedArgs &p, int w, bool report,
+                                              Item &it) {
+    const GroupedArgs &a = p.g;
+    const int sh = a.num_seqs * a.num_kv_heads;
+    const int level = w / (sh * p.splits);
+    int rem = w - level * (sh * p.splits);
+    const int split = rem / sh;
+    rem -= split * sh;
+    const int s = rem / a.num_kv_heads;
+    return item_geometry(p, s, rem - s * a.num_kv_heads, p.num_pairs - 1 - level, split, report, it);
+}
+
+// The same work by falling numbers of keys whatever sequence they are of, for up to 32
+// sequences (a lane has one) and more items than CTAs: a chunk of a long context that
+// starts last would run alone at the end (four chunks of 512 tokens over 4097 to 8192
+// keys: 174 us by levels of pairs, 158 so).  A sequence's pairs end `step` keys apart, so
+// how many of them end at T or later is a division, and the r-th place is found by
+// halving the range of T.
+struct ByLength {
+    int end, n, step, total, most;         // end of the last pair's keys; pairs; sums over the lanes
+    __device__ __forceinline__ void load(const PrefillGroupedArgs &p, int lane) {
+        const GroupedArgs &a = p.g;
+        step = 2 * p.tpt;
+        end = n = 0;
+        if (lane < a.num_seqs) {
+            const int q0 = __ldg(a.query_start + lane), q1 = __ldg(a.query_start + lane + 1);
+            const int ctx = __ldg(a.context_lens + lane), q = q1 - q0;
+            const bool rows_bad = q0 < 0 || q1 < q0 || q1 > a.total_q;
+            const bool bad = rows_bad || (q > 0 && (q > ctx || ctx > a.max_blocks_per_seq * a.block_size || q > a.max_q));
+            if (bad && blockIdx.x == 0) atomicOr(a.err, PA_DEVERR_CONTEXT);
+            if (!bad && q > 0) {
+                n = (q - 1) / step + 1;
+                end = ctx - q + n * step;
+            }
+        }
+        total = __reduce_add_sync(0xffffffffu, n);
+        most = __reduce_max_sync(0xffffffffu, end);
+    }
+    __device__ __forceinline__ int at_least(int t) const {
+        return __reduce_add_sync(0xffffffffu, end < t ? 0 : min(n, (end - t) / step + 1));
+    }
+    // Place r < total: its sequence and pair.
+    __device__ __forceinline__ void find(int r, int &s, int &pair) const {
+        int lo = 1, hi = most;             // the largest T that r + 1 pairs reach
+        while (lo < hi) {
+            const int mid = lo + (hi - lo + 1) / 2;
+            if (at_least(mid) > r)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        const int back = end < lo ? 0 : (end - lo) / step;
+        const bool here = end >= lo && back < n && end - back * step == lo;
+        const unsigned mask = __ballot_sync(0xffffffffu, here);
+        s = static_cast<int>(__fns(mask, 0, r - at_least(lo + 1) + 1)) & 31;
+        pair = __shfl_sync(0xffffffffu, n - 1 - back, s);
+    }
+};
 
 // A sequence's blocks of one K/V head, as the copies of K and V take them:
 // lane i holds block i of a key tile.  Only blocks that some query of the
@@ -446,6 +497,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             int k = 0, q_loads = 0;                // items whose K is issued, Q loads issued
             int joins = 0;                         // bit t: parity of tile t's split items
             bool ok = true;
+            const bool by_length = kQ8 && a.num_seqs <= 32 && a.num_seqs > 1 && p.splits == 1 &&
+                                   static_cast<unsigned>(p.num_items) > gridDim.x;
+            ByLength order = {};
+            if (by_length) order.load(p, lane);
             for (;;) {
                 int w = 0;
                 Item it;
@@ -459,6 +514,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                         w = __shfl_sync(0xffffffffu, w, 0);
                     }
                     if (static_cast<unsigned>(w) >= static_cast<unsigned>(p.num_items)) break;
+                    if (by_length) {
+                        const int r = w / a.num_kv_heads;
+                        if (r >= order.total) {    // the rest are empty
+                            w = p.num_items;
+                            break;
+                        }
+                        int s, pair;
+                        order.find(r, s, pair);
+                        if (item_geometry(p, s, w - r * a.num_kv_heads, pair, 0, false, it)) break;
+                        continue;
+                    }
                     if (item_geometry(p, w, lane == 0, it)) break;
                 }
                 const bool done = static_cast<unsigned>(w) >= static_cast<unsigned>(p.num_items);

@@ -483,6 +483,36 @@ def test_prefill_long(dev):
     prefill(make_q8_case(48, [6000, 5000], [64, 300], 8, 4, 64, 16, BF16, alibi=True), dev)
 
 
+@pytest.mark.parametrize("heads,B", [((16, 16), 16), ((24, 8), 8)])
+def test_prefill_more_items_than_processors(dev, heads, B):
+    """Items are then taken by falling numbers of keys, whatever sequence they are of."""
+    ctx = [900, 1500, 33, 1500, 0, 1200, 700]
+    new = [900, 300, 33, 1500, 0, 257, 1]
+    prefill(make_q8_case(51, ctx, new, *heads, 64, B, F16), dev)
+    c = make_q8_case(52, ctx, new, *heads, 64, B, BF16, window=300, prefix=[0, 40, 5, 0, 0, 1000, 3])
+    d = to_dev(c, dev)
+    good = run_prefill(c, d).cpu()
+    assert pa.device_errors() == 0
+    check(c, good, True)
+    d["lens"][3] = 1499                               # shorter than its queries
+    out = torch.full_like(d["q"], 5.0)
+    run_prefill(c, d, out)
+    assert pa.device_errors() == pa.DEVERR_CONTEXT
+    r0, r1 = c.starts_list[3], c.starts_list[4]
+    out = out.cpu()
+    assert (out[r0:r1] == 5).all()
+    assert torch.equal(out[:r0], good[:r0]) and torch.equal(out[r1:], good[r1:])
+    pa.reset_workspaces()
+
+
+def test_prefill_many_sequences(dev):
+    # past 32 sequences items go by levels of pairs
+    g = torch.Generator().manual_seed(9)
+    ctx = torch.randint(1, 90, (200,), generator=g).tolist()
+    new = [min(c, int(n)) for c, n in zip(ctx, torch.randint(1, 90, (200,), generator=g))]
+    prefill(make_q8_case(53, ctx, new, 4, 2, 64, 16, BF16), dev)
+
+
 def test_prefill_rows_left_alone_and_flags(dev):
     c = make_q8_case(49, [100, 50, 70], [20, 50, 1], 4, 2, 128, 16, BF16)
     d = to_dev(c, dev)
