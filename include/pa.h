@@ -70,7 +70,8 @@ typedef enum pa_status {
  * manual, "PagedAttention V1 内核": FP16/BF16). */
 typedef enum pa_dtype {
     PA_DTYPE_F16 = 0,
-    PA_DTYPE_BF16 = 1
+    PA_DTYPE_BF16 = 1,
+    PA_DTYPE_E4M3 = 2    /* pa_copy_blocks only: blocks of an 8-bit cache */
 } pa_dtype;
 
 /* Sizes shared by both calls.
@@ -128,7 +129,8 @@ int pa_reshape_and_cache(const void *k, const void *v, void *k_cache, void *v_ca
  * (source pool = destination pool), swap-out (device -> host) and swap-in
  * (host -> device).
  *
- *   src_k, src_v    [src_num_blocks, H, B, D] 16-bit elements: the source pool
+ *   src_k, src_v    [src_num_blocks, H, B, D] 16-bit elements, or e4m3 numbers
+ *                   with PA_DTYPE_E4M3: the source pool
  *   dst_k, dst_v    [dst_num_blocks, H, B, D]: the destination pool (written)
  *   block_pairs     device (or device-addressable), int32 [num_pairs][2]:
  *                   (source block, destination block)

@@ -78,6 +78,7 @@ class PaError(RuntimeError):
 
 DTYPE_F16 = 0
 DTYPE_BF16 = 1
+DTYPE_E4M3 = 2
 
 
 class Dims(ctypes.Structure):
@@ -266,8 +267,9 @@ def reshape_and_cache(k, v, k_cache, v_cache, slot_mapping, stream=None):
 def copy_blocks(src_k, src_v, dst_k, dst_v, block_pairs, stream=None):
     """Copy K and V of block src to block dst (all heads) for every row
     (src, dst) of block_pairs [n, 2] int32 (a CUDA tensor).  The pools are
-    [N, H, B, D] tensors of one 16-bit dtype, each on the CUDA device or in
-    pinned host memory, so one call does copy-on-write (same pool), swap-out
+    [N, H, B, D] tensors of one 16-bit dtype, or of float8_e4m3fn (an 8-bit
+    cache's scales are its heads', so blocks move without them), each on the
+    CUDA device or in pinned host memory, so one call does copy-on-write (same pool), swap-out
     (device -> pinned host) or swap-in (pinned host -> device)."""
     torch = _torch()
     if not isinstance(block_pairs, torch.Tensor) or not block_pairs.is_cuda:
@@ -276,7 +278,7 @@ def copy_blocks(src_k, src_v, dst_k, dst_v, block_pairs, stream=None):
     if block_pairs.dtype != torch.int32 or block_pairs.dim() != 2 or block_pairs.shape[1] != 2 \
             or not block_pairs.is_contiguous():
         raise ValueError("block_pairs must be a contiguous int32 [n, 2] tensor")
-    _element_dtype(src_k)
+    code = DTYPE_E4M3 if src_k.dtype == torch.float8_e4m3fn else _element_dtype(src_k)
     for name, t in (("src_k", src_k), ("src_v", src_v), ("dst_k", dst_k), ("dst_v", dst_v)):
         if not isinstance(t, torch.Tensor) or t.dtype != src_k.dtype or t.dim() != 4 \
                 or not t.is_contiguous():
@@ -289,7 +291,7 @@ def copy_blocks(src_k, src_v, dst_k, dst_v, block_pairs, stream=None):
     if src_v.shape != src_k.shape or dst_v.shape != dst_k.shape or src_k.shape[1:] != dst_k.shape[1:]:
         raise ValueError("copy_blocks: inconsistent pool shapes")
     N_src, H, B, D = src_k.shape
-    dims = Dims(0, H, D, B, N_src, _element_dtype(src_k))
+    dims = Dims(0, H, D, B, N_src, code)
     sh, _ = _stream_handle(dev, stream)
     with torch.cuda.device(dev):
         rc = lib().pa_copy_blocks(_ptr(src_k), _ptr(src_v), N_src, _ptr(dst_k), _ptr(dst_v),

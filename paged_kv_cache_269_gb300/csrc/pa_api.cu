@@ -208,7 +208,8 @@ int pa_copy_blocks(const void *src_k, const void *src_v, int32_t src_num_blocks,
     if (dims->num_heads <= 0 || dims->head_dim <= 0 || dims->block_size <= 0 || num_pairs < 0 ||
         src_num_blocks <= 0 || dst_num_blocks <= 0)
         return PA_ERR_SHAPE;
-    if (!decode_variant_supported(dims->dtype, dims->head_dim, dims->block_size))
+    const bool e4m3 = dims->dtype == PA_DTYPE_E4M3;
+    if (!decode_variant_supported(e4m3 ? PA_DTYPE_F16 : dims->dtype, dims->head_dim, dims->block_size))
         return PA_ERR_UNSUPPORTED;
     if (num_pairs == 0) return PA_OK;
     if (!src_k || !src_v || !dst_k || !dst_v || !block_pairs) return PA_ERR_NULL;
@@ -229,7 +230,7 @@ int pa_copy_blocks(const void *src_k, const void *src_v, int32_t src_num_blocks,
     }
     e = launch_copy_blocks(static_cast<const uint16_t *>(src_k), static_cast<const uint16_t *>(src_v),
                            static_cast<uint16_t *>(dst_k), static_cast<uint16_t *>(dst_v),
-                           block_pairs, num_pairs, dims->num_heads, dims->head_dim,
+                           block_pairs, num_pairs, dims->num_heads, e4m3 ? dims->head_dim / 2 : dims->head_dim,
                            dims->block_size, src_num_blocks, dst_num_blocks, st->num_sms, st->err,
                            static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PA_OK : fail_cuda(e);

@@ -61,6 +61,7 @@ struct WorkspaceLayout {
 void workspace_layout(int32_t num_seqs, int32_t num_heads, int32_t head_dim, int32_t max_parts,
                       WorkspaceLayout *out);
 
+// (head_dim: in elements of 16 bits)
 cudaError_t launch_copy_blocks(const uint16_t *src_k, const uint16_t *src_v, uint16_t *dst_k,
                                uint16_t *dst_v, const int32_t *block_pairs, int32_t num_pairs,
                                int32_t num_heads, int32_t head_dim, int32_t block_size,

@@ -134,6 +134,60 @@ def test_append_many_tokens(dev):
     Append(4, 1300, 9, 3, 256, 16, F16, norm=False, interleaved=True).check(dev)
 
 
+@pytest.mark.parametrize("q8", [True, False])
+@pytest.mark.parametrize("heads,D", [((5, 1), 64), ((7, 3), 128)])
+def test_append_many_tokens_skips_and_flags(dev, q8, heads, D):
+    T, g = 1501, torch.Generator().manual_seed(2)
+    a = Append(13, T, *heads, D, 16, BF16, q8=q8, rotary=48)
+    a.slots[torch.rand(T, generator=g) < 0.2] = -1
+    a.slots[7::97] = a.N * 16
+    a.positions[torch.rand(T, generator=g) < 0.2] = -5
+    a.positions[3::101] = a.most
+    a.check(dev, flags=pa.DEVERR_SLOT | pa.DEVERR_POSITION)
+    a.slots[:], a.positions[:] = -1, -1                      # nothing to do for any token
+    a.check(dev)
+
+
+def test_append_many_tokens_of_k_and_v_alone(dev):
+    T = 1400
+    a = Append(14, T, 1, 3, 128, 8, F16, rotary=0, norm=False)
+    a.slots[5::9] = -1
+    kc, vc = (torch.zeros(a.N, 3, 8, 128, dtype=BYTE, device=dev).view(E4M3) for _ in range(2))
+    pa.reshape_and_cache_q8(a.qkv[:, 1:4].to(dev), a.qkv[:, 4:].to(dev), kc, vc, a.ks.to(dev), a.vs.to(dev),
+                            a.slots.to(dev))
+    assert pa.device_errors() == 0
+    keep = a.slots >= 0
+    at = a.slots[keep].long()
+    for cache, x, s in ((kc, a.qkv[:, 1:4], a.ks), (vc, a.qkv[:, 4:], a.vs)):
+        want = (x[keep].float() / s[:, None]).clamp(-448, 448).to(E4M3).view(BYTE)
+        assert torch.equal(cache.cpu().view(BYTE)[at // 8, :, at % 8], want)
+
+
+@pytest.mark.parametrize("heads,D", [((40, 8), 256), ((100, 1), 256), ((226, 2), 256), ((250, 2), 256)])
+def test_append_many_tokens_of_long_rows(dev, heads, D):
+    # rows for which fewer CTAs fit a processor, and none: the same as in shorter calls
+    Hq, H = heads
+    T = 1300
+    g = torch.Generator(device=dev).manual_seed(1)
+    qkv = torch.randn(T, Hq + 2 * H, D, generator=g, device=dev).to(BF16)
+    slots = torch.randperm(T, generator=g, device=dev).to(torch.int32)
+    pos = torch.randint(0, 500, (T,), generator=g, device=dev).to(torch.int32)
+    table, w = pa.rope_table(500, D, device=dev), 1 + 0.1 * torch.randn(D, generator=g, device=dev)
+    s = scales_for(3, H).to(dev)
+    got = []
+    for step in (T, 600):
+        out = torch.zeros(T, Hq, D, dtype=BF16, device=dev)
+        kc, vc = (torch.zeros(-(-T // 16), H, 16, D, dtype=BYTE, device=dev).view(E4M3) for _ in range(2))
+        for i in range(0, T, step):
+            x = qkv[i:i + step]
+            pa.norm_rope_and_cache(out[i:i + step], x[:, :Hq], x[:, Hq:Hq + H], x[:, Hq + H:], kc, vc, pos[i:i + step],
+                                   table, slots[i:i + step], w, w, k_scales=s, v_scales=s)
+        got.append((out, kc.view(BYTE), vc.view(BYTE)))
+    assert pa.device_errors() == 0
+    for x, y in zip(*got):
+        assert torch.equal(x, y)
+
+
 @pytest.mark.parametrize("packed", [True, False])
 @pytest.mark.parametrize("q8", [True, False])
 def test_append_in_place(dev, packed, q8):
@@ -313,6 +367,30 @@ def test_gather_flags_and_refuses(dev):
             pa.gather_cache_q8(*args)
     pa.gather_cache_q8(o[:0], o2[:0], c, c, s, s, slots[:0])
     assert pa.device_errors() == 0
+
+
+# ------------------------------------------------------------------ blocks
+
+@pytest.mark.parametrize("H,D,B", [(1, 64, 8), (3, 64, 8), (5, 128, 16), (2, 256, 32)])
+def test_copy_blocks(dev, H, D, B):
+    g = torch.Generator().manual_seed(4)
+    kc, vc = (torch.randint(0, 256, (9, H, B, D), generator=g).to(BYTE) for _ in range(2))
+    a, b = kc.to(dev).view(E4M3), vc.to(dev).view(E4M3)
+    pairs = torch.tensor([[0, 7], [3, 8], [1, 99]], dtype=torch.int32, device=dev)
+    pa.copy_blocks(a, b, a, b, pairs)
+    assert pa.device_errors() == pa.DEVERR_TABLE
+    host = torch.empty(4, H, B, D, dtype=BYTE).pin_memory().view(E4M3)
+    assert host.is_pinned()
+    pa.copy_blocks(a, b, host, host, torch.tensor([[7, 1]], dtype=torch.int32, device=dev)[:0])
+    host_k, host_v = (torch.zeros(4, H, B, D, dtype=BYTE).pin_memory().view(E4M3) for _ in range(2))
+    pa.copy_blocks(a, b, host_k, host_v, torch.tensor([[7, 1], [8, 3]], dtype=torch.int32, device=dev))
+    assert pa.device_errors() == 0
+    for cache, was, out in ((a, kc, host_k), (b, vc, host_v)):
+        want = was.clone()
+        want[7], want[8] = was[0], was[3]
+        assert torch.equal(cache.view(BYTE).cpu(), want)
+        assert torch.equal(out.view(BYTE)[1], was[0]) and torch.equal(out.view(BYTE)[3], was[3])
+        assert (out.view(BYTE)[[0, 2]] == 0).all()
 
 
 # ------------------------------------------------------------------ attention

@@ -108,6 +108,16 @@ def test_gather_rejects(lib):
     assert call(ks=ctypes.c_void_p(0x100002)) == -4
 
 
+def test_copy_blocks_of_8bit_pools(lib):
+    def call(d):
+        return lib.pa_copy_blocks(FAKE, FAKE, 32, FAKE, FAKE, 32, FAKE, 0, ctypes.byref(d), None)
+    assert call(dims(dtype=2)) == 0
+    assert call(dims(dtype=2, D=32)) == -3
+    assert call(dims(dtype=3)) == -3
+    with pytest.raises(ValueError):
+        pa.copy_blocks(*[torch.zeros(2, 1, 8, 64).to(E4M3)] * 4, torch.zeros(1, 2, dtype=torch.int32))
+
+
 def _opts(cap=0.0, window=0):
     return ctypes.byref(AttnOpts(cap, window, None, None))
 
