@@ -591,6 +591,49 @@ def test_prefill_many_sequences(dev):
     prefill(make_q8_case(53, ctx, new, 4, 2, 64, 16, BF16), dev)
 
 
+@pytest.mark.parametrize("q_scale", [1e-30, 1e-3, 1e4, 1e30])
+@pytest.mark.parametrize("cap", [0.0, 12.0])
+def test_prefill_sizes_of_queries(dev, q_scale, cap):
+    """As for the decode; items follow one another on a processor, so that the rows of
+    one are scaled while the item before is finished."""
+    ctx = [300, 1100, 77]
+    c = make_q8_case(54, ctx, ctx, 32, 16, 128, 16, BF16, q_scale=q_scale, scale=128 ** -0.5 / q_scale, cap=cap)
+    if cap and c.scale / cap < 2.0 ** -100:           # the range of scale / softcap
+        with pytest.raises(pa.PaError):
+            run_prefill(c, to_dev(c, dev))
+        return
+    prefill(c, dev)
+    c.q[7, 3] = 0.0
+    c.q[250] = 0.0
+    c.q[311, 2, 5] = 3e4 * q_scale
+    c.scale = 1e-4 / q_scale
+    prefill(c, dev)
+
+
+def test_attention_of_keys_that_are_not_numbers(dev):
+    """A NaN among one sequence's keys or values reaches that sequence's rows alone, and
+    nothing at all from where no query sees it."""
+    ctx, new = [200, 150, 90], [40, 150, 1]
+    for D in (64, 128):
+        c = make_q8_case(55, ctx, new, 8, 2, D, 16, F16, window=60)
+        d = to_dev(c, dev)
+        one = dict(d, q=d["q"][[39, 189, 190]].contiguous())
+        good_d, good_p = run_decode(c, one).cpu(), run_prefill(c, d).cpu()
+        assert torch.isfinite(good_d).all() and torch.isfinite(good_p).all()
+        for name in ("k8", "v8"):
+            x = d[name].clone()
+            blk = int(c.tables[1, 9])                         # tokens 144 to 149 of sequence 1
+            x[blk, 0, 2] = torch.tensor(float("nan"), device=dev).to(E4M3)
+            got_d, got_p = run_decode(c, dict(one, **{name: x})).cpu(), run_prefill(c, dict(d, **{name: x})).cpu()
+            assert pa.device_errors() == 0
+            assert got_d[1, :4].isnan().any() and got_p[189, :4].isnan().any()
+            assert torch.equal(got_d[[0, 2]], good_d[[0, 2]]) and torch.equal(got_d[1, 4:], good_d[1, 4:])
+            assert torch.equal(got_p[:40], good_p[:40]) and torch.equal(got_p[190:], good_p[190:])
+            assert torch.equal(got_p[:, 4:], good_p[:, 4:])
+            if name == "k8":
+                assert torch.equal(got_p[40:40 + 146], good_p[40:40 + 146])
+
+
 def test_prefill_rows_left_alone_and_flags(dev):
     c = make_q8_case(49, [100, 50, 70], [20, 50, 1], 4, 2, 128, 16, BF16)
     d = to_dev(c, dev)
