@@ -404,7 +404,7 @@ int pa_gather_cache_q8(void *k_out, void *v_out, const void *k_cache, const void
     a.block_shift = block_shift(dims);
     a.pool_slots = pool;
     a.wide_stores = aligned(k_out, 32) && aligned(v_out, 32);
-    return finish(launch_gather_q8(a, dims->dtype, static_cast<cudaStream_t>(stream)));
+    return finish(launch_gather_q8(a, dims->dtype, sms, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -622,8 +622,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, kDup, kQ8>::kCtasPerSm ==
                 const uint2 *src2 = reinterpret_cast<const uint2 *>(src);
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks)
-                    raw[ks] = live ? __ldg(src2 + (hq * D + ks * 16) / 4 + (lane & 3)) : make_uint2(0u, 0u);
-                float f = live ? __ldg(a.k_scales + hk) : 0.f;
+                    raw[ks] = live ? src2[(hq * D + ks * 16) / 4 + (lane & 3)] : make_uint2(0u, 0u);
+                float f = live ? a.k_scales[hk] : 0.f;
                 if (p.io_bf16) {
                     // to fp16, by a power of two that brings the row's largest element to
                     // [2^10, 2^11): bf16's exponents do not fit, its 8 bits do

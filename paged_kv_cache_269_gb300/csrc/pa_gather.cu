@@ -4,12 +4,13 @@
 // out[i, h] = code(slot_i, h) * scale_h for K and V, the product in fp32 and
 // rounded once.  1 byte in and 2 out per element, one flop: bound by HBM.
 //
-// One thread moves 16 codes (one 16-byte load, one 32-byte store) four times; the chunks
-// of a token's K then V rows lie side by side in its index, so the stores of a warp are
-// whole rows of the output.  64 sequences of 256 to 2048 tokens, 8 heads of 128, bf16
-// (403 MB): 62 us, 6.5 TB/s, 0.97 of this GPU's copy rate; a persistent grid, with the
-// next slots asked for while numbers are on their way, took 71 us.  1000 tokens 3.1 us,
-// what a launch costs and two round trips.
+// One thread moves 16 codes (one 16-byte load, one 32-byte store), one or four times; the
+// chunks of a token's K then V rows lie side by side in its index, so the stores of a
+// warp are whole rows of the output.  64 sequences of 256 to 2048 tokens, 8 heads of 128,
+// bf16 (403 MB): 62 us, 6.5 TB/s, 0.97 of this GPU's copy rate; a persistent grid, with
+// the next slots asked for while numbers are on their way, took 71 us, and all of a
+// thread's slots asked for before its first number 66.  1000 tokens: 2.1 us, what a launch
+// costs and two round trips.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <stdint.h>
@@ -22,7 +23,6 @@ namespace pa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;             // chunks a thread has on their way at once
 
 template <bool kBf16>
 __device__ __forceinline__ uint32_t scaled(uint32_t f16x2, float scale) {
@@ -43,40 +43,44 @@ __device__ __forceinline__ void store32(void *dst, const uint32_t (&v)[8]) {
                  : "memory");
 }
 
-template <bool kBf16>
+template <bool kBf16, int kUnroll>
 __global__ void __launch_bounds__(kThreads) gather_q8_kernel(const GatherArgs a, int chunk_shift) {
     allow_dependents_to_launch();
-    grid_dependency_wait();
     // chunk `rest` of token `token`: its K rows, then its V rows; the thread's chunks are
-    // kThreads apart
+    // kThreads apart.  (All of it is reckoned while the kernel before still runs.)
     const int per_matrix = a.num_kv_heads << chunk_shift, per_token = 2 * per_matrix;
     const int step_tokens = kThreads / per_token, step_rest = kThreads - step_tokens * per_token;
     const long long first = static_cast<long long>(blockIdx.x) * (kThreads * kUnroll) + threadIdx.x;
-    int token = static_cast<int>(first / per_token);
-    int rest = static_cast<int>(first - static_cast<long long>(token) * per_token);
+    int token[kUnroll], rest[kUnroll];
+    token[0] = static_cast<int>(first / per_token);
+    rest[0] = static_cast<int>(first - static_cast<long long>(token[0]) * per_token);
+#pragma unroll
+    for (int u = 1; u < kUnroll; ++u) {
+        token[u] = token[u - 1] + step_tokens;
+        rest[u] = rest[u - 1] + step_rest;
+        if (rest[u] >= per_token) rest[u] -= per_token, ++token[u];
+    }
+    grid_dependency_wait();
     uint4 codes[kUnroll];
     float scale[kUnroll];
     uint8_t *dst[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
         dst[u] = nullptr;
-        const int slot = token < a.num_tokens ? __ldg(a.slots + token) : -1;
+        const int slot = token[u] < a.num_tokens ? a.slots[token[u]] : -1;
+        const bool is_v = rest[u] >= per_matrix;
+        scale[u] = (is_v ? a.v_scales : a.k_scales)[(is_v ? rest[u] - per_matrix : rest[u]) >> chunk_shift];
         if (slot >= 0 && slot < a.pool_slots) {
-            const bool is_v = rest >= per_matrix;
-            const int c = is_v ? rest - per_matrix : rest, h = c >> chunk_shift;
+            const int c = is_v ? rest[u] - per_matrix : rest[u], h = c >> chunk_shift;
             const int block = slot >> a.block_shift, off = slot - (block << a.block_shift);
             const size_t row = ((static_cast<size_t>(block) * a.num_kv_heads + h) << a.block_shift) + off;
-            codes[u] = __ldg(reinterpret_cast<const uint4 *>(is_v ? a.v_cache : a.k_cache) +
+            codes[u] = __ldcg(reinterpret_cast<const uint4 *>(is_v ? a.v_cache : a.k_cache) +
                               ((row - h) << chunk_shift) + c);
-            scale[u] = __ldg((is_v ? a.v_scales : a.k_scales) + h);
             dst[u] = reinterpret_cast<uint8_t *>(is_v ? a.v_out : a.k_out) +
-                     32 * (static_cast<size_t>(token) * per_matrix + c);
-        } else if (slot >= 0 && rest == 0) {
+                     32 * (static_cast<size_t>(token[u]) * per_matrix + c);
+        } else if (slot >= 0 && rest[u] == 0) {
             atomicOr(a.err, PA_DEVERR_SLOT);
         }
-        token += step_tokens;
-        rest += step_rest;
-        if (rest >= per_token) rest -= per_token, ++token;
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
@@ -99,10 +103,14 @@ __global__ void __launch_bounds__(kThreads) gather_q8_kernel(const GatherArgs a,
 
 }  // namespace
 
-cudaError_t launch_gather_q8(const GatherArgs &args, int dtype, cudaStream_t stream) {
+cudaError_t launch_gather_q8(const GatherArgs &args, int dtype, int num_sms, cudaStream_t stream) {
     const int chunk_shift = args.head_dim == 64 ? 2 : (args.head_dim == 128 ? 3 : 4);
     const long long total = (2LL * args.num_kv_heads << chunk_shift) * args.num_tokens;
-    const long long ctas = (total + kThreads * kUnroll - 1) / (kThreads * kUnroll);
+    // Four chunks a thread where the device is full of them (403 MB: 62 us, 72 with one);
+    // one where it is not, and the two round trips of a thread are all there is (1000
+    // tokens in a graph: 2.1 us, 3.6 with four).
+    const int unroll = total > 8LL * kThreads * num_sms ? 4 : 1;
+    const long long ctas = (total + kThreads * unroll - 1) / (kThreads * unroll);
     if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -113,8 +121,10 @@ cudaError_t launch_gather_q8(const GatherArgs &args, int dtype, cudaStream_t str
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, dtype == PA_DTYPE_BF16 ? gather_q8_kernel<true> : gather_q8_kernel<false>, args,
-                              chunk_shift);
+    const bool bf16 = dtype == PA_DTYPE_BF16;
+    const auto kernel = unroll == 4 ? (bf16 ? gather_q8_kernel<true, 4> : gather_q8_kernel<false, 4>)
+                                    : (bf16 ? gather_q8_kernel<true, 1> : gather_q8_kernel<false, 1>);
+    return cudaLaunchKernelEx(&cfg, kernel, args, chunk_shift);
 }
 
 }  // namespace pa

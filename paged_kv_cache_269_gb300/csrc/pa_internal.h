@@ -241,6 +241,6 @@ struct GatherArgs {
     long long pool_slots;          // N * B
     unsigned int *err;
 };
-cudaError_t launch_gather_q8(const GatherArgs &args, int dtype, cudaStream_t stream);
+cudaError_t launch_gather_q8(const GatherArgs &args, int dtype, int num_sms, cudaStream_t stream);
 
 }  // namespace pa

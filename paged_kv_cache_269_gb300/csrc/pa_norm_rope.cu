@@ -66,7 +66,7 @@ __device__ __forceinline__ uint4 round8(const float *x) {
     return make_uint4(u[0], u[1], u[2], u[3]);
 }
 __device__ __forceinline__ void load8(const float *p, float *x) {
-    const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
     x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
     x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
 }
@@ -171,7 +171,7 @@ __device__ __forceinline__ void store_row(const AppendArgs &a, const uint64_t (&
     const size_t at = (cache_row + (static_cast<size_t>(h) << a.block_shift)) * D;
     void *cache = is_v ? a.v_cache : a.k_cache;
     if constexpr (kQ8) {
-        const float scale = __ldg((is_v ? a.v_scales : a.k_scales) + h), inv = fast_rcp(scale);
+        const float scale = (is_v ? a.v_scales : a.k_scales)[h], inv = fast_rcp(scale);
         uint32_t c[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) c[i] = quantise_pair(x[i], make_pair(-scale, -scale), make_pair(inv, inv));
@@ -197,14 +197,11 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const AppendArgs a,
     constexpr int kLanes = D / 16;         // threads that share a head row
     constexpr int kRows = kThreads / kLanes;
     allow_dependents_to_launch();
-    grid_dependency_wait();
+    // (what needs no memory is reckoned while the kernel before still runs)
     const int p = threadIdx.x % kLanes;
     const int token = row_splits == 1 ? blockIdx.x : blockIdx.x / row_splits;
     const int split = row_splits == 1 ? 0 : blockIdx.x - token * row_splits;
     const int Hq = a.num_q_heads, Hk = a.num_kv_heads;
-    const int pos = a.positions ? __ldg(a.positions + token) : 0;
-    const int slot = __ldg(a.slot_mapping + token);
-
     const int pairs = a.rotary_dim / 16;   // threads of a row whose chunks are rotated
     const bool rotated = p < pairs;
     // the thread's two chunks of 8, at these elements of the row
@@ -213,9 +210,12 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const AppendArgs a,
     const uint16_t *q = a.q + token * a.q_stride, *k = a.k + token * a.k_stride - static_cast<ptrdiff_t>(Hq) * D;
     const uint16_t *v = a.v + token * a.v_stride - static_cast<ptrdiff_t>(Hq + Hk) * D;
     auto row_of = [&](int r) { return (r < Hq ? q : (r < Hq + Hk ? k : v)) + static_cast<ptrdiff_t>(r) * D; };
-    // the first row is asked for together with the position and the slot
     int r = split * kRows + threadIdx.x / kLanes;
     const int step = row_splits * kRows;
+    grid_dependency_wait();
+    // the first row is asked for together with the position and the slot
+    const int pos = a.positions ? a.positions[token] : 0;
+    const int slot = a.slot_mapping[token];
     uint4 d0 = make_uint4(0, 0, 0, 0), d1 = d0;
     if (r < Hq + 2 * Hk) {
         const uint16_t *src = row_of(r);
@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kStreamThreads, kMostCtas) norm_rope_stream_ke
     if constexpr (kNorm) {
         for (int i = threadIdx.x; i < 2 * D; i += kStreamThreads) {
             const float *src = i < D ? a.q_weight : a.k_weight;
-            weights[i] = src ? __ldg(src + i % D) : 0.f;
+            weights[i] = src ? src[i % D] : 0.f;
         }
     }
     __syncthreads();
@@ -308,8 +308,8 @@ __global__ void __launch_bounds__(kStreamThreads, kMostCtas) norm_rope_stream_ke
             const long long t = blockIdx.x + (i + lane) * gridDim.x;
             pos = -1, slot = -1;
             if (t < a.num_tokens) {
-                pos = a.positions ? __ldg(a.positions + t) : 0;
-                slot = __ldg(a.slot_mapping + t);
+                pos = a.positions ? a.positions[t] : 0;
+                slot = a.slot_mapping[t];
             }
         };
         int next_pos, next_slot;
