@@ -58,11 +58,12 @@ typedef enum pa_status {
 /* Bits of the per-device error word (pa_device_errors). */
 #define PA_DEVERR_TABLE   0x1u  /* a used block-table entry was outside [0, num_blocks)   */
 #define PA_DEVERR_CONTEXT 0x2u  /* a context length was < 0 or > max_blocks_per_seq * block_size */
-#define PA_DEVERR_SLOT    0x4u  /* a slot_mapping entry was >= num_blocks * block_size      */
+#define PA_DEVERR_SLOT    0x4u  /* a slot_mapping (or gathered slot) entry was >= num_blocks * block_size */
 #define PA_DEVERR_TIMEOUT 0x8u  /* an internal pipeline wait gave up (should never happen) */
 #define PA_DEVERR_PREFIX  0x10u /* pa_decode_shared_prefix: a sequence could not use its group's
                                    shared prefix (see there) and was decoded in full instead */
-#define PA_DEVERR_POSITION 0x20u /* pa_rope_and_cache: a position was >= max_positions      */
+#define PA_DEVERR_POSITION 0x20u /* pa_rope_and_cache, pa_norm_rope_and_cache: a position was >=
+                                    max_positions */
 
 /* Element type of q, the caches and the output (and of k, v for
  * reshape_and_cache): IEEE binary16, or bfloat16 (the top 16 bits of an
@@ -606,7 +607,8 @@ typedef struct pa_append_opts {
  * then the rotation, then one rounding: q, and k and v in a 16-bit cache, to the
  * element type; in an 8-bit cache to e4m3 of x / scales[h], to nearest even,
  * values past 448 at 448 (infinities too; NaN stays).  The arithmetic is fp32: a
- * row whose sum of squares is past fp32 comes out 0.  v is not normed.
+ * row whose sum of squares is past fp32 comes out 0, and with eps = 0 one whose
+ * squares are below it infinite.  v is not normed.
  *
  * The arguments are those of pa_rope_and_cache, with these additions:
  *   num_q_heads  may be 0: q and q_out are not read and may be NULL

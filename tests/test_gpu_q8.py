@@ -776,3 +776,88 @@ def test_graph_capture_and_streams(dev):
     graphs[0].replay()
     torch.cuda.synchronize()
     assert torch.equal(out_d, want) and pa.device_errors() == 0
+
+
+def test_two_streams_at_once(dev):
+    """Calls on two streams, each with its stream's buffers, over and over."""
+    cases = [make_q8_case(70 + i, [2000, 300, 40, 5], [30, 300, 1, 5], 8, 2, 128, 16, BF16) for i in range(2)]
+    ds = [to_dev(c, dev) for c in cases]
+    ones = [dict(d, q=d["q"][[29, 329, 330, 335]].contiguous()) for d in ds]
+    want = [(run_decode(c, o).clone(), run_prefill(c, d).clone()) for c, d, o in zip(cases, ds, ones)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(dev) for _ in range(2)]
+    got = [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append((run_decode(cases[i], ones[i]), run_prefill(cases[i], ds[i])))
+    torch.cuda.synchronize()
+    assert pa.device_errors() == 0
+    for g, w in zip(got, want):
+        assert all(torch.equal(x, w[0]) and torch.equal(y, w[1]) for x, y in g)
+
+
+def test_pools_past_2_31_bytes(dev):
+    """Blocks at the far end of pools of more than 2^32 bytes."""
+    H, D, B, N = 8, 256, 32, 70000
+    assert N * H * B * D > 2 ** 32
+    kc, vc = (torch.empty(N, H, B, D, dtype=BYTE, device=dev).view(E4M3) for _ in range(2))
+    g = torch.Generator().manual_seed(1)
+    T = 150
+    far = torch.tensor([N - 1, N - 3, N // 2 + 7, N - 2, 1], dtype=torch.int32)
+    x = torch.randn(T, 2 * H + 16, D, generator=g).to(BF16).to(dev)
+    ks, vs = scales_for(1, H).to(dev), scales_for(2, H).to(dev)
+    t = torch.arange(T)
+    slots = (far[t // B].long() * B + t % B).to(torch.int32).to(dev)
+    pa.reshape_and_cache_q8(x[:, :H], x[:, H:2 * H], kc, vc, ks, vs, slots)
+    ko, vo = (torch.empty(T, H, D, dtype=BF16, device=dev) for _ in range(2))
+    pa.gather_cache_q8(ko, vo, kc, vc, ks, vs, slots)
+    tables, lens = far[None].to(dev), torch.tensor([T], dtype=torch.int32, device=dev)
+    q = x[:1, 2 * H:].contiguous()
+    out = torch.empty_like(q)
+    pa.decode_grouped_q8(out, q, kc, vc, ks, vs, tables, lens, D ** -0.5)
+    assert pa.device_errors() == 0
+    # the same in a pool of five blocks
+    k5, v5 = (torch.empty(5, H, B, D, dtype=BYTE, device=dev).view(E4M3) for _ in range(2))
+    near = torch.arange(5, dtype=torch.int32)
+    pa.reshape_and_cache_q8(x[:, :H], x[:, H:2 * H], k5, v5, ks, vs, torch.arange(T, dtype=torch.int32, device=dev))
+    want = torch.empty_like(q)
+    pa.decode_grouped_q8(want, q, k5, v5, ks, vs, near[None].to(dev), lens, D ** -0.5)
+    assert torch.equal(out, want)
+    for o, c, s in ((ko, k5, ks), (vo, v5, vs)):
+        rows = c.view(BYTE).permute(0, 2, 1, 3).reshape(5 * B, H, D)[:T].view(E4M3).float() * s[:, None]
+        assert torch.equal(o, rows.to(BF16))
+    # and the prefill, at head_dim 128 (the same bytes as twice the heads)
+    k2, v2 = kc.view(BYTE).view(N, 2 * H, B, 128).view(E4M3), vc.view(BYTE).view(N, 2 * H, B, 128).view(E4M3)
+    assert k2.numel() > 2 ** 32
+    s2 = torch.full((2 * H,), 0.01, device=dev)
+    q2 = torch.randn(T, 2 * H, 128, generator=g).to(BF16).to(dev)
+    xs = torch.randn(T, 2 * H, 128, generator=g).to(BF16).to(dev)
+    pa.reshape_and_cache_q8(xs, xs, k2, v2, s2, s2, slots)
+    k5, v5 = k5.view(BYTE).view(5, 2 * H, B, 128).view(E4M3), v5.view(BYTE).view(5, 2 * H, B, 128).view(E4M3)
+    pa.reshape_and_cache_q8(xs, xs, k5, v5, s2, s2, torch.arange(T, dtype=torch.int32, device=dev))
+    starts = torch.tensor([0, T], dtype=torch.int32, device=dev)
+    a, b = torch.empty_like(q2), torch.empty_like(q2)
+    pa.prefill_grouped_q8(a, q2, k2, v2, s2, s2, tables, lens, starts, 128 ** -0.5, max_query_len=T)
+    pa.prefill_grouped_q8(b, q2, k5, v5, s2, s2, near[None].to(dev), lens, starts, 128 ** -0.5, max_query_len=T)
+    assert pa.device_errors() == 0 and torch.equal(a, b)
+
+
+def test_appended_then_read_in_one_stream(dev):
+    """Each call reads what the one before wrote, without a wait in between."""
+    H, D, B, N = 4, 128, 16, 64
+    g = torch.Generator(device=dev).manual_seed(8)
+    kc, vc = (torch.zeros(N, H, B, D, dtype=BYTE, device=dev).view(E4M3) for _ in range(2))
+    s = torch.full((H,), 2.0 ** -5, device=dev)
+    slots = torch.randperm(N * B, generator=g, device=dev).to(torch.int32)
+    x = [torch.randn(N * B, 2 * H, D, generator=g, device=dev).to(BF16) for _ in range(40)]
+    got = []
+    for y in x:
+        pa.reshape_and_cache_q8(y[:, :H], y[:, H:], kc, vc, s, s, slots)
+        ko, vo = (torch.empty(N * B, H, D, dtype=BF16, device=dev) for _ in range(2))
+        pa.gather_cache_q8(ko, vo, kc, vc, s, s, slots)
+        got.append((ko, vo))
+    assert pa.device_errors() == 0
+    for y, (ko, vo) in zip(x, got):
+        for o, r in ((ko, y[:, :H]), (vo, y[:, H:])):
+            assert torch.equal(o, ((r.float() * 32).clamp(-448, 448).to(E4M3).float() / 32).to(BF16))
