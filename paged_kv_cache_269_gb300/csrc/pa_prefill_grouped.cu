@@ -88,9 +88,16 @@
 // two warps set the pace (chunks of 512 tokens over 4097 to 8192 keys, 32 heads on 8: 313
 // us, and 174 so; a 16-bit cache 152). A bf16 Q is made fp16 by its softmax threads, row by
 // row with a scale of its own, while the item before waits for its last product.
-// Measured: those chunks 159 us, 1180 TFLOP/s (fp16 154), with the items by falling numbers
-// of keys (ByLength); 8191 tokens of head_dim 64, 32 heads on 4, distance biases 372 us
+// Measured: those chunks 161 us, 1165 TFLOP/s (fp16 150), with the items by falling numbers
+// of keys (ByLength); 8191 tokens of head_dim 64, 32 heads on 4, distance biases 373 us
 // (fp16 359, the 16-bit cache's time).
+// What bounds it at head_dim 128 is shared memory: the products' operands take 87 of its 128
+// bytes a cycle, and a step's tiles are written as bytes, read, and written widened (1060
+// cycles a tile of a step's 1500, half of them waiting for the stores to drain). Between
+// items nothing makes up for it: one prompt of 8192 tokens, 32 heads on 4, takes 368 us in
+// fp16 (335 over 16 bits), 16 prompts of 333 to 1024 tokens 90 (81); and a bf16 Q costs
+// another 3500 cycles an item, for the same reason: 400 and 108 us. Bytes loaded to registers
+// by three warps instead of staged took 632 us (latency), half a tile ahead in registers 409.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -325,11 +332,14 @@ __device__ __forceinline__ bool item_geometry(const PrefillGroupedArgs &p, int w
 }
 
 // The same work by falling numbers of keys whatever sequence they are of, for up to 32
-// sequences (a lane has one) and more items than CTAs: a chunk of a long context that
-// starts last would run alone at the end (four chunks of 512 tokens over 4097 to 8192
-// keys: 174 us by levels of pairs, 158 so).  A sequence's pairs end `step` keys apart, so
-// how many of them end at T or later is a division, and the r-th place is found by
-// halving the range of T.
+// sequences (a lane has one) and one to four rounds of CTAs (with more the rest evens out
+// by itself: 16 prompts of 333 to 1024 tokens, fp16, 101 us so, 90 by levels): a chunk of
+// a long context that starts last would run alone at the end (four chunks of 512 tokens
+// over 4097 to 8192 keys, bf16: 174 us by levels of pairs, 158 so).  A sequence's pairs end
+// `step` keys apart, so how many of them end at T or later is a division, and the r-th place
+// is found by halving the range of T.  Calls with distance biases keep the levels: their
+// loop pays for the code beside it (8191 tokens of head_dim 64 359 us, 381 with it).
+constexpr unsigned kOrderedRounds = 4;
 struct ByLength {
     int end, n, step, total, most;         // end of the last pair's keys; pairs; sums over the lanes
     __device__ __forceinline__ void load(const PrefillGroupedArgs &p, int lane) {
@@ -350,26 +360,26 @@ struct ByLength {
         total = __reduce_add_sync(0xffffffffu, n);
         most = __reduce_max_sync(0xffffffffu, end);
     }
-    __device__ __forceinline__ int at_least(int t) const {
-        return __reduce_add_sync(0xffffffffu, end < t ? 0 : min(n, (end - t) / step + 1));
-    }
-    // Place r < total: its sequence and pair.
-    __device__ __forceinline__ void find(int r, int &s, int &pair) const {
-        int lo = 1, hi = most;             // the largest T that r + 1 pairs reach
-        while (lo < hi) {
-            const int mid = lo + (hi - lo + 1) / 2;
-            if (at_least(mid) > r)
-                lo = mid;
-            else
-                hi = mid - 1;
-        }
-        const int back = end < lo ? 0 : (end - lo) / step;
-        const bool here = end >= lo && back < n && end - back * step == lo;
-        const unsigned mask = __ballot_sync(0xffffffffu, here);
-        s = static_cast<int>(__fns(mask, 0, r - at_least(lo + 1) + 1)) & 31;
-        pair = __shfl_sync(0xffffffffu, n - 1 - back, s);
-    }
 };
+// Place r < total: its sequence (low 5 bits) and pair.  A call of its own: inlined, its
+// registers cost the loop around it (one prompt of 8192 tokens, which has no use for it,
+// 382 -> 397 us).
+__device__ __noinline__ int find_place(int end, int n, int step, int most, int r) {
+    auto at_least = [&](int t) { return __reduce_add_sync(0xffffffffu, end < t ? 0 : min(n, (end - t) / step + 1)); };
+    int lo = 1, hi = most;                 // the largest T that r + 1 pairs reach
+    while (lo < hi) {
+        const int mid = lo + (hi - lo + 1) / 2;
+        if (at_least(mid) > r)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    const int back = end < lo ? 0 : (end - lo) / step;
+    const bool here = end >= lo && back < n && end - back * step == lo;
+    const unsigned mask = __ballot_sync(0xffffffffu, here);
+    const int s = static_cast<int>(__fns(mask, 0, r - at_least(lo + 1) + 1)) & 31;
+    return __shfl_sync(0xffffffffu, n - 1 - back, s) << 5 | s;
+}
 
 // A sequence's blocks of one K/V head, as the copies of K and V take them:
 // lane i holds block i of a key tile.  Only blocks that some query of the
@@ -509,8 +519,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             int k = 0, q_loads = 0;                // items whose K is issued, Q loads issued
             int joins = 0;                         // bit t: parity of tile t's split items
             bool ok = true;
-            const bool by_length = kQ8 && a.num_seqs <= 32 && a.num_seqs > 1 && p.splits == 1 &&
-                                   static_cast<unsigned>(p.num_items) > gridDim.x;
+            const bool by_length = kQ8 && !kAlibi && a.num_seqs <= 32 && a.num_seqs > 1 && p.splits == 1 &&
+                                   static_cast<unsigned>(p.num_items) > gridDim.x &&
+                                   static_cast<unsigned>(p.num_items) <= kOrderedRounds * gridDim.x;
             ByLength order = {};
             if (by_length) order.load(p, lane);
             for (;;) {
@@ -532,9 +543,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             w = p.num_items;
                             break;
                         }
-                        int s, pair;
-                        order.find(r, s, pair);
-                        if (item_geometry(p, s, w - r * a.num_kv_heads, pair, 0, false, it)) break;
+                        const int at = find_place(order.end, order.n, order.step, order.most, r);
+                        if (item_geometry(p, at & 31, w - r * a.num_kv_heads, at >> 5, 0, false, it)) break;
                         continue;
                     }
                     if (item_geometry(p, w, lane == 0, it)) break;
@@ -833,9 +843,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         // Item k's Q, where it has to be made fp16: each row by a power of two that brings
         // its largest element to [2^10, 2^11), since bf16's exponents do not fit and its 8
-        // bits do.  A thread takes its own row, while the item before waits for its last
-        // product.  Returns what the row's scores are short of.
+        // bits do.  A thread takes its own row: while the item before waits for its last
+        // product, if Q is there by then, and else after that item's output (waiting for it
+        // first cost 16 prompts of 333 to 1024 tokens 114 us instead of 108).  q_factor: what
+        // the row's scores are short of.
         float q_factor = 1.f;
+        int q_ready = -1;          // the last item whose Q is ready
         auto ready_q = [&](int k) {
             const int slot = k % 2;
             if (!warp_all(mbar_wait(&bar[C::ITEM_FULL + slot], (k / 2) & 1, abort_flag, a.err))) return false;
@@ -875,12 +888,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[C::Q_READY + slot * 2 + t]);
+            q_ready = k;
             return true;
         };
         uint32_t n = 0;            // S tiles consumed
         uint32_t tiles = 0;        // key tiles of all items (mask ring)
         bool ok = true;
-        if constexpr (kScaleQ) ok = ready_q(0);
         for (int k = 0; ok; ++k) {
             const int slot = k % 2;
             ok = warp_all(mbar_wait(&bar[C::ITEM_FULL + slot], (k / 2) & 1, abort_flag, a.err));
@@ -891,6 +904,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool done = it->done;
             const int nk = t == 0 ? it->nk0 : it->nk1;
             if (done) break;
+            if constexpr (kScaleQ) {
+                if (q_ready < k) ok = ready_q(k);
+                if (!ok) break;
+            }
             // the tile's Q is done with when its last S is: then the warp's output
             // rows are staged there
             uint8_t *staging = smem + C::OFF_Q + (slot * 2 + t) * C::kTileQ + (warp % 4) * (C::kTileQ / 4);
@@ -900,7 +917,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (nk < 0) {
                 release();
                 pending = slot;
-                if constexpr (kScaleQ) ok = ready_q(k + 1);
                 continue;
             }
             // The row's position.  A row without a query stands where the warp's last
@@ -1156,9 +1172,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!ok) break;
             if constexpr (kScaleQ) {
-                release();         // (an item without key tiles)
-                ok = ready_q(k + 1);
-                if (!ok) break;
+                const int after = (k + 1) % 2, wrap = ((k + 1) / 2) & 1;
+                if (nk > 0 && warp_all(mbar_test(&bar[C::ITEM_FULL + after], wrap) &&
+                                       mbar_test(&bar[C::Q_FULL + after], wrap))) {
+                    ok = ready_q(k + 1);
+                    if (!ok) break;
+                }
             }
             if (nk > 0) {
                 ok = warp_all(mbar_wait(&bar[C::PV_DONE + t * 3 + (n - 1) % C::kBufs], ((n - 1) / C::kBufs) & 1, abort_flag,
