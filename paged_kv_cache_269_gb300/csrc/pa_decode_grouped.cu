@@ -226,6 +226,7 @@ struct Cursor {
     int s, unit, idx;
     Geo g;
     int base, ctx_l, pre_l;
+    int pad = 0;               // 0, or what every unit takes of the line
     __device__ __forceinline__ void load_group(const GroupedArgs &a, int lane) {
         base = s & ~31;
         ctx_l = load_ctx(a, base + lane);
@@ -234,6 +235,7 @@ struct Cursor {
     __device__ __forceinline__ void set_geo(const GroupedArgs &a) {
         g = make_geo<TK, kCost>(a, __shfl_sync(0xffffffffu, ctx_l, s & 31),
                          __shfl_sync(0xffffffffu, pre_l, s & 31));
+        if (pad) g.len = pad;
     }
     // The next sequence with tiles (or s = num_seqs, nt = 0).
     __device__ __forceinline__ void next_seq(const GroupedArgs &a, int lane) {
@@ -285,6 +287,10 @@ struct Cfg {
     // tiles' time: 64 sequences 61.3 us uncounted, 57.1 at 4; 16 heads 69.5 at 4,
     // 66.0 at 8
     static constexpr int kCost = 4 * NT;
+    // 8-bit caches, a CTA for every unit: units of up to so many tiles are not cut. 20
+    // sequences, 4 K/V heads of 128: 100 tokens 9.2 us cut, 6.8 whole, 300 9.4 and 9.0, 400
+    // 9.3 and 9.9; of 256 (half the keys a tile): 300 tokens 14.6 and 11.7
+    static constexpr int kUncut = D == 256 ? 20 : 12;
     static constexpr int kRow = D + 4;                 // floats of a merge row (no bank conflicts)
     static constexpr int OFF_O = kW * kStages * kStage;
     static constexpr int OFF_ML = OFF_O + kW * kOut * kRow * 4;
@@ -420,11 +426,20 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, kDup, kQ8>::kCtasPerSm ==
     Cursor<TK, kCost> cons;
     cons.base = -1;
     const bool small = a.num_seqs <= 32;
+    // 8-bit caches, few short contexts: a unit to a CTA, whole, by taking all of them for
+    // as long as the longest.  (Cut, they cost a partial, a ticket and a join.)
+    [[maybe_unused]] auto whole_units = [&](int live, int most) {
+        return most <= C::kUncut && static_cast<long long>(live) * units <= gridDim.x ? most + kCost : 0;
+    };
     long long total;
     if (small) {
         cons.s = 0;
         cons.load_group(a, lane);
-        total = static_cast<long long>(make_geo<TK, kCost>(a, cons.ctx_l, cons.pre_l).len) * units;
+        const Geo mine_ = make_geo<TK, kCost>(a, cons.ctx_l, cons.pre_l);
+        if constexpr (kQ8)
+            cons.pad = whole_units(__popc(__ballot_sync(0xffffffffu, mine_.nt > 0)),
+                                   __reduce_max_sync(0xffffffffu, mine_.nt));
+        total = static_cast<long long>(cons.pad && mine_.nt > 0 ? cons.pad : mine_.len) * units;
 #pragma unroll
         for (int o = 16; o > 0; o /= 2) total += __shfl_xor_sync(0xffffffffu, total, o);
         __syncthreads();                              // the barriers are set up
@@ -439,9 +454,30 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, kDup, kQ8>::kCtasPerSm ==
                 ctx[i] = load_ctx(a, threadIdx.x * kPer + i);
                 pre[i] = load_pre(a, threadIdx.x * kPer + i);
             }
+            if constexpr (kQ8) {
+                int live = 0, most = 0;
 #pragma unroll
-            for (int i = 0; i < kPer; ++i)
-                v[i] = static_cast<long long>(make_geo<TK, kCost>(a, ctx[i], pre[i]).len) * units;
+                for (int i = 0; i < kPer; ++i) {
+                    const int nt = make_geo<TK, kCost>(a, ctx[i], pre[i]).nt;
+                    live += nt > 0;
+                    most = max(most, nt);
+                }
+                live = __reduce_add_sync(0xffffffffu, live);
+                most = __reduce_max_sync(0xffffffffu, most);
+                if (lane == 0) prefix[warp] = static_cast<long long>(live) << 32 | most;
+                __syncthreads();                      // (prefix is written after the next one)
+                live = most = 0;
+                for (int w = 0; w < kW; ++w) {
+                    live += static_cast<int>(prefix[w] >> 32);
+                    most = max(most, static_cast<int>(prefix[w]));
+                }
+                cons.pad = whole_units(live, most);
+            }
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const int len = make_geo<TK, kCost>(a, ctx[i], pre[i]).len;
+                v[i] = static_cast<long long>(len && cons.pad ? cons.pad : len) * units;
+            }
         } else
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
@@ -482,7 +518,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, kDup, kQ8>::kCtasPerSm ==
     // piece and its joining of the other pieces' partials take equally long.
     const float mean = static_cast<float>(total) / (static_cast<float>(a.num_seqs) * units);
     const int least = max(kW, static_cast<int>(sqrtf(mean * 0.5f)));
-    const long long ctas = min(static_cast<long long>(gridDim.x), (total + least - 1) / least);
+    const long long ctas =
+        cons.pad ? total / cons.pad : min(static_cast<long long>(gridDim.x), (total + least - 1) / least);
     if (blockIdx.x >= ctas) {
         zero_rows();
         return;
@@ -504,9 +541,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, kDup, kQ8>::kCtasPerSm ==
         for (;;) {
             cons.s = s;
             if ((s & ~31) != cons.base) cons.load_group(a, lane);
-            const long long n = lane >= (s & 31)
-                                    ? static_cast<long long>(make_geo<TK, kCost>(a, cons.ctx_l, cons.pre_l).len) * units
-                                    : 0;
+            const int len = make_geo<TK, kCost>(a, cons.ctx_l, cons.pre_l).len;
+            const long long n = lane >= (s & 31) ? static_cast<long long>(len && cons.pad ? cons.pad : len) * units : 0;
             long long run = n;
 #pragma unroll
             for (int o = 1; o < 32; o *= 2) {
