@@ -71,11 +71,12 @@
 // What bounds it there is the latency of a tile's work with two warps a scheduler, so
 // registers are held to 168 and the merge area to four heads, and three CTAs fit (head_dim
 // 64 and 128, up to 8 heads a K/V head): 128 sequences of 256 to 2048 tokens, 32 heads on 8
-// of 128, bf16, 305 MB: 61.5 us, 5.0 TB/s (69 with two CTAs, also with a third stage of
+// of 128, bf16, 305 MB: 62 us, 4.9 TB/s (69 with two CTAs, also with a third stage of
 // tiles each); 6 sequences of 20001 to 32768 tokens, 16 heads on 8 of 256, capped, 663 MB:
 // 107 us, 6.2 TB/s, 0.93 of the rate of a copy. From L2, where only the work counts, 8 KB
 // take a processor 143 ns (8 heads a K/V head 222, head_dim 64 221, head_dim 256 180);
-// HBM brings them in 186.
+// HBM brings them in 186.  Short contexts are taken whole (whole_units): 50 sequences of 67 to
+// 100 tokens, 8 K/V heads, 9.2 us, cut 15.3.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -96,6 +97,7 @@ constexpr int kW = 4;                  // warps per CTA
 constexpr int kThreads = kW * 32;
 constexpr int kChunks = 512;           // entries of the CTA's prefix over the sequences
 constexpr int kMaxCtas = 640;          // bounds the partial slots (2 per CTA)
+constexpr int kUncutRounds = 8;        // 8-bit caches: see whole_units
 // The reference is raised by scores more than this above it.  The sum is rounded
 // down: past 2^26 fp32's step is 8 and the bias below becomes 8 too, so a score one
 // step above the reference would have a weight of 2^16, past fp16.
@@ -221,24 +223,26 @@ __device__ __forceinline__ int load_pre(const GroupedArgs &a, int s) {
 // A position on the line: tile `idx` of unit `unit` of sequence s.  A unit is
 // one (K/V head, chunk of query heads); the lanes hold the lengths of 32
 // sequences.
-template <int TK, int kCost>
+template <int TK, int kCost, bool kPad>
 struct Cursor {
     int s, unit, idx;
     Geo g;
     int base, ctx_l, pre_l;
-    int pad = 0;               // 0, or what every unit takes of the line
     __device__ __forceinline__ void load_group(const GroupedArgs &a, int lane) {
         base = s & ~31;
         ctx_l = load_ctx(a, base + lane);
         pre_l = load_pre(a, base + lane);
     }
-    __device__ __forceinline__ void set_geo(const GroupedArgs &a) {
+    // pad: 0, or what every unit takes of the line (in shared memory: it is read where a
+    // sequence starts, and a register of the loop otherwise)
+    __device__ __forceinline__ void set_geo(const GroupedArgs &a, const volatile int *pad) {
         g = make_geo<TK, kCost>(a, __shfl_sync(0xffffffffu, ctx_l, s & 31),
                          __shfl_sync(0xffffffffu, pre_l, s & 31));
-        if (pad) g.len = pad;
+        if constexpr (kPad)
+            if (const int all = *pad) g.len = all;
     }
     // The next sequence with tiles (or s = num_seqs, nt = 0).
-    __device__ __forceinline__ void next_seq(const GroupedArgs &a, int lane) {
+    __device__ __forceinline__ void next_seq(const GroupedArgs &a, const volatile int *pad, int lane) {
         ++s;
         unit = 0;
         for (;;) {
@@ -251,17 +255,17 @@ struct Cursor {
             const unsigned rest = __ballot_sync(0xffffffffu, ctx_l > 0) >> (s & 31);
             if (rest) {
                 s += __ffs(rest) - 1;
-                set_geo(a);
+                set_geo(a, pad);
                 return;
             }
             s = base + 32;
         }
     }
-    __device__ __forceinline__ void advance(const GroupedArgs &a, int units, int by, int lane) {
+    __device__ __forceinline__ void advance(const GroupedArgs &a, const volatile int *pad, int units, int by, int lane) {
         idx += by;
         while (idx >= g.len && s < a.num_seqs) {
             idx -= g.len;
-            if (++unit == units) next_seq(a, lane);
+            if (++unit == units) next_seq(a, pad, lane);
         }
     }
 };
@@ -390,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, kDup, kQ8>::kCtasPerSm ==
     long long *prefix = reinterpret_cast<long long *>(smem + C::OFF_PREFIX);
     long long *warp_sum = prefix + kChunks + 1;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_FLAG);
-    volatile int *last_flag = abort_flag + 1;
+    volatile int *last_flag = abort_flag + 1, *pad_slot = abort_flag + 2;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     uint64_t *bar = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR) + warp * C::kStages;
     uint64_t *part_bar = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR) + kW * C::kStages;
@@ -423,13 +427,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, kDup, kQ8>::kCtasPerSm ==
 
     // The line's length, and prefix[c], the tiles of the sequences before chunk
     // c.  Up to 32 sequences need no prefix: a warp's lanes hold them.
-    Cursor<TK, kCost> cons;
+    Cursor<TK, kCost, kQ8> cons;
     cons.base = -1;
     const bool small = a.num_seqs <= 32;
-    // 8-bit caches, few short contexts: a unit to a CTA, whole, by taking all of them for
-    // as long as the longest.  (Cut, they cost a partial, a ticket and a join.)
-    [[maybe_unused]] auto whole_units = [&](int live, int most) {
-        return most <= C::kUncut && static_cast<long long>(live) * units <= gridDim.x ? most + kCost : 0;
+    int pad = 0;
+    // 8-bit caches, short contexts (live of them, the longest of `most` tiles, `sum` in all): as
+    // many whole units to a CTA as to every other, by taking all of them for as long as the
+    // longest.  (Cut, they cost a partial, a ticket and a join.)  More than one to a CTA
+    // only where that is within a quarter of what they are.
+    [[maybe_unused]] auto whole_units = [&](int live, int most, int sum) {
+        const long long all = static_cast<long long>(live) * units;
+        const bool even = static_cast<long long>(most + kCost) * live * 4 <= (sum + static_cast<long long>(kCost) * live) * 5;
+        return most <= C::kUncut && (all <= gridDim.x || (even && all <= kUncutRounds * gridDim.x)) ? most + kCost : 0;
     };
     long long total;
     if (small) {
@@ -437,11 +446,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, kDup, kQ8>::kCtasPerSm ==
         cons.load_group(a, lane);
         const Geo mine_ = make_geo<TK, kCost>(a, cons.ctx_l, cons.pre_l);
         if constexpr (kQ8)
-            cons.pad = whole_units(__popc(__ballot_sync(0xffffffffu, mine_.nt > 0)),
-                                   __reduce_max_sync(0xffffffffu, mine_.nt));
-        total = static_cast<long long>(cons.pad && mine_.nt > 0 ? cons.pad : mine_.len) * units;
+            pad = whole_units(__popc(__ballot_sync(0xffffffffu, mine_.nt > 0)),
+                                   __reduce_max_sync(0xffffffffu, mine_.nt),
+                                   __reduce_add_sync(0xffffffffu, min(mine_.nt, C::kUncut + 1)));
+        total = static_cast<long long>(pad && mine_.nt > 0 ? pad : mine_.len) * units;
 #pragma unroll
         for (int o = 16; o > 0; o /= 2) total += __shfl_xor_sync(0xffffffffu, total, o);
+        if (kQ8 && threadIdx.x == 0) *pad_slot = pad;
         __syncthreads();                              // the barriers are set up
     } else {
         constexpr int kPer = kChunks / kThreads;      // neighbouring entries per thread
@@ -455,28 +466,34 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, kDup, kQ8>::kCtasPerSm ==
                 pre[i] = load_pre(a, threadIdx.x * kPer + i);
             }
             if constexpr (kQ8) {
-                int live = 0, most = 0;
+                int live = 0, most = 0, sum_nt = 0;
 #pragma unroll
                 for (int i = 0; i < kPer; ++i) {
                     const int nt = make_geo<TK, kCost>(a, ctx[i], pre[i]).nt;
                     live += nt > 0;
                     most = max(most, nt);
+                    sum_nt += min(nt, C::kUncut + 1);
                 }
+                sum_nt = __reduce_add_sync(0xffffffffu, sum_nt);
                 live = __reduce_add_sync(0xffffffffu, live);
                 most = __reduce_max_sync(0xffffffffu, most);
-                if (lane == 0) prefix[warp] = static_cast<long long>(live) << 32 | most;
+                if (lane == 0) {
+                    prefix[warp] = static_cast<long long>(live) << 32 | most;
+                    prefix[kW + warp] = sum_nt;
+                }
                 __syncthreads();                      // (prefix is written after the next one)
-                live = most = 0;
+                live = most = sum_nt = 0;
                 for (int w = 0; w < kW; ++w) {
                     live += static_cast<int>(prefix[w] >> 32);
                     most = max(most, static_cast<int>(prefix[w]));
+                    sum_nt += static_cast<int>(prefix[kW + w]);
                 }
-                cons.pad = whole_units(live, most);
+                pad = whole_units(live, most, sum_nt);
             }
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
                 const int len = make_geo<TK, kCost>(a, ctx[i], pre[i]).len;
-                v[i] = static_cast<long long>(len && cons.pad ? cons.pad : len) * units;
+                v[i] = static_cast<long long>(len && pad ? pad : len) * units;
             }
         } else
 #pragma unroll
@@ -503,6 +520,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, kDup, kQ8>::kCtasPerSm ==
             if (lane >= o) run += t;
         }
         if (lane == 31) warp_sum[warp] = run;
+        if (kQ8 && threadIdx.x == 0) *pad_slot = pad;
         __syncthreads();
         run -= sum;
         for (int w = 0; w < warp; ++w) run += warp_sum[w];
@@ -518,13 +536,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, kDup, kQ8>::kCtasPerSm ==
     // piece and its joining of the other pieces' partials take equally long.
     const float mean = static_cast<float>(total) / (static_cast<float>(a.num_seqs) * units);
     const int least = max(kW, static_cast<int>(sqrtf(mean * 0.5f)));
-    const long long ctas =
-        cons.pad ? total / cons.pad : min(static_cast<long long>(gridDim.x), (total + least - 1) / least);
+    long long ctas = min(static_cast<long long>(gridDim.x), (total + least - 1) / least), share = 0;
+    if (pad) {   // whole units
+        share = (total / pad + gridDim.x - 1) / gridDim.x * pad;
+        ctas = share ? (total + share - 1) / share : 0;
+    }
     if (blockIdx.x >= ctas) {
         zero_rows();
         return;
     }
-    const long long f0 = blockIdx.x * total / ctas, f1 = (blockIdx.x + 1) * total / ctas;
+    const long long f0 = share ? blockIdx.x * share : blockIdx.x * total / ctas;
+    const long long f1 = share ? min(total, f0 + share) : (blockIdx.x + 1) * total / ctas;
     const int mine = static_cast<int>(f1 - f0);       // tiles of this CTA
 
     // the piece's start: its prefix entry, then its sequence within the entry
@@ -542,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, kDup, kQ8>::kCtasPerSm ==
             cons.s = s;
             if ((s & ~31) != cons.base) cons.load_group(a, lane);
             const int len = make_geo<TK, kCost>(a, cons.ctx_l, cons.pre_l).len;
-            const long long n = lane >= (s & 31) ? static_cast<long long>(len && cons.pad ? cons.pad : len) * units : 0;
+            const long long n = lane >= (s & 31) ? static_cast<long long>(len && pad ? pad : len) * units : 0;
             long long run = n;
 #pragma unroll
             for (int o = 1; o < 32; o *= 2) {
@@ -554,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, kDup, kQ8>::kCtasPerSm ==
                 const int l = __ffs(past) - 1;
                 r -= __shfl_sync(0xffffffffu, run - n, l);
                 cons.s = cons.base + l;
-                cons.set_geo(a);
+                cons.set_geo(a, pad_slot);
                 cons.unit = static_cast<int>(r / cons.g.len);
                 cons.idx = static_cast<int>(r - static_cast<long long>(cons.unit) * cons.g.len);
                 break;
@@ -573,14 +595,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, kDup, kQ8>::kCtasPerSm ==
     const int RB = kQ8 ? min(B, TK) : (B == 8 ? 8 : 16);
     const int rb_shift = RB == 8 ? 3 : (RB == 16 ? 4 : 5), b_shift = B == 8 ? 3 : (B == 16 ? 4 : 5);
     const int boxes = TK / RB;
-    Cursor<TK, kCost> prod = cons;
+    Cursor<TK, kCost, kQ8> prod = cons;
     int at = 0;                              // tile of the piece `prod` is at
     // the lane's box of tile `at`: physical block (-1: not needed, -2: needed
     // but its entry is bad) and row within the block
     int box_blk = -1, box_row = 0;
     auto look_up = [&](int tile) {           // moves to the warp's first tile from `tile` on
         while (tile < mine) {
-            prod.advance(a, units, tile - at, lane);
+            prod.advance(a, pad_slot, units, tile - at, lane);
             at = tile;
             if (prod.idx < prod.g.nt) break;
             tile += kW;
@@ -735,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, kDup, kQ8>::kCtasPerSm ==
             seg_start += seg_len;
             cons.idx += seg_len;
             if (seg_start < mine) {
-                cons.advance(a, units, 0, lane);
+                cons.advance(a, pad_slot, units, 0, lane);
                 load_q();
             }
             continue;
@@ -1032,7 +1054,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, kDup, kQ8>::kCtasPerSm ==
         seg_start += seg_len;
         cons.idx += seg_len;
         if (seg_start < mine) {
-            cons.advance(a, units, 0, lane);
+            cons.advance(a, pad_slot, units, 0, lane);
             load_q();
         }
         constexpr int kVec = D / 4;            // float4s per head

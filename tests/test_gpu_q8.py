@@ -478,6 +478,25 @@ def test_decode_long_and_many(dev):
     decode(make_q8_case(29, ctx, [1] * 3000, 2, 1, 64, 16, F16), dev)
 
 
+@pytest.mark.parametrize("S,heads,lo,hi,D", [(50, (16, 8), 60, 100, 128), (150, (8, 4), 90, 100, 128),
+                                             (500, (9, 3), 50, 64, 64), (512, (10, 1), 1, 33, 128),
+                                             (31, (6, 2), 1, 320, 256), (90, (40, 8), 120, 130, 64)])
+def test_decode_short_contexts(dev, S, heads, lo, hi, D):
+    """Whole contexts to a CTA, one or several, some empty; and one that is too long for it."""
+    g = torch.Generator().manual_seed(S)
+    ctx = torch.randint(lo, hi + 1, (S,), generator=g).tolist()
+    decode(make_q8_case(33, ctx, [1] * S, *heads, D, 16, BF16), dev)
+    ctx[S // 2] = ctx[1] = 0
+    c = make_q8_case(34, ctx, [1] * S, *heads, D, 16, F16, window=40, prefix=[3] * S, cap=9.0)
+    decode(c, dev)
+    ctx[S - 1] = 1500
+    decode(make_q8_case(35, ctx, [1] * S, *heads, D, 16, F16, alibi=True), dev)
+    d = to_dev(c, dev)
+    d["lens"][:] = 0
+    out = run_decode(c, d)
+    assert pa.device_errors() == 0 and (out == 0).all()
+
+
 @pytest.mark.parametrize("q_scale", [1e-30, 1e-3, 1e4, 1e30])
 def test_decode_sizes_of_queries(dev, q_scale):
     """bf16 queries of any size go through fp16 products: a scale that undoes theirs
