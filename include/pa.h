@@ -651,9 +651,10 @@ int pa_gather_cache_q8(void *k_out, void *v_out, const void *k_cache, const void
  * The numbers are widened exactly on the way to the products, scores are fp32 and
  * get k_scales[h], outputs v_scales[h], in fp32.  The products run on fp16 operands
  * whatever the type of q and out: a bf16 query row is first scaled by a power of two
- * that brings its largest element to [2^10, 2^11), which moves no element down to
- * 2^-27 of the largest and lower ones by at most 2^-35 of it; and the prefill's
- * weights are rounded to fp16.
+ * that brings its largest element to [2^10, 2^11) (a row below 2^-116 by 2^126), which
+ * moves no element down to 2^-27 of the largest and lower ones by at most 2^-35 of it.
+ * What undoes that is one factor with scale and k_scales[h].  The prefill's weights are
+ * rounded to fp16.
  */
 int pa_decode_grouped_q8(void *out, const void *q, const void *k_cache, const void *v_cache,
                          const float *k_scales, const float *v_scales, const int32_t *block_tables,

@@ -679,7 +679,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, kDup, kQ8>::kCtasPerSm ==
 
     uint32_t qf[KS][NT][2];
     float m[NT][2], l[NT][2], o[KS][NT][4], slope[NT][2];
-    float qs[NT][2];                         // 8-bit caches: what a column's scores are short of
+    // 8-bit caches: what turns a column's products into x, or with a cap into v: the head's
+    // scale and what its q is short of, times scale_log2 or cap_v
+    float qs[NT][2];
     bool ok = true;
     int n_done = 0;                          // tiles taken
     int seg_start = 0;                       // CTA tile at which the segment starts
@@ -699,11 +701,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, kDup, kQ8>::kCtasPerSm ==
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks)
                     raw[ks] = live ? src2[(hq * D + ks * 16) / 4 + (lane & 3)] : make_uint2(0u, 0u);
-                float f = live ? a.k_scales[hk] : 0.f;
+                float up = 1.f;
                 if (p.io_bf16) {
-                    // to fp16, by a power of two that brings the row's largest element to
-                    // [2^10, 2^11): bf16's exponents do not fit, its 8 bits do
-                    float top = 0.f;
+                    float top = 0.f, down;
 #pragma unroll
                     for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
@@ -713,9 +713,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, kDup, kQ8>::kCtasPerSm ==
                         }
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                    const int e = max(static_cast<int>(__float_as_uint(top) >> 23) - 137, -100);
-                    const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-                    f *= __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+                    fp16_row_factors(top, down, up);
 #pragma unroll
                     for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
@@ -728,6 +726,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, kDup, kQ8>::kCtasPerSm ==
 #pragma unroll
                     for (int ks = 0; ks < KS; ++ks) qf[ks][nt][0] = raw[ks].x, qf[ks][nt][1] = raw[ks].y;
                 }
+                const float f = product3(up, live ? a.k_scales[hk] : 0.f, a.softcap > 0.f ? p.cap_v : p.scale_log2);
                 // the factors of the lane's two columns, from the lanes that hold these heads
                 qs[nt][0] = __shfl_sync(0xffffffffu, f, 4 * col);
                 qs[nt][1] = __shfl_sync(0xffffffffu, f, 4 * col + 4);
@@ -846,7 +845,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, kDup, kQ8>::kCtasPerSm ==
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             if constexpr (kQ8) sc[mt][nt][e] *= qs[nt][e & 1];
-                            const float v = sc[mt][nt][e] * p.cap_v;
+                            const float v = kQ8 ? sc[mt][nt][e] : sc[mt][nt][e] * p.cap_v;
                             far |= !(v * v < 2.f);
                         }
                 far = __any_sync(0xffffffffu, far);
@@ -857,13 +856,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, kDup, kQ8>::kCtasPerSm ==
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             float &x = sc[mt][nt][e];
-                            const float s = x, v = x * p.cap_v, w = v * v;
+                            const float v = kQ8 ? x : x * p.cap_v, w = v * v;
+                            const float turn = kQ8 ? v * kCapInPerV : x * p.cap_in;
                             float y = p.tanh_k[4];
 #pragma unroll
                             for (int i = 3; i >= 0; --i) y = fmaf(y, w, p.tanh_k[i]);
                             x = v * y;
                             if (far && !(w < 2.f))
-                                x = p.cap_log2 - 2.f * p.cap_log2 * fast_rcp(1.f + fast_exp2(s * p.cap_in));
+                                x = p.cap_log2 - 2.f * p.cap_log2 * fast_rcp(1.f + fast_exp2(turn));
                         }
             } else {
 #pragma unroll
@@ -871,7 +871,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, kDup, kQ8>::kCtasPerSm ==
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) sc[mt][nt][e] *= kQ8 ? p.scale_log2 * qs[nt][e & 1] : p.scale_log2;
+                        for (int e = 0; e < 4; ++e) sc[mt][nt][e] *= kQ8 ? qs[nt][e & 1] : p.scale_log2;
             }
             // (bias and mask as steps of their own: as conditions of one, every tile paid for
             // both)

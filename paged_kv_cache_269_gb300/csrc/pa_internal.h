@@ -165,10 +165,11 @@ struct GroupedArgs {
 // value and 4e-7 in all, as one of degree 11 would be up to u = 1.  That term
 // is a step of the softmax more for every score; scores that far out take the
 // exponential form instead.
+constexpr double kTanhUPerV = 0.53033008588991064;   // 0.75 / sqrt(2)
 inline void fill_tanh(float scale, float softcap, float *cap_v, float (&k)[5]) {
     const double tanh_u[5] = {0.99999943500438748, -0.33328250820635219, 0.13258976152428414,
                               -0.050056102813472059, 0.012929458742386161};
-    const double u_over_v = 0.53033008588991064, log2e = 1.4426950408889634;
+    const double u_over_v = kTanhUPerV, log2e = 1.4426950408889634;
     *cap_v = softcap > 0.f ? static_cast<float>(scale / u_over_v / softcap) : 0.f;
     double power = softcap * log2e * u_over_v;
     for (int i = 0; i < 5; ++i, power *= u_over_v * u_over_v)

@@ -841,9 +841,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             pending = -1;
         };
-        // Item k's Q, where it has to be made fp16: each row by a power of two that brings
-        // its largest element to [2^10, 2^11), since bf16's exponents do not fit and its 8
-        // bits do.  A thread takes its own row: while the item before waits for its last
+        // Item k's Q, where it has to be made fp16, each row by a power of two of its own
+        // (fp16_row_factors).  A thread takes its own row: while the item before waits for its last
         // product, if Q is there by then, and else after that item's output (waiting for it
         // first cost 16 prompts of 333 to 1024 tokens 114 us instead of 108).  q_factor: what
         // the row's scores are short of.
@@ -872,9 +871,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         most = __hmax2(most, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&u[z])));
                 }
                 const float top = fmaxf(__low2float(most), __high2float(most));
-                const int e = max(static_cast<int>(__float_as_uint(top) >> 23) - 137, -100);
-                const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-                q_factor = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+                float down;
+                fp16_row_factors(top, down, q_factor);
 #pragma unroll
                 for (int i = 0; i < D / 8; ++i) {
                     uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
@@ -932,11 +930,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int pre_all = it->pre, na = it->na, skip = it->skip, j0 = it->j0;
             const int last = j0 + max(nk, 0) - 1;
             if constexpr (kQ8) {
-                const float f = __ldg(a.k_scales + it->hk) * (kScaleQ ? q_factor : 1.f);
-                c = p.scale_log2 * f;
+                const float f = __ldg(a.k_scales + it->hk), up = kScaleQ ? q_factor : 1.f;
+                c = product3(up, f, p.scale_log2);
                 if constexpr (kCap) {
-                    cap_v = p.cap_v * f;
-                    cap_in = p.cap_in * f;
+                    cap_v = product3(up, f, p.cap_v);
+                    cap_in = kCapInPerV * cap_v;
                     cap_v2 = keep_pair(cap_v);
                 }
             }
