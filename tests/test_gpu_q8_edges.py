@@ -1,14 +1,15 @@
-"""GPU tests of the 8-bit cache's calls at the ends of their ranges.  References and
-bounds as in q8_ref and grouped_ref."""
+"""GPU tests of the 8-bit cache's calls at the ends of their ranges and where their
+kernels change form.  References and bounds as in q8_ref and grouped_ref."""
 import pytest
 import torch
 
 import paged_kv_cache_269_gb300 as pa
-from q8_ref import make_q8_case, refresh
+from q8_ref import E4M3, make_q8_case, refresh, scales_for
 from test_gpu_q8 import decode, prefill
 
 pytestmark = pytest.mark.gpu
 F16, BF16 = torch.float16, torch.bfloat16
+BYTE = torch.uint8
 
 
 @pytest.fixture(scope="module")
@@ -20,6 +21,10 @@ def dev():
     pa.lib()
     pa.device_errors()
     return d
+
+
+def processors(dev):
+    return torch.cuda.get_device_properties(dev).multi_processor_count
 
 
 # ------------------------------------------------------------------ sizes of queries
@@ -59,3 +64,56 @@ def test_prefill_of_the_smallest_queries(dev, down, cap):
     c.q[7] = 0.0
     c.q[11, 2, 5] = 2.0 ** (7 - down)
     prefill(c, dev)
+
+
+# ------------------------------------------------------------------ read-backs that fill the device
+
+def gather_case(seed, T, H, D, B, dtype, offset, dev, bad=None):
+    """Random codes and slots, outputs that start `offset` elements past a 256-byte line;
+    checked bit for bit against the definition, and what must not be written."""
+    g = torch.Generator(device=dev).manual_seed(seed)
+    N = 37
+    kc, vc = (torch.randint(0, 256, (N, H, B, D), generator=g, device=dev).to(BYTE).view(E4M3) for _ in range(2))
+    ks, vs = scales_for(1, H).to(dev), scales_for(2, H).to(dev)
+    slots = torch.randint(-3, N * B, (T,), generator=g, device=dev).to(torch.int32)
+    if bad is not None:
+        slots[bad] = N * B
+    base = [torch.full((T * H * D + 128,), -3.5, dtype=dtype, device=dev) for _ in range(2)]
+    assert all(b.data_ptr() % 256 == 0 for b in base)
+    ko, vo = (b[offset:offset + T * H * D].view(T, H, D) for b in base)
+    pa.gather_cache_q8(ko, vo, kc, vc, ks, vs, slots)
+    assert pa.device_errors() == (0 if bad is None else pa.DEVERR_SLOT)
+    keep = (slots >= 0) & (slots < N * B)
+    at = slots.clamp(0, N * B - 1).long()
+    for o, b, c, s in ((ko, base[0], kc, ks), (vo, base[1], vc, vs)):
+        want = (c.view(BYTE)[at // B, :, at % B].view(E4M3).float() * s[:, None]).to(dtype)
+        want[~keep] = -3.5
+        assert torch.equal(o.isnan(), want.isnan())
+        assert torch.equal(o.nan_to_num(0.0).view(torch.int16), want.nan_to_num(0.0).view(torch.int16))
+        assert (b[:offset] == -3.5).all() and (b[offset + T * H * D:] == -3.5).all()
+
+
+def full_tokens(dev, H, D):
+    """The tokens past which a read-back takes four chunks of 16 numbers a thread: the device
+    is full of threads (8 CTAs of 256 a processor) by then."""
+    return 8 * 256 * processors(dev) * 16 // (2 * H * D)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("H,D,B", [(1, 64, 16), (3, 64, 8), (5, 128, 16), (8, 128, 32), (3, 256, 32), (8, 256, 8), (40, 128, 16)])
+@pytest.mark.parametrize("offset", [0, 8, 16, 24])
+def test_gather_that_fills_the_device(dev, dtype, H, D, B, offset):
+    # (offsets of 8 and 24 elements: rows on 16-byte and not on 32-byte lines)
+    T = full_tokens(dev, H, D) + 1
+    assert 2 * T * H * D // 16 > 8 * 256 * processors(dev)
+    gather_case(1, T + 36, H, D, B, dtype, offset, dev, bad=T)
+    if offset == 0:
+        gather_case(2, T, H, D, B, dtype, offset, dev)
+        gather_case(3, T - 1, H, D, B, dtype, offset, dev)      # the last with one chunk
+
+
+@pytest.mark.parametrize("offset", [0, 8, 16, 24])
+@pytest.mark.parametrize("T", [1, 7, 301])
+def test_gather_to_any_aligned_output(dev, T, offset):
+    gather_case(4, T, 3, 64, 16, F16, offset, dev)
+    gather_case(5, T, 2, 128, 16, BF16, offset, dev, bad=T - 1)
