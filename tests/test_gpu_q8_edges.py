@@ -5,7 +5,7 @@ import torch
 
 import paged_kv_cache_269_gb300 as pa
 from q8_ref import E4M3, make_q8_case, refresh, scales_for
-from test_gpu_q8 import decode, prefill
+from test_gpu_q8 import check, decode, prefill, run_prefill, to_dev
 
 pytestmark = pytest.mark.gpu
 F16, BF16 = torch.float16, torch.bfloat16
@@ -64,6 +64,107 @@ def test_prefill_of_the_smallest_queries(dev, down, cap):
     c.q[7] = 0.0
     c.q[11, 2, 5] = 2.0 ** (7 - down)
     prefill(c, dev)
+
+
+# ------------------------------------------------------------------ the prefill's queue
+
+def items(c):
+    """Work items of a prefill without key splits: pairs of tiles of the longest query, for
+    every sequence and K/V head."""
+    pair = 2 * (128 // (c.q_heads // c.kv_heads))
+    return -(-max(c.new) // pair) * len(c.ctx) * c.kv_heads
+
+
+def assert_ordered(c, dev, ordered=True):
+    """Items are taken by falling numbers of keys with up to 32 sequences, no distance bias
+    and one to four rounds of processors."""
+    n, sms = items(c), processors(dev)
+    assert (sms < n <= 4 * sms and 1 < len(c.ctx) <= 32) == ordered and n > sms, (n, sms)
+
+
+CTX = [900, 1500, 33, 1500, 0, 1200, 700]
+NEW = [900, 300, 33, 1500, 0, 257, 1]
+
+
+@pytest.mark.parametrize("heads,B,dtype", [((8, 8), 16, F16), ((12, 4), 8, BF16), ((14, 7), 32, BF16)])
+def test_prefill_in_order_of_keys(dev, heads, B, dtype):
+    c = make_q8_case(211, CTX, NEW, *heads, 64, B, dtype)
+    assert_ordered(c, dev)
+    prefill(c, dev)
+    c = make_q8_case(212, CTX, NEW, *heads, 128, B, dtype, window=300, prefix=[0, 40, 5, 0, 0, 1000, 3], cap=9.0)
+    assert_ordered(c, dev)
+    prefill(c, dev)
+
+
+@pytest.mark.parametrize("heads", [(16, 16), (24, 8)])
+def test_prefill_by_levels_past_four_rounds(dev, heads):
+    c = make_q8_case(213, CTX, NEW, *heads, 64, 16, F16)
+    assert_ordered(c, dev, ordered=False)
+    prefill(c, dev)
+
+
+@pytest.mark.parametrize("ctx,new", [
+    ([512] * 5, [512] * 5),                                     # every end in every sequence
+    ([0, 700, 700, 0, 444, 700, 0], [0, 700, 444, 0, 444, 1, 0]),   # the first and the last are empty
+    ([768, 512, 1024, 256, 1280], [768, 512, 1024, 256, 1280]),     # whole pairs: all ends meet
+    ([2000, 1, 1999, 1], [1000, 1, 999, 1])])
+def test_prefill_in_order_of_ends_that_meet(dev, ctx, new):
+    S = len(ctx)
+    H = -(-(processors(dev) + 1) // (-(-max(new) // 256) * S))
+    c = make_q8_case(214, ctx, new, H, H, 64, 16, BF16)
+    assert_ordered(c, dev)
+    prefill(c, dev)
+
+
+def test_prefill_in_order_of_32_sequences(dev):
+    g = torch.Generator().manual_seed(5)
+    ctx = torch.randint(1, 200, (32,), generator=g).tolist()
+    ctx[31] = 500
+    new = [min(c, int(n)) for c, n in zip(ctx, torch.randint(0, 200, (32,), generator=g))]
+    new[31] = 500
+    c = make_q8_case(215, ctx, new, 4, 2, 64, 16, F16)
+    assert_ordered(c, dev)
+    prefill(c, dev)
+
+
+@pytest.mark.parametrize("who", [0, 3, 6])
+@pytest.mark.parametrize("fault", ["short", "long", "rows", "longest"])
+def test_prefill_in_order_with_a_rejected_sequence(dev, who, fault):
+    """A sequence whose lengths are inconsistent is flagged and its rows are left; the
+    others' rows are what they are without it, to the bit."""
+    ctx = [900, 1500, 33, 1300, 0, 1200, 1000]
+    new = [700, 300, 33, 701, 0, 257, 650]
+    if fault == "longest":
+        new[who] = 768                                # alone past max_query_len
+    c = make_q8_case(216, ctx, new, 12, 12, 64, 16, BF16)
+    d = to_dev(c, dev)
+    assert_ordered(c, dev)
+    good = run_prefill(c, d).cpu()
+    assert pa.device_errors() == 0
+    check(c, good, True)
+    last = len(ctx) - 1
+    kw = {}
+    lost = {who}
+    if fault == "short":
+        d["lens"][who] = new[who] - 1
+    elif fault == "long":
+        d["lens"][who] = d["tables"].shape[1] * 16 + 1
+    elif fault == "longest":
+        kw["max_query_len"] = 767
+    elif who == last:
+        d["starts"][last + 1] += 1                    # a row past the last
+    else:                                             # an end before its start, and what follows from it
+        d["starts"][who + 1] = d["starts"][who] - 1
+        lost = {who, who + 1}
+        d["lens"][who + 1] = min(ctx[who + 1], new[who])    # shorter than the rows it now has
+    out = torch.full_like(d["q"], 5.0)
+    run_prefill(c, d, out, **kw)
+    assert pa.device_errors() == pa.DEVERR_CONTEXT
+    pa.reset_workspaces()
+    out = out.cpu()
+    for s in range(len(ctx)):
+        r0, r1 = c.starts_list[s], c.starts_list[s + 1]
+        assert (out[r0:r1] == 5).all() if s in lost else torch.equal(out[r0:r1], good[r0:r1]), s
 
 
 # ------------------------------------------------------------------ read-backs that fill the device
