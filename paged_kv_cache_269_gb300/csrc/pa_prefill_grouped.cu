@@ -1240,9 +1240,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             } else if constexpr (kSplit) {
+                // The thread's place, at head_dim 128 read again: kept from the kernel's start,
+                // what is reckoned from it for this part holds registers in the loop above (4
+                // tokens over 32000 keys, 16 bits: 42.6 us so kept, 41.3 so; spills too).
+                int tid = threadIdx.x;
+                if constexpr (D == 128) asm volatile("mov.u32 %0, %%tid.x;" : "=r"(tid));
+                const int place = tid % 32, quarter = tid / 32 % 4;
                 // a partial: [split][tile][D + 2][128 rows]
                 constexpr size_t kPart = static_cast<size_t>(D + 2) * kBM;
-                float *base = p.partials + (static_cast<size_t>(it->slot) * p.splits * 2 + t) * kPart + r;
+                float *base = p.partials + (static_cast<size_t>(it->slot) * p.splits * 2 + t) * kPart + quarter * 32 + place;
                 float *mine = base + static_cast<size_t>(it->split) * 2 * kPart;
 #pragma unroll
                 for (int q = 0; q < D / 32; ++q) {
@@ -1265,11 +1271,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // a few rows kept one warp: 4 tokens of 8 heads took 44 us over 32000
                 // keys, and take 30).
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar[C::PARTS + t]);
-                if (warp % 4 == 0) {
+                if (place == 0) mbar_arrive(&bar[C::PARTS + t]);
+                if (quarter == 0) {
                     ok = warp_all(mbar_wait(&bar[C::PARTS + t], (it->joins >> t) & 1, abort_flag, a.err));
                     if (!ok) break;
-                    if (lane == 0) {
+                    if (place == 0) {
                         uint32_t *ticket = a.counters + 2 + it->slot * 2 + t;
                         const bool last = ticket_add(ticket, 1u) == static_cast<uint32_t>(splits - 1);
                         if (last) atomicExch(ticket, 0u);
@@ -1281,8 +1287,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 const int ntok = min(p.tpt, it->q_len - it->tok0 - t * p.tpt);
                 for (int r0 = 0; last_flag[t] && r0 < ntok * p.group; r0 += 32) {
-                    const int rr = min(r0 + lane, ntok * p.group - 1);
-                    const float *rows = base - r + rr;
+                    const int rr = min(r0 + place, ntok * p.group - 1);
+                    const float *rows = base - (quarter * 32 + place) + rr;
                     uint16_t *dst = a.out + (static_cast<size_t>(it->q_first + it->tok0 + t * p.tpt + rr / p.group) *
                                                  a.num_q_heads + it->hk * p.group + rr % p.group) * D;
                     // four splits at a time, so that their loads share a round trip
@@ -1292,11 +1298,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         return rows + static_cast<size_t>(min(z, splits - 1)) * 2 * kPart;
                     };
                     // Up to kZ splits: everything a row needs in one round trip, in the order of
-                    // the loop below (3 chunks of up to 17 tokens of 4 heads over 640 keys: 13.2 us
-                    // so, 13.9 by the loop).
-                    if (splits <= kZ) {
+                    // the loop below (3 chunks of up to 17 tokens of 4 heads over 640 keys: 15.4 us
+                    // so, 16.9 by the loop; over 8 bits 16.3 and 17.9, at head_dim 64 12.9 and 14.4,
+                    // but over 16 bits 14.0 and 13.6, so not there).
+                    if ((kQ8 || D == 128) && splits <= kZ) {
                         constexpr int kDims = D / 4;
-                        const int d0 = warp % 4 * kDims;
+                        const int d0 = quarter * kDims;
                         float mz[kZ], lz[kZ], v[kZ][kDims];
 #pragma unroll
                         for (int z = 0; z < kZ; ++z) {
@@ -1315,7 +1322,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         float inv = total > 0.f ? 1.f / total : 0.f;
                         if constexpr (kQ8) inv *= __ldg(a.v_scales + it->hk);
-                        if (r0 + lane < ntok * p.group) {
+                        if (r0 + place < ntok * p.group) {
 #pragma unroll
                             for (int e = 0; e < kDims; e += 8) {
                                 uint4 out;
@@ -1354,7 +1361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float inv = total > 0.f ? 1.f / total : 0.f;
                     if constexpr (kQ8) inv *= __ldg(a.v_scales + it->hk);
 #pragma unroll 1
-                    for (int d0 = warp % 4 * (D / 4); d0 < (warp % 4 + 1) * (D / 4); d0 += 16) {
+                    for (int d0 = quarter * (D / 4); d0 < (quarter + 1) * (D / 4); d0 += 16) {
                         float acc[16];
 #pragma unroll
                         for (int e = 0; e < 16; ++e) acc[e] = 0.f;
@@ -1374,7 +1381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 for (int e = 0; e < 16; ++e) acc[e] += f[z] * v[z][e];
                             }
                         }
-                        if (r0 + lane < ntok * p.group) {
+                        if (r0 + place < ntok * p.group) {
 #pragma unroll
                             for (int e = 0; e < 16; e += 8) {
                                 uint4 v;

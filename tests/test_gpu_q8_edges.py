@@ -1,9 +1,13 @@
 """GPU tests of the 8-bit cache's calls at the ends of their ranges and where their
 kernels change form.  References and bounds as in q8_ref and grouped_ref."""
+import math
+
 import pytest
 import torch
 
 import paged_kv_cache_269_gb300 as pa
+import test_gpu_grouped
+from grouped_ref import make_case
 from q8_ref import E4M3, make_q8_case, refresh, scales_for
 from test_gpu_q8 import check, decode, prefill, run_prefill, to_dev
 
@@ -165,6 +169,35 @@ def test_prefill_in_order_with_a_rejected_sequence(dev, who, fault):
     for s in range(len(ctx)):
         r0, r1 = c.starts_list[s], c.starts_list[s + 1]
         assert (out[r0:r1] == 5).all() if s in lost else torch.equal(out[r0:r1], good[r0:r1]), s
+
+
+# ------------------------------------------------------------------ joins of key splits
+
+def parts(ctx, splits):
+    """Parts that the item of a few queries over ctx keys is split into: one for every
+    sqrt(n / 2) of its n tiles of 128 keys, of two such tiles at least."""
+    count = -(-ctx // 64)
+    per = math.ceil(2 * max(2.0, math.sqrt(count / 4)))
+    return min(splits, -(-count // per))
+
+
+@pytest.mark.parametrize("bits", [8, 16])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("cap,alibi", [(0.0, False), (20.0, True)])
+def test_prefill_joins_few_and_many_splits(dev, bits, dtype, D, cap, alibi):
+    """Up to four parts are joined in one round trip, more in a loop: items of 1 to 7 parts in
+    one call, rows that end within a warp's, several warps' and a second tile's."""
+    ctx = [60, 512, 700, 1024, 1300, 1600, 2300, 3200]
+    assert [parts(n, 152 // len(ctx)) for n in ctx] == [1, 2, 3, 4, 5, 5, 6, 7]
+    for new, heads in (([3, 1, 5, 2, 6, 1, 4, 5], (5, 1)), ([60, 43, 1, 40, 17, 33, 5, 16], (3, 1))):
+        if bits == 8:
+            prefill(make_q8_case(221, ctx, new, *heads, D, 16, dtype, cap=cap, alibi=alibi), dev)
+        else:
+            c = make_case(222, ctx, new, *heads, D, 16, dtype, cap=cap, alibi=alibi)
+            got = test_gpu_grouped.run_prefill(c, test_gpu_grouped.to_dev(c, dev))
+            assert pa.device_errors() == 0
+            check(c, got, True)
 
 
 # ------------------------------------------------------------------ read-backs that fill the device
