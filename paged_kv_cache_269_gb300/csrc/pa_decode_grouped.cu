@@ -432,13 +432,25 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, kDup, kQ8>::kCtasPerSm ==
     const bool small = a.num_seqs <= 32;
     int pad = 0;
     // 8-bit caches, short contexts (live of them, the longest of `most` tiles, `sum` in all): as
-    // many whole units to a CTA as to every other, by taking all of them for as long as the
-    // longest.  (Cut, they cost a partial, a ticket and a join.)  More than one to a CTA
-    // only where that is within a quarter of what they are.
+    // many whole units to a CTA as to every other (`rounds`), by taking all of them for as
+    // long as the longest.  (Cut, they cost a partial, a ticket and a join.)  More than one
+    // to a CTA only where that is within a quarter of what they are, and where the last round
+    // leaves the CTAs little to stand idle for: 16 tiles' time each on average, 13.5 from a
+    // third round on, and a tile's time for 512 numbers of a unit's output, which a cut would
+    // write and read again.  5 to 8 heads of 64, 12 tiles: 1.05 rounds 23.2 us cut and 21.8
+    // whole, 2.05 rounds 31.3 and 32.6; of 256: 2.05 rounds 31.4 and 30.4; 4 heads of 256, 20
+    // tiles: 1.05 rounds 24.1 and 25.8, 1.9 rounds 32.7 and 27.8.
+    [[maybe_unused]] int rounds = 1;
     [[maybe_unused]] auto whole_units = [&](int live, int most, int sum) {
-        const long long all = static_cast<long long>(live) * units;
-        const bool even = static_cast<long long>(most + kCost) * live * 4 <= (sum + static_cast<long long>(kCost) * live) * 5;
-        return most <= C::kUncut && (all <= gridDim.x || (even && all <= kUncutRounds * gridDim.x)) ? most + kCost : 0;
+        const long long count = static_cast<long long>(live) * units;
+        if (most > C::kUncut || count > kUncutRounds * gridDim.x) return 0;
+        const int all = static_cast<int>(count), grid = gridDim.x, each = most + kCost;
+        if (all > grid) {
+            rounds = static_cast<int>(static_cast<unsigned>(all + grid - 1) / static_cast<unsigned>(grid));
+            const int idle = (rounds == 2 ? 32 : 27) + min(kHeads, p.group) * D / 256;   // half tiles
+            if (each * live * 4 > (sum + kCost * live) * 5 || (rounds * grid - all) * each * 2 >= idle * grid) return 0;
+        }
+        return each;
     };
     long long total;
     if (small) {
@@ -538,8 +550,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, kDup, kQ8>::kCtasPerSm ==
     const int least = max(kW, static_cast<int>(sqrtf(mean * 0.5f)));
     long long ctas = min(static_cast<long long>(gridDim.x), (total + least - 1) / least), share = 0;
     if (pad) {   // whole units
-        share = (total / pad + gridDim.x - 1) / gridDim.x * pad;
-        ctas = share ? (total + share - 1) / share : 0;
+        share = static_cast<long long>(rounds) * pad;
+        ctas = (total + share - 1) / share;
     }
     if (blockIdx.x >= ctas) {
         zero_rows();

@@ -70,6 +70,23 @@ def test_prefill_of_the_smallest_queries(dev, down, cap):
     prefill(c, dev)
 
 
+# ------------------------------------------------------------------ short contexts
+
+@pytest.mark.parametrize("group,D,tiles", [(1, 64, 12), (4, 128, 8), (4, 256, 20), (8, 128, 12), (16, 64, 12),
+                                           (16, 128, 8)])
+@pytest.mark.parametrize("rounds", [1, 2, 3])
+def test_decode_of_short_contexts_around_full_rounds(dev, group, D, tiles, rounds):
+    """As many units as CTAs (two or three a processor), twice and three times as many, and a
+    sequence more or less: cut or whole, each context's rows are right."""
+    H, TK = 4, 4096 // D
+    ctas = processors(dev) * (3 if D <= 128 and group <= 8 else 2)
+    for S in (rounds * ctas // H, rounds * ctas // H + 1, rounds * ctas * 9 // 10 // H):
+        g = torch.Generator().manual_seed(S)
+        ctx = torch.randint(TK * tiles * 7 // 10, TK * tiles + 1, (S,), generator=g).tolist()
+        ctx[S // 3] = TK * tiles
+        decode(make_q8_case(231, ctx, [1] * S, H * group, H, D, 16, BF16), dev)
+
+
 # ------------------------------------------------------------------ the prefill's queue
 
 def items(c):
