@@ -713,9 +713,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, kDup, kQ8>::kCtasPerSm ==
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks)
                     raw[ks] = live ? src2[(hq * D + ks * 16) / 4 + (lane & 3)] : make_uint2(0u, 0u);
-                float up = 1.f;
+                const float k_scale = live ? a.k_scales[hk] : 0.f;
+                int ex = 0;                  // the lane's row is 2^ex times what it holds
                 if (p.io_bf16) {
-                    float top = 0.f, down;
+                    float top = 0.f;
 #pragma unroll
                     for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
@@ -725,7 +726,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, kDup, kQ8>::kCtasPerSm ==
                         }
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                    fp16_row_factors(top, down, up);
+                    ex = fp16_row_exponent(top);
+                    const float down = power_of_two(-ex);
 #pragma unroll
                     for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
@@ -738,7 +740,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, kDup, kQ8>::kCtasPerSm ==
 #pragma unroll
                     for (int ks = 0; ks < KS; ++ks) qf[ks][nt][0] = raw[ks].x, qf[ks][nt][1] = raw[ks].y;
                 }
-                const float f = product3(up, live ? a.k_scales[hk] : 0.f, a.softcap > 0.f ? p.cap_v : p.scale_log2);
+                const float f = score_factor(k_scale, a.softcap > 0.f ? p.cap_v : p.scale_log2, ex);
                 // the factors of the lane's two columns, from the lanes that hold these heads
                 qs[nt][0] = __shfl_sync(0xffffffffu, f, 4 * col);
                 qs[nt][1] = __shfl_sync(0xffffffffu, f, 4 * col + 4);

@@ -55,22 +55,20 @@ __device__ __forceinline__ uint32_t quantise_pair(uint64_t x, uint64_t minus, ui
     return f32x2_to_e4m3x2(a1, b1);
 }
 
-// A bf16 query row is made fp16 by a power of two that brings its largest element, `top`,
-// to [2^10, 2^11): bf16's exponents do not fit, its 8 bits do.  The exponent of that power
-// ends at 126, where fp32 ends; nothing is lost there: bf16 numbers are multiples of
-// 2^-133, so those of a row below 2^-116 become multiples of 2^-7 below 2^10, which fp16
-// holds.  `up` undoes `down`.
-__device__ __forceinline__ void fp16_row_factors(float top, float &down, float &up) {
-    const int e = max(static_cast<int>(__float_as_uint(top) >> 23) - 137, -126);
-    down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-    up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+// A bf16 query row is made fp16 by a power of two, 2^-e, that brings its largest element,
+// `top`, to [2^10, 2^11): bf16's exponents do not fit, its 8 bits do.  e ends at -126,
+// where fp32 does; nothing is lost there: bf16 numbers are multiples of 2^-133, so those
+// of a row below 2^-116 become multiples of 2^-7 below 2^10, which fp16 holds.
+__device__ __forceinline__ int fp16_row_exponent(float top) {
+    return max(static_cast<int>(__float_as_uint(top) >> 23) - 137, -126);
 }
-// up * a * b (up a power of two) in an order in which no partial product is further out
-// of fp32's range than the whole.
-__device__ __forceinline__ float product3(float up, float a, float b) {
-    const bool a_far = fabsf(a) > fabsf(b);
-    const float far = a_far ? a : b, near = a_far ? b : a;
-    return up < 1.f ? up * far * near : up * near * far;
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+// a (a scale of a head) times b (of the softmax) times 2^e, each with one half of the
+// power, so that neither leaves fp32's range where the whole is within 2^+-90 (scales of
+// heads are within 2^+-60, scale and scale / cap within 2^+-100, rows within 2^+-128).
+__device__ __forceinline__ float score_factor(float a, float b, int e) {
+    const int half = e >> 1;
+    return (a * power_of_two(half)) * (b * power_of_two(e - half));
 }
 
 // What a score's v (fill_tanh) is multiplied by for 2^(..) = e^(2 s / cap).

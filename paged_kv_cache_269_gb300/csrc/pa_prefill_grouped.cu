@@ -842,11 +842,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             pending = -1;
         };
         // Item k's Q, where it has to be made fp16, each row by a power of two of its own
-        // (fp16_row_factors).  A thread takes its own row: while the item before waits for its last
+        // (fp16_row_exponent).  A thread takes its own row: while the item before waits for its last
         // product, if Q is there by then, and else after that item's output (waiting for it
-        // first cost 16 prompts of 333 to 1024 tokens 114 us instead of 108).  q_factor: what
-        // the row's scores are short of.
-        float q_factor = 1.f;
+        // first cost 16 prompts of 333 to 1024 tokens 114 us instead of 108).  The row is
+        // 2^q_exponent times what its buffer holds.
+        int q_exponent = 0;
         int q_ready = -1;          // the last item whose Q is ready
         auto ready_q = [&](int k) {
             const int slot = k % 2;
@@ -871,8 +871,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         most = __hmax2(most, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&u[z])));
                 }
                 const float top = fmaxf(__low2float(most), __high2float(most));
-                float down;
-                fp16_row_factors(top, down, q_factor);
+                q_exponent = fp16_row_exponent(top);
+                const float down = power_of_two(-q_exponent);
 #pragma unroll
                 for (int i = 0; i < D / 8; ++i) {
                     uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
@@ -930,10 +930,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int pre_all = it->pre, na = it->na, skip = it->skip, j0 = it->j0;
             const int last = j0 + max(nk, 0) - 1;
             if constexpr (kQ8) {
-                const float f = __ldg(a.k_scales + it->hk), up = kScaleQ ? q_factor : 1.f;
-                c = product3(up, f, p.scale_log2);
+                const float f = __ldg(a.k_scales + it->hk);
+                const int e = kScaleQ ? q_exponent : 0;
+                c = score_factor(f, p.scale_log2, e);
                 if constexpr (kCap) {
-                    cap_v = product3(up, f, p.cap_v);
+                    cap_v = score_factor(f, p.cap_v, e);
                     cap_in = kCapInPerV * cap_v;
                     cap_v2 = keep_pair(cap_v);
                 }
