@@ -132,43 +132,62 @@ struct Append {
     const int32_t *positions, *slots;
     const float *table;
 };
-// q8: the caches are e4m3.
-bool append(Args &g, bool q8, Append *x) {
+// q8: the caches are e4m3.  optional: q with q_out may be None (k and v alone), and so
+// may cos_sin (no rotation), with positions or without.
+bool append(Args &g, bool q8, bool optional, Append *x) {
     at::ScalarType type;
-    const Tensor *q = g.tensor(1);
-    if (!q || q->dim() != 3 || !caches(g, 4, &x->d, &type, q8 ? q : nullptr)) return false;
-    const int64_t T = q->size(0), Hq = q->size(1), H = x->d.num_heads, D = x->d.head_dim;
-    q = rows(g, 1, type, T, Hq, D, &x->qs);
-    const Tensor *o = g.ok ? rows(g, 0, type, T, Hq, D, &x->os) : nullptr;
-    const Tensor *k = g.ok ? rows(g, 2, type, T, H, D, &x->ks) : nullptr;
+    const bool has_q = !optional || g.a[0] != Py_None || g.a[1] != Py_None;
+    const bool turns = !optional || g.a[7] != Py_None, placed = turns || g.a[6] != Py_None;
+    const Tensor *k = g.tensor(2);
+    if (!k || k->dim() != 3 || !caches(g, 4, &x->d, &type, q8 ? k : nullptr)) return false;
+    const int64_t T = k->size(0), H = x->d.num_heads, D = x->d.head_dim;
+    k = rows(g, 2, type, T, H, D, &x->ks);
     const Tensor *v = g.ok ? rows(g, 3, type, T, H, D, &x->vs) : nullptr;
-    const Tensor *pos = g.ok ? g.plain(6, at::kInt, 1) : nullptr;
-    const Tensor *cs = g.ok ? g.plain(7, at::kFloat, 2) : nullptr;
     const Tensor *slots = g.ok ? g.plain(8, at::kInt, 1) : nullptr;
-    if (!g.ok || T <= 0 || T > 0x7fffffff || Hq <= 0 || Hq > 0x7fffffff || pos->size(0) != T ||
-        slots->size(0) != T || cs->size(0) > 0x7fffffff || cs->size(1) > 0x7fffffff || cs->size(1) <= 0 ||
-        (T > 1 && x->os < Hq * D))
-        return false;
-    const bool in_place = o->data_ptr() == q->data_ptr() && (x->os == x->qs || T == 1);
-    if ((!in_place && overlap(o, x->os, Hq * D, q, x->qs, Hq * D, T)) ||
-        overlap(o, x->os, Hq * D, k, x->ks, H * D, T) || overlap(o, x->os, Hq * D, v, x->vs, H * D, T))
-        return false;
+    if (!g.ok || T <= 0 || T > 0x7fffffff || slots->size(0) != T) return false;
+    x->Hq = 0;
+    x->qs = x->os = 0;
+    x->out = nullptr;
+    x->q = nullptr;
+    if (has_q) {
+        const Tensor *q = g.tensor(1);
+        if (!q || q->dim() != 3) return false;
+        const int64_t Hq = q->size(1);
+        q = rows(g, 1, type, T, Hq, D, &x->qs);
+        const Tensor *o = g.ok ? rows(g, 0, type, T, Hq, D, &x->os) : nullptr;
+        if (!o || Hq <= 0 || Hq > 0x7fffffff || (T > 1 && x->os < Hq * D)) return false;
+        const bool in_place = o->data_ptr() == q->data_ptr() && (x->os == x->qs || T == 1);
+        if ((!in_place && overlap(o, x->os, Hq * D, q, x->qs, Hq * D, T)) ||
+            overlap(o, x->os, Hq * D, k, x->ks, H * D, T) || overlap(o, x->os, Hq * D, v, x->vs, H * D, T))
+            return false;
+        x->Hq = static_cast<int32_t>(Hq);
+        x->out = o->data_ptr();
+        x->q = q->data_ptr();
+    }
+    x->rotary = x->most = 0;
+    x->table = nullptr;
+    if (turns) {
+        const Tensor *cs = g.plain(7, at::kFloat, 2);
+        if (!cs || cs->size(0) > 0x7fffffff || cs->size(1) > 0x7fffffff || cs->size(1) <= 0) return false;
+        x->rotary = static_cast<int32_t>(cs->size(1));
+        x->most = static_cast<int32_t>(cs->size(0));
+        x->table = static_cast<const float *>(cs->data_ptr());
+    }
+    x->positions = nullptr;
+    if (placed) {
+        const Tensor *pos = g.plain(6, at::kInt, 1);
+        if (!pos || pos->size(0) != T) return false;
+        x->positions = static_cast<const int32_t *>(pos->data_ptr());
+    }
     x->turn = PyObject_IsTrue(g.a[9]);
     x->stream = pointer(g.a[11]);
     if (PyErr_Occurred() || x->turn < 0) return false;
     x->T = static_cast<int32_t>(T);
-    x->Hq = static_cast<int32_t>(Hq);
-    x->rotary = static_cast<int32_t>(cs->size(1));
-    x->most = static_cast<int32_t>(cs->size(0));
-    x->out = o->data_ptr();
     x->k_cache = g.pointer(4);
     x->v_cache = g.pointer(5);
-    x->q = q->data_ptr();
     x->k = k->data_ptr();
     x->v = v->data_ptr();
-    x->positions = static_cast<const int32_t *>(pos->data_ptr());
     x->slots = static_cast<const int32_t *>(slots->data_ptr());
-    x->table = static_cast<const float *>(cs->data_ptr());
     return true;
 }
 
@@ -177,7 +196,7 @@ PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (n != 13) return take_over();
     Args g{a, static_cast<int>(integer(a[10]))};
     Append x;
-    if (!append(g, false, &x)) return take_over();
+    if (!append(g, false, false, &x)) return take_over();
     auto fn = reinterpret_cast<decltype(&pa_rope_and_cache)>(pointer(a[12]));
     if (PyErr_Occurred() || !fn) return take_over();
     int rc;
@@ -194,7 +213,7 @@ PyObject *norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
     Args g{a, static_cast<int>(integer(a[10]))};
     const bool q8 = a[15] != Py_None || a[16] != Py_None;
     Append x;
-    if (!append(g, q8, &x)) return take_over();
+    if (!append(g, q8, true, &x)) return take_over();
     pa_append_opts o{};
     const float **weights[2] = {&o.q_weight, &o.k_weight};
     for (int i = 0; i < 2; ++i) {

@@ -73,7 +73,7 @@ def norm_rope_and_cache(q_out, q, k, v, k_cache, v_cache, positions, cos_sin, sl
     The rest as rope_and_cache, except that cos_sin may be None (no rotation;
     positions too, if no token is padding) and q with q_out (k and v alone)."""
     pa = _g._pa()
-    if _g._marshal is not None and q is not None and cos_sin is not None:
+    if _g._marshal is not None:
         device = _g._get_device()
         rc = _g._marshal.norm_rope(q_out, q, k, v, k_cache, v_cache, positions, cos_sin, slot_mapping, interleaved,
                                    device, _g._raw_stream(device) if stream is None else stream.cuda_stream,

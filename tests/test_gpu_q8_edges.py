@@ -8,6 +8,7 @@ import torch
 import paged_kv_cache_269_gb300 as pa
 import test_gpu_grouped
 from grouped_ref import make_case
+from paged_kv_cache_269_gb300 import grouped
 from q8_ref import E4M3, make_q8_case, refresh, scales_for
 from test_gpu_q8 import check, decode, prefill, run_prefill, to_dev
 
@@ -68,6 +69,76 @@ def test_prefill_of_the_smallest_queries(dev, down, cap):
     c.q[7] = 0.0
     c.q[11, 2, 5] = 2.0 ** (7 - down)
     prefill(c, dev)
+
+
+# ------------------------------------------------------------------ appends without q or a rotation
+
+class Watched:
+    """The marshalling module, with what its append returned."""
+
+    def __init__(self, module):
+        self.module, self.seen = module, []
+
+    def norm_rope(self, *args):
+        self.seen.append(self.module.norm_rope(*args))
+        return self.seen[-1]
+
+
+@pytest.mark.parametrize("q8", [True, False])
+@pytest.mark.parametrize("T", [1, 45])
+@pytest.mark.parametrize("with_q,turn,placed", [(False, False, False), (False, False, True), (False, True, True),
+                                                (True, False, False), (True, False, True), (True, True, True)])
+def test_append_without_q_or_rotation_is_marshalled(dev, monkeypatch, q8, T, with_q, turn, placed):
+    """These forms go through the compiled marshalling too, and do what they do through the
+    Python checks, bit for bit."""
+    H, D, B, N = 2, 64, 16, 5
+    g = torch.Generator().manual_seed(T)
+    x = torch.randn(T, 3 + 2 * H, D, generator=g).to(BF16).to(dev)
+    pos = torch.randint(-1, 50, (T,), generator=g).to(torch.int32).to(dev) if placed else None
+    table = pa.rope_table(50, 32, device=dev) if turn else None
+    slots = torch.randperm(N * B, generator=g)[:T].to(torch.int32).to(dev)
+    w = (1.0 + 0.1 * torch.randn(D, generator=g)).to(dev)
+    s = scales_for(1, H).to(dev) if q8 else None
+    pa.device_errors()
+    grouped._pa()
+    watched, got = Watched(grouped._marshal), []
+    for module in (watched, None):
+        monkeypatch.setattr(grouped, "_marshal", module)
+        out = torch.full((T, 3, D), 7.0, dtype=BF16, device=dev) if with_q else None
+        kc, vc = (torch.zeros(N, H, B, D, dtype=BYTE if q8 else BF16, device=dev) for _ in range(2))
+        a, b = (c.view(E4M3) if q8 else c for c in (kc, vc))
+        r = pa.norm_rope_and_cache(out, x[:, :3] if with_q else None, x[:, 3:3 + H], x[:, 3 + H:], a, b, pos, table, slots,
+                                   w if with_q else None, w, 1e-5, True, s, s)
+        assert r is out and pa.device_errors() == 0
+        got.append((kc.view(BYTE), vc.view(BYTE)) + (() if out is None else (out.view(BYTE),)))
+    assert watched.seen == [0]
+    assert all(torch.equal(m, p) for m, p in zip(*got)) and got[0][0].any()
+
+
+def test_append_without_q_or_rotation_refuses(dev):
+    H, D = 2, 64
+    x = torch.zeros(4, 2 * H + 3, D, dtype=F16, device=dev)
+    kc, vc = (torch.zeros(3, H, 16, D, dtype=BYTE, device=dev).view(E4M3) for _ in range(2))
+    s, slots = torch.ones(H, device=dev), torch.arange(4, dtype=torch.int32, device=dev)
+    table = pa.rope_table(9, D, device=dev)
+    base = dict(q_out=None, q=None, k=x[:, :H], v=x[:, H:2 * H], k_cache=kc, v_cache=vc, positions=None, cos_sin=None,
+                slot_mapping=slots, k_scales=s, v_scales=s)
+    for kind, kw in ((ValueError, dict(q=x[:, 2 * H:])), (ValueError, dict(q_out=x[:, 2 * H:])),
+                     (ValueError, dict(cos_sin=table)), (ValueError, dict(positions=slots[:3])),
+                     (TypeError, dict(positions=slots.long())), (TypeError, dict(cos_sin=table.double(), positions=slots)),
+                     (ValueError, dict(cos_sin=table[:, :0], positions=slots)), (TypeError, dict(k=None)),
+                     (ValueError, dict(v=x[:3, :H])), (TypeError, dict(slot_mapping=None)), (TypeError, dict(v_scales=None))):
+        with pytest.raises(kind):
+            pa.norm_rope_and_cache(**{**base, **kw})
+    for name in ("q", "k", "v"):                      # the rotary append takes none of them away
+        full = dict(q_out=x[:, 4:].clone(), q=x[:, 4:], k=x[:, :H], v=x[:, H:2 * H])
+        c16 = torch.zeros(3, H, 16, D, dtype=F16, device=dev)
+        with pytest.raises(TypeError):
+            pa.rope_and_cache(**{**full, name: None}, k_cache=c16, v_cache=c16.clone(), positions=slots, cos_sin=table,
+                              slot_mapping=slots)
+    with pytest.raises(TypeError):
+        pa.rope_and_cache(x[:, 4:].clone(), x[:, 4:], x[:, :H], x[:, H:2 * H], c16, c16.clone(), slots, None, slots)
+    assert pa.norm_rope_and_cache(**base) is None and pa.device_errors() == 0
 
 
 # ------------------------------------------------------------------ short contexts
