@@ -42,7 +42,7 @@
 //  * Keys that are not visible get weight 0 and their V values are cleared in
 //    registers, so nothing they hold reaches the output.
 //
-// Shape: 4 warps a CTA and 2 CTAs an SM, as many as 181 to 251 registers a thread
+// Shape: 4 warps a CTA and 2 CTAs an SM, as many as 187 to 254 registers a thread
 // leave, with as many stages a warp as shared memory holds.  A third stage at
 // head_dim 128 (in exchange for a smaller merge area) cost 4 % (59.5 us against
 // 57.1 on the first batch below), at 256 nothing changed.  Work cut into small
@@ -75,8 +75,9 @@
 // tiles each); 6 sequences of 20001 to 32768 tokens, 16 heads on 8 of 256, capped, 663 MB:
 // 107 us, 6.2 TB/s, 0.93 of the rate of a copy. From L2, where only the work counts, 8 KB
 // take a processor 143 ns (8 heads a K/V head 222, head_dim 64 221, head_dim 256 180);
-// HBM brings them in 186.  Short contexts are taken whole (whole_units): 50 sequences of 67 to
-// 100 tokens, 8 K/V heads, 9.2 us, cut 15.3.
+// HBM brings them in 186.  (At 5 to 8 heads of 128 a lane spills 40 bytes for the third CTA.)
+// Short contexts are taken whole (whole_units): 50 sequences of 67 to 100 tokens, 8 K/V heads,
+// 9.2 us, cut 15.3.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>

@@ -84,7 +84,7 @@
 // K and V blocks arrive by untiled copies in the upper half of their tile's slot, and warps
 // 14 and 15 widen each tile where it lies (widen_tile), so the ring has as many tiles as
 // that of 16 bits and the products see no difference. A key tile of 64 x 128 costs its warp
-// 256 conversions a lane; with bf16 operands, three instructions more for each pair, the
+// 128 conversions of pairs a lane; with bf16 operands, three instructions more for each pair, the
 // two warps set the pace (chunks of 512 tokens over 4097 to 8192 keys, 32 heads on 8: 313
 // us, and 174 so; a 16-bit cache 152). A bf16 Q is made fp16 by its softmax threads, row by
 // row with a scale of its own, while the item before waits for its last product.

@@ -147,11 +147,11 @@ def test_append_without_q_or_rotation_refuses(dev):
                                            (16, 128, 8)])
 @pytest.mark.parametrize("rounds", [1, 2, 3])
 def test_decode_of_short_contexts_around_full_rounds(dev, group, D, tiles, rounds):
-    """As many units as CTAs (two or three a processor), twice and three times as many, and a
-    sequence more or less: cut or whole, each context's rows are right."""
+    """As many units as CTAs (two or three a processor) and a sequence more, twice and three
+    times as many, and less than a round: cut or whole, each context's rows are right."""
     H, TK = 4, 4096 // D
-    ctas = processors(dev) * (3 if D <= 128 and group <= 8 else 2)
-    for S in (rounds * ctas // H, rounds * ctas // H + 1, rounds * ctas * 9 // 10 // H):
+    full = rounds * processors(dev) * (3 if D <= 128 and group <= 8 else 2) // H
+    for S in (full, full * 9 // 10) if rounds == 2 else (full + 1,):
         g = torch.Generator().manual_seed(S)
         ctx = torch.randint(TK * tiles * 7 // 10, TK * tiles + 1, (S,), generator=g).tolist()
         ctx[S // 3] = TK * tiles
